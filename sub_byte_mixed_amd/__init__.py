@@ -17,6 +17,9 @@ the C entry points (include/snip.h):
   layer_stats(stats)                       -> list of per-tensor reports
   timing_start(capacity), timing_read()    -> per-launch kernel times
 
+and those of include/snip_ops.h, the operators around the linear layers
+(ops.py): rmsnorm_fwd, rmsnorm_bwd, swiglu_fwd, swiglu_bwd, qgemv.
+
 The library is built in-tree by `python -m sub_byte_mixed_amd.build`. If it is
 missing, importing works but every call raises: there is no CPU fallback.
 """
@@ -77,7 +80,7 @@ class LaunchRecord(ctypes.Structure):
                 ("work", ctypes.c_double), ("ms", ctypes.c_double)]
 
 
-LAUNCH_KINDS = {0: "amax", 1: "quantize", 2: "gemm", 3: "splitk", 4: "finalize"}
+LAUNCH_KINDS = {0: "amax", 1: "quantize", 2: "gemm", 3: "splitk", 4: "finalize", 5: "norm", 6: "gate", 7: "gemv"}
 
 STATS_BYTES = 24     # sizeof(snip_stats)
 
@@ -143,7 +146,7 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m sub_byte_mixed_amd.build`")
         h = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in _SIGS.items():
+        for name, (res, args) in {**_SIGS, **ops.SIGS}.items():
             f = getattr(h, name)
             f.restype = res
             f.argtypes = args
@@ -519,3 +522,7 @@ def timing_read() -> Tuple[List[dict], int]:
     recs = [{"kind": LAUNCH_KINDS.get(r.kind, str(r.kind)), "format": r.format, "layout": r.layout,
              "rounding": r.rounding, "work": r.work, "ms": r.ms} for r in buf[:n]]
     return recs, int(untimed.value)
+
+
+from . import ops  # noqa: E402  (uses the definitions above)
+from .ops import qgemv, rmsnorm_bwd, rmsnorm_fwd, swiglu_bwd, swiglu_fwd  # noqa: E402,F401

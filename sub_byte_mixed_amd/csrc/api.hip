@@ -8,14 +8,13 @@
 // stochastic rounding for back-propagation and update operands).
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
 #include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
 
+#include "api_common.h"
 #include "kernels.h"
 
 using namespace snip;
@@ -58,50 +57,6 @@ void timing_end(int slot, hipStream_t s) {
 
 namespace {
 
-thread_local std::string g_err;
-
-int fail(int code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  std::vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_err = buf;
-  return code;
-}
-
-int ok() {
-  g_err.clear();
-  return SNIP_OK;
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-constexpr size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-// Formats a qtensor may hold (the FP4 design-space variants included) and
-// the formats the GEMM and layer calls take.
-bool valid_format(int f) { return f >= SNIP_BF16 && f <= SNIP_FP4_BF16_B32; }
-bool gemm_format(int f) { return f >= SNIP_BF16 && f <= SNIP_MXFP4; }
-bool fp4_variant(int f) { return f >= SNIP_FP4_E4M3_B32 && f <= SNIP_FP4_BF16_B32; }
-int block_of(int f) {
-  return (f == SNIP_MXFP4 || f == SNIP_FP4_E4M3_B32 || f == SNIP_FP4_BF16_B32) ? 32 : 16;
-}
-bool has_scales(int f) { return f == SNIP_NVFP4 || f == SNIP_MXFP4 || fp4_variant(f); }
-bool has_texp(int f) { return f == SNIP_NVFP4 || f == SNIP_FP8_E4M3 || f == SNIP_FP4_E4M3_B32; }
-bool needs_amax(int f) { return has_texp(f); }
-
-int64_t code_bytes(int f, int64_t rows, int64_t k) {
-  if (f == SNIP_NVFP4 || f == SNIP_MXFP4 || fp4_variant(f)) return rows * k / 2;
-  if (f == SNIP_FP8_E4M3) return rows * k;
-  if (f == SNIP_BF16) return rows * k * 2;
-  return -1;
-}
-int64_t scale_bytes(int f, int64_t rows, int64_t k) {
-  if (!has_scales(f)) return 0;
-  const int per = (f == SNIP_FP4_BF16_B16 || f == SNIP_FP4_BF16_B32) ? 2 : 1;
-  return rows * (k / block_of(f)) * per;
-}
-
 // The LDS-DMA GEMM kernels address an operand's rows with 32-bit byte
 // offsets, so the codes of every GEMM operand (A[M][K] and B[N][K]; their
 // block scales are smaller) must stay below 4 GiB. Checked before any HIP
@@ -117,7 +72,6 @@ int gemm_operands_fit(int f, int64_t M, int64_t N, int64_t K, const char* who) {
   return 0;
 }
 
-constexpr size_t kAlign = 256;
 constexpr size_t kAmaxBytes = align_up(kAmaxWG * sizeof(uint32_t), kAlign);
 constexpr size_t kPartBytes = align_up(kQuantWG * sizeof(StatPart), kAlign);
 // scratch of one quantize pass: amax partials + statistics partials
@@ -127,18 +81,6 @@ size_t qtensor_ws_bytes(int f, int64_t rows, int64_t k) {
   return align_up((size_t)code_bytes(f, rows, k), kAlign) +
          align_up((size_t)scale_bytes(f, rows, k), kAlign) + kAlign;
 }
-
-// Bump allocator over the caller's workspace.
-struct Carver {
-  uint8_t* base;
-  size_t used = 0;
-  explicit Carver(void* p) : base(static_cast<uint8_t*>(p)) {}
-  uint8_t* take(size_t n) {
-    uint8_t* p = base + used;
-    used += align_up(n, kAlign);
-    return p;
-  }
-};
 
 // Grid sizes.
 int amax_wg(int64_t rows, int64_t cols) {
@@ -160,16 +102,6 @@ int quant_wg(int layout, int f, int64_t rows, int64_t cols) {
   }
   if (wg < 1) wg = 1;
   return (int)(wg > kQuantWG ? kQuantWG : wg);
-}
-
-hipError_t g_last_hip = hipSuccess;
-
-int hip_check(hipError_t e, const char* what) {
-  if (e != hipSuccess) {
-    g_last_hip = e;
-    return fail(SNIP_E_HIP, "%s: %s", what, hipGetErrorString(e));
-  }
-  return SNIP_OK;
 }
 
 // One planned quantize pass (used by snip_quantize and the linear layer).
@@ -380,27 +312,12 @@ int dual_wg(int f, int64_t rows, int64_t cols) {
   return (int)(wg < 1 ? 1 : wg > kQuantWG ? kQuantWG : wg);
 }
 
-int validate_qtensor(const snip_qtensor* q, const char* name, bool need_codes = true) {
-  if (!q) return fail(SNIP_E_NULL, "%s: descriptor is NULL", name);
-  if (!valid_format(q->format)) return fail(SNIP_E_FORMAT, "%s: unknown format %d", name, q->format);
-  if (q->rows <= 0 || q->k <= 0) return fail(SNIP_E_SHAPE, "%s: rows=%lld k=%lld must be > 0", name,
-                                           (long long)q->rows, (long long)q->k);
-  if (q->k % block_of(q->format)) return fail(SNIP_E_SHAPE, "%s: k=%lld not a multiple of %d", name,
-                                             (long long)q->k, block_of(q->format));
-  if (need_codes && !q->codes) return fail(SNIP_E_NULL, "%s: codes is NULL", name);
-  if (has_scales(q->format) && !q->scales) return fail(SNIP_E_NULL, "%s: scales is NULL", name);
-  if (has_texp(q->format) && !q->tensor_exp) return fail(SNIP_E_NULL, "%s: tensor_exp is NULL", name);
-  if (!aligned(q->codes, 16) || !aligned(q->scales, 16) || !aligned(q->tensor_exp, 4))
-    return fail(SNIP_E_ALIGN, "%s: device pointers must be 16-byte aligned", name);
-  return SNIP_OK;
-}
-
 }  // namespace
 
 // ====================================================================== API
 extern "C" {
 
-const char* snip_last_error(void) { return g_err.c_str(); }
+const char* snip_last_error(void) { return last_error().c_str(); }
 
 int snip_version(void) { return 100; }
 

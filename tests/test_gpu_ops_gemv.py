@@ -1,0 +1,140 @@
+"""snipop_qgemv against the float64 product of the values that the stored
+bytes stand for, within the library's bar for GEMM outputs: 1e-5 of
+sum |a||b| (168 roundings of fp32 in a row; a lane sums at most K / 16
+products before the 64 lanes and 4 waves join), plus half a step of bf16
+where y is bf16."""
+import numpy as np
+import pytest
+import torch
+
+import sub_byte_mixed_amd as S
+from oracle import ops as OO
+from ops_common import BF, F32, HALF, f64, rand, say
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = [S.FP8, S.NVFP4, S.MXFP4, S.FP4_E4M3_B32, S.FP4_E8M0_B16, S.FP4_BF16_B16, S.FP4_BF16_B32]
+
+
+def raw_weights(fmt, n, k, seed):
+    """Every code, and scales over their range, at random: the bytes of an
+    operand as they may come, not only as the quantizer makes them."""
+    g = np.random.default_rng(seed)
+    w = S.QuantizedTensor(fmt, n, k, "cuda")
+    codes = g.integers(0, 256, w.codes.numel(), dtype=np.uint8)
+    if fmt == S.FP8:
+        codes[(codes & 0x7F) == 0x7F] = 0x7E                          # no NaN
+    w.codes.copy_(torch.from_numpy(codes))
+    if w.scales is not None:
+        kind = S.FP4_LAYOUT[fmt][1]
+        m = w.scales.numel()
+        if kind == "e4m3":
+            sc = g.integers(0, 0x7F, m, dtype=np.uint8)               # zero and subnormal ones too
+        elif kind == "e8m0":
+            sc = g.integers(110, 140, m, dtype=np.uint8)
+        else:
+            sc = (2.0 ** g.uniform(-12, 12, m // 2)).astype(np.float32).view(np.uint32) >> 16
+            sc = sc.astype(np.uint16).view(np.uint8)
+        w.scales.copy_(torch.from_numpy(sc))
+    w.texp.fill_(-7)
+    return w
+
+
+def values(w):
+    return OO.dequantize(w.format, w.codes.cpu().numpy(), None if w.scales is None else w.scales.cpu().numpy(),
+                         int(w.texp.cpu()), w.rows, w.k)
+
+
+def check(x, w, y):
+    a, b = f64(x), values(w)
+    want, size = a @ b.T, np.abs(a) @ np.abs(b).T
+    tol = 1e-5 * size + HALF[y.dtype] * np.abs(want)
+    bad = ~(np.abs(f64(y) - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), f64(y)[bad][:4], want[bad][:4])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n,k", [(1, 32), (5, 64), (17, 96), (256, 2048), (33, 2080), (100, 5632), (16, 8192), (7, 11008)])
+def test_formats_and_sizes(fmt, n, k):
+    w = raw_weights(fmt, n, k, 7 * n + k)
+    for m in (1, 2, 3, 4, 5, 8, 9, 16):
+        say("qgemv", fmt, n, k, m)
+        x = rand((m, k), BF, m).cuda()
+        y = S.qgemv(x, w)
+        check(x, w, y)
+        assert torch.equal(y, S.qgemv(x, w))                          # the same bits again
+        assert torch.equal(S.qgemv(x, w, y_dtype=BF), y.to(BF))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_quantizer_output_as_weights(fmt):
+    wt = rand((384, 1024), BF, 1, 0.02)
+    w, _ = S.quantize(wt.cuda(), S.ROWWISE, fmt)
+    x = rand((3, 1024), BF, 2).cuda()
+    check(x, w, S.qgemv(x, w))
+
+
+@pytest.mark.parametrize("m", [1, 3, 7, 16])
+def test_strides(m):
+    n, k = 70, 320
+    w = raw_weights(S.NVFP4, n, k, 3)
+    buf = torch.full((m, k + 64), 3.0e38, dtype=BF, device="cuda")
+    buf[:, 8:8 + k] = rand((m, k), BF, 4).cuda()
+    x = buf[:, 8:8 + k]
+    out = torch.full((m + 2, n + 13), 9.0, dtype=F32, device="cuda")
+    flat = out.view(-1)[:(m + 1) * (n + 13)]
+    y = flat[:m * (n + 13)].view(m, n + 13)[:, :n]                    # odd row stride
+    S.qgemv(x, w, y=y)
+    check(x, w, y)
+    assert torch.equal(y, S.qgemv(x.contiguous(), w))
+    rest = out.clone()
+    rest.view(-1)[:m * (n + 13)].view(m, n + 13)[:, :n] = 9.0
+    assert (rest == 9.0).all()
+
+
+def test_tokens_do_not_mix():
+    """A token's result does not depend on the other tokens' values."""
+    w = raw_weights(S.MXFP4, 64, 512, 5)
+    for m in (2, 4, 11, 16):
+        x = rand((m, 512), BF, 6).cuda()
+        y = S.qgemv(x, w)
+        x2 = x.clone()
+        x2[: m - 1] = float("nan")
+        y2 = S.qgemv(x2, w)
+        assert torch.equal(y2[m - 1], y[m - 1]) and torch.isnan(y2[: m - 1]).all()
+
+
+def test_nonfinite_activations():
+    w, _ = S.quantize(torch.ones((48, 128), dtype=BF, device="cuda"), S.ROWWISE, S.NVFP4)
+    x = torch.ones((2, 128), dtype=BF, device="cuda")
+    x[0, 17] = float("inf")
+    x[1, 100] = float("nan")
+    y = S.qgemv(x, w)
+    assert torch.isinf(y[0]).all() and torch.isnan(y[1]).all()
+
+
+def test_small_and_large_values():
+    """bf16 activations over their exponents against weights of 1: no flush
+    of small products next to nothing else, no early overflow."""
+    w, _ = S.quantize(torch.ones((32, 64), dtype=BF, device="cuda"), S.ROWWISE, S.MXFP4)
+    for e in (-100, -60, 0, 60, 100):
+        for m in (1, 4, 16):
+            x = torch.zeros((m, 64), dtype=BF, device="cuda")
+            x[m - 1, 5] = 1.5 * 2.0 ** e
+            y = S.qgemv(x, w)
+            want = 1.5 * 2.0 ** e
+            assert torch.allclose(y[m - 1].double(), torch.full((32,), want, dtype=torch.float64, device="cuda"), rtol=1e-5)
+
+
+def test_refusals_in_the_binding():
+    w = raw_weights(S.NVFP4, 8, 64, 8)
+    x = rand((1, 64), BF, 9).cuda()
+    with pytest.raises(ValueError):
+        S.qgemv(x.float(), w)
+    with pytest.raises(ValueError):
+        S.qgemv(rand((1, 96), BF, 9).cuda(), w)
+    with pytest.raises(ValueError):
+        S.qgemv(x, w, y=torch.empty((1, 9), device="cuda"))
+    with pytest.raises(S.SnipError) as e:
+        S.qgemv(rand((17, 64), BF, 9).cuda(), w)
+    assert e.value.code == -2
