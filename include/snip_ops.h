@@ -126,7 +126,8 @@ int snipop_swiglu_bwd(const void* dy, int dy_type, int64_t lddy, const void* gat
  * step's linear layer, with the activations left in bf16.
  *   x          device bf16, ldx; 1 <= tokens <= SNIPOP_QGEMV_MAX_TOKENS.
  *   w          host descriptor: N = w->rows, K = w->k; any format but BF16
- *              (FP8_E4M3, NVFP4, MXFP4 and the FP4 variants); K % 32 == 0.
+ *              (FP8_E4M3, NVFP4, MXFP4 and the FP4 variants); K % 32 == 0;
+ *              N <= 2^31, K and ldx <= 2^25.
  *   y          device, y_type, ldy >= N.
  * Products are exact and sums are fp32 in a fixed order that depends on the
  * shapes alone. No workspace.

@@ -282,10 +282,12 @@ int snipop_qgemv(const void* x, int64_t ldx, int64_t tokens, const snip_qtensor*
   if (tokens < 1 || tokens > SNIPOP_QGEMV_MAX_TOKENS)
     return fail(SNIP_E_SHAPE, "%s: %lld tokens outside 1 .. %d", who, (long long)tokens, SNIPOP_QGEMV_MAX_TOKENS);
   if (w->k % 32) return fail(SNIP_E_SHAPE, "%s: K=%lld not a multiple of 32", who, (long long)w->k);
-  if (w->rows > (int64_t)1 << 31 || w->k > (int64_t)1 << 31)
-    return fail(SNIP_E_SHAPE, "%s: N=%lld, K=%lld above 2^31", who, (long long)w->rows, (long long)w->k);
+  constexpr int64_t kMaxK = (int64_t)1 << 25;           // 16 rows of codes or tokens within 32-bit offsets
+  if (w->rows > (int64_t)1 << 31 || w->k > kMaxK || ldx > kMaxK)
+    return fail(SNIP_E_SHAPE, "%s: N=%lld above 2^31, or K=%lld or ldx=%lld above 2^25", who, (long long)w->rows,
+                (long long)w->k, (long long)ldx);
   if ((rc = check_type(who, "y", y_type))) return rc;
-  if (ldx < w->k || ldx > kMaxDim || ldx % 8)
+  if (ldx < w->k || ldx % 8)
     return fail(SNIP_E_SHAPE, "%s: ldx=%lld must be >= K=%lld and a multiple of 8", who, (long long)ldx,
                 (long long)w->k);
   if (ldy < w->rows || ldy > kMaxDim) return fail(SNIP_E_SHAPE, "%s: ldy=%lld must be >= N=%lld", who, (long long)ldy,

@@ -9,29 +9,9 @@
 // chunks of 8 elements (chunk t + v TPR, so that a wave's accesses are
 // contiguous): with 64 the reduction needs no LDS and a workgroup holds four
 // rows, with more it crosses the waves through LDS once per row.
-#include <type_traits>
-
 #include "row_common.h"
 
 namespace snip {
-
-// Sum over the wave, in every lane: four steps within rows of 16 lanes, then
-// the four row sums.
-__device__ __forceinline__ float wave_sum_f(float v) {
-  auto step = [](float x, auto ctrl) {
-    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, true));
-  };
-  v = step(v, std::integral_constant<int, 0xB1>{});    // lane ^ 1
-  v = step(v, std::integral_constant<int, 0x4E>{});    // lane ^ 2
-  v = step(v, std::integral_constant<int, 0x141>{});   // mirror of 8
-  v = step(v, std::integral_constant<int, 0x140>{});   // mirror of 16
-  const int b = __float_as_int(v);
-  const float r0 = __int_as_float(__builtin_amdgcn_readlane(b, 0));
-  const float r1 = __int_as_float(__builtin_amdgcn_readlane(b, 16));
-  const float r2 = __int_as_float(__builtin_amdgcn_readlane(b, 32));
-  const float r3 = __int_as_float(__builtin_amdgcn_readlane(b, 48));
-  return (r0 + r1) + (r2 + r3);
-}
 
 // Sum over the threads of a row. `red`: the workgroup's wave sums, one set
 // per parity of the call, so that one barrier a call is enough.

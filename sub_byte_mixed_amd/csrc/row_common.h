@@ -4,6 +4,8 @@
 // two (16 elements) or four (32) neighbouring lanes.
 #pragma once
 
+#include <type_traits>
+
 #include "ops.h"
 #include "quant_common.h"
 
@@ -95,6 +97,24 @@ __device__ __forceinline__ float quad_xor1(float v) {
 }
 __device__ __forceinline__ float quad_xor2(float v) {
   return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, true));
+}
+
+// Sum over the wave, in every lane: four steps within rows of 16 lanes, then
+// the four row sums.
+__device__ __forceinline__ float wave_sum_f(float v) {
+  auto step = [](float x, auto ctrl) {
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  v = step(v, std::integral_constant<int, 0xB1>{});    // lane ^ 1
+  v = step(v, std::integral_constant<int, 0x4E>{});    // lane ^ 2
+  v = step(v, std::integral_constant<int, 0x141>{});   // mirror of 8
+  v = step(v, std::integral_constant<int, 0x140>{});   // mirror of 16
+  const int b = __float_as_int(v);
+  const float r0 = __int_as_float(__builtin_amdgcn_readlane(b, 0));
+  const float r1 = __int_as_float(__builtin_amdgcn_readlane(b, 16));
+  const float r2 = __int_as_float(__builtin_amdgcn_readlane(b, 32));
+  const float r3 = __int_as_float(__builtin_amdgcn_readlane(b, 48));
+  return (r0 + r1) + (r2 + r3);
 }
 
 // Statistics of one thread's quantized chunks.

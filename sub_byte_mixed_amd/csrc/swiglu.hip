@@ -8,8 +8,6 @@
 // host has divided once, and the next chunk's loads are issued before the
 // present one is worked on. sigmoid is 1 / (1 + exp(-g)) with the accurate
 // exp and division of fp32: they cost less than the chunk's bytes.
-#include <type_traits>
-
 #include "row_common.h"
 
 namespace snip {

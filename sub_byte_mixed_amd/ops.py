@@ -47,40 +47,59 @@ _TYPES = {torch.bfloat16: 0, torch.float32: 1}
 _ABSENT = (None, 0, 0)
 
 
-def _mat(t: Optional[torch.Tensor], name: str, shape, device) -> Tuple:
+def _mat(t: Optional[torch.Tensor], name: str, rows: int, cols: int, dev: int) -> Tuple:
     """(address, element type, leading dimension) of a matrix argument."""
     if t is None:
         return _ABSENT
     ty = _TYPES.get(t.dtype)
-    if ty is None:
-        raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-    if t.dim() != 2 or t.shape != shape:
-        raise ValueError(f"{name} must be of shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor on {device}, got one on {t.device}")
-    rows, cols = shape
-    if cols > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if ty is None or len(shape) != 2 or shape[0] != rows or shape[1] != cols or t.get_device() != dev:
+        raise ValueError(f"{name} must be a bfloat16 or float32 tensor of shape ({rows}, {cols}) on GPU {dev}, got "
+                         f"{t.dtype}, {tuple(shape)} on {t.device}")
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    ld = t.stride(0) if rows > 1 else -(-cols // 8) * 8      # one row: its stride says nothing
+    if rows == 1:                                            # one row: its stride says nothing
+        ld = -(-cols // 8) * 8
     return t.data_ptr(), ty, ld
 
 
-def _vec(t: Optional[torch.Tensor], name: str, n: int, dtypes, device) -> Optional[int]:
+def _vec(t: Optional[torch.Tensor], name: str, n: int, dtypes, dev: int) -> Optional[int]:
     if t is None:
         return None
-    if t.dtype not in dtypes or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous vector of {n} in {' or '.join(map(str, dtypes))}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor on {device}")
+    if t.dtype not in dtypes or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n} in {' or '.join(map(str, dtypes))} on GPU {dev}, "
+                         f"got {t.dtype}, {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _new(shape, dtype, device) -> torch.Tensor:
+def _new(rows: int, cols: int, dtype, dev: int) -> torch.Tensor:
     """A matrix whose rows are 16-byte aligned (a view of padded rows where the width asks for it)."""
-    rows, cols = shape
     pad = -(-cols // 8) * 8
-    t = torch.empty((rows, pad), dtype=dtype, device=device)
+    t = torch.empty((rows, pad), dtype=dtype, device=dev)
     return t if pad == cols else t[:, :cols]
+
+
+def _operand(q: "_S.QuantizedTensor", name: str, dev: int):
+    """Reference to a quantized operand's descriptor, once its buffers are known to hold it."""
+    blk, kind = _S.FP4_LAYOUT.get(q.format, (0, ""))
+    n = q.rows * q.k
+    need = ((q.codes, n // 2 if blk else n if q.format == _S.FP8 else 2 * n),
+            (q.scales, 0 if not blk else n // blk * (2 if kind == "bf16" else 1)), (q.texp, 4))
+    for t, size in need:
+        if size and (t is None or t.get_device() != dev or t.nbytes < size or not t.is_contiguous()):
+            raise ValueError(f"{name}: codes, scales and texp must be contiguous on GPU {dev} and hold "
+                             f"[{q.rows}][{q.k}] in format {q.format}")
+    return ctypes.byref(q.desc())
+
+
+def _scratch(ws: Optional[torch.Tensor], dev: int) -> Tuple[Optional[int], int]:
+    """(address, bytes) of a workspace argument."""
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on GPU {dev}")
+    return ws.data_ptr(), ws.nbytes
 
 
 def _placed(fn):
@@ -89,40 +108,48 @@ def _placed(fn):
     the stream that its kernels run on."""
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
-        if not isinstance(first, torch.Tensor) or first.dim() != 2 or not first.is_cuda:
+        dev = first.get_device() if isinstance(first, torch.Tensor) and first.dim() == 2 else -1
+        if dev < 0:
             raise ValueError(f"the first argument of {fn.__name__} must be a 2-D GPU tensor")
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
-                stream = (torch.cuda.ExternalStream(int(stream), device=first.device) if int(stream)
-                          else torch.cuda.default_stream(first.device))
+                stream = torch.cuda.ExternalStream(int(stream), dev) if int(stream) else torch.cuda.default_stream(dev)
             with torch.cuda.stream(stream):
                 return fn(first, *args, **kw)
-        if first.device.index != torch.cuda.current_device():
-            with torch.cuda.device(first.device):
+        if dev != torch.cuda.current_device():
+            with torch.cuda.device(dev):
                 return fn(first, *args, **kw)
         return fn(first, *args, **kw)
     return call
+
+
+def _current(dev: int) -> int:
+    """Handle of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 _F32 = (torch.float32,)
 _ANY = (torch.bfloat16, torch.float32)
 
 
-def _quant_out(q, out_fmt, shape, device, amax, stats, with_stats, ws, sizer):
-    """The quantized output's arguments of a forward call: descriptor, stats, workspace."""
+def _quant_out(q, out_fmt, rows, cols, dev, amax, stats, with_stats, ws, sizer):
+    """The quantized output of a forward call: (q, stats, their arguments of
+    the C call: descriptor, maximum, statistics, workspace address and size)."""
     if q is None and out_fmt is None:
         if stats is not None:
             raise ValueError("stats belong to a quantized output (out_fmt or q)")
-        return None, None, None
+        return None, None, (None, None, None, None, 0)
     if q is None:
-        q = _S.QuantizedTensor(out_fmt, shape[0], shape[1], device)
+        q = _S.QuantizedTensor(out_fmt, rows, cols, dev)
     elif out_fmt is not None and q.format != out_fmt:
         raise ValueError(f"q is in format {q.format}, out_fmt is {out_fmt}")
-    if stats is None and with_stats:
-        stats = _S.new_stats(1, device)
+    if stats is None:
+        stats = _S.new_stats(1, dev) if with_stats else None
+    elif stats.get_device() != dev or stats.nbytes < _S.STATS_BYTES or not stats.is_contiguous():
+        raise ValueError(f"stats must be a statistics tensor (new_stats) on GPU {dev}")
     if ws is None:
-        ws = _S._workspace(sizer(shape[0], shape[1], q.format), device)
-    return q, stats, ws
+        ws = _S._workspace(sizer(rows, cols, q.format), dev)
+    return q, stats, (_operand(q, "q", dev), _S._amax_ptr(amax), _S._ptr(stats), *_scratch(ws, dev))
 
 
 @_placed
@@ -141,24 +168,24 @@ def rmsnorm_fwd(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, res: Op
     or MXFP4, or a QuantizedTensor to write into; None otherwise). amax: a
     supplied max|y| for its tensor scale, as in linear_fwd_save (unused without
     q)."""
-    shape, dev = x.shape, x.device
-    rows, cols = shape
-    px = _mat(x, "x", shape, dev)
-    pr = _mat(res, "res", shape, dev)
+    rows, cols = x.shape
+    dev = x.get_device()
+    px = _mat(x, "x", rows, cols, dev)
+    pr = _mat(res, "res", rows, cols, dev)
     pg = _vec(gamma, "gamma", cols, _ANY, dev)
     if h is None and res is not None:
-        h = _new(shape, h_dtype, dev)
+        h = _new(rows, cols, h_dtype, dev)
     if y is None and with_y:
-        y = _new(shape, y_dtype, dev)
+        y = _new(rows, cols, y_dtype, dev)
     if rstd is None and with_rstd:
         rstd = torch.empty(rows, dtype=torch.float32, device=dev)
     L = _S.lib()
-    q, stats, ws = _quant_out(q, out_fmt, shape, dev, amax, stats, with_stats, ws, L.snipop_rmsnorm_fwd_workspace)
-    d = None if q is None else ctypes.byref(q.desc())
+    q, stats, (d, pa, ps, *pw) = _quant_out(q, out_fmt, rows, cols, dev, amax, stats, with_stats, ws,
+                                            L.snipop_rmsnorm_fwd_workspace)
     _S._check(L.snipop_rmsnorm_fwd(
-        *px, *pr, pg, _TYPES[gamma.dtype], rows, cols, eps, *_mat(h, "h", shape, dev), *_mat(y, "y", shape, dev),
-        _vec(rstd, "rstd", rows, _F32, dev), d, rounding, seed, tensor_id, _S._amax_ptr(amax), _S._ptr(stats),
-        _S._ptr(ws), 0 if ws is None else ws.numel(), _S._stream(None)))
+        *px, *pr, pg, _TYPES[gamma.dtype], rows, cols, eps, *_mat(h, "h", rows, cols, dev),
+        *_mat(y, "y", rows, cols, dev), _vec(rstd, "rstd", rows, _F32, dev), d, rounding, seed, tensor_id, pa, ps, *pw,
+        _current(dev)))
     return y, h, rstd, q, stats
 
 
@@ -170,12 +197,12 @@ def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, rstd: to
     """snipop_rmsnorm_bwd: the gradients of y from rmsnorm_fwd. h: its h (x
     where there was no res); dres: the gradient that reaches h along the
     residual stream. Returns (dx, dgamma); dx is the gradient of x and of res."""
-    shape, dev = dy.shape, dy.device
-    rows, cols = shape
-    py = _mat(dy, "dy", shape, dev)
-    ph = _mat(h, "h", shape, dev)
+    rows, cols = dy.shape
+    dev = dy.get_device()
+    py = _mat(dy, "dy", rows, cols, dev)
+    ph = _mat(h, "h", rows, cols, dev)
     if dx is None and need_dx:
-        dx = _new(shape, dx_dtype, dev)
+        dx = _new(rows, cols, dx_dtype, dev)
     if dgamma is None and need_dgamma:
         dgamma = torch.empty(cols, dtype=torch.float32, device=dev)
     L = _S.lib()
@@ -183,8 +210,8 @@ def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, rstd: to
         ws = _S._workspace(L.snipop_rmsnorm_bwd_workspace(rows, cols), dev)
     _S._check(L.snipop_rmsnorm_bwd(
         *py, *ph, _vec(gamma, "gamma", cols, _ANY, dev), _TYPES[gamma.dtype], _vec(rstd, "rstd", rows, _F32, dev),
-        *_mat(dres, "dres", shape, dev), rows, cols, *_mat(dx, "dx", shape, dev),
-        _vec(dgamma, "dgamma", cols, _F32, dev), _S._ptr(ws), 0 if ws is None else ws.numel(), _S._stream(None)))
+        *_mat(dres, "dres", rows, cols, dev), rows, cols, *_mat(dx, "dx", rows, cols, dev),
+        _vec(dgamma, "dgamma", cols, _F32, dev), *_scratch(ws, dev), _current(dev)))
     return dx, dgamma
 
 
@@ -197,20 +224,20 @@ def swiglu_fwd(gate: torch.Tensor, up: torch.Tensor, y: Optional[torch.Tensor] =
     """snipop_swiglu_fwd: y = gate * sigmoid(gate) * up. Returns (y, q,
     stats), with q, amax and stats as in rmsnorm_fwd. gate and up may be the
     two halves of one tensor's columns."""
-    shape, dev = gate.shape, gate.device
-    rows, cols = shape
+    rows, cols = gate.shape
+    dev = gate.get_device()
     if up.dtype != gate.dtype:
         raise ValueError("gate and up must have the same type")
-    pg, tg, lg = _mat(gate, "gate", shape, dev)
-    pu, _, lu = _mat(up, "up", shape, dev)
+    pg, tg, lg = _mat(gate, "gate", rows, cols, dev)
+    pu, _, lu = _mat(up, "up", rows, cols, dev)
     if y is None and with_y:
-        y = _new(shape, y_dtype, dev)
+        y = _new(rows, cols, y_dtype, dev)
     L = _S.lib()
-    q, stats, ws = _quant_out(q, out_fmt, shape, dev, amax, stats, with_stats, ws, L.snipop_swiglu_fwd_workspace)
-    d = None if q is None else ctypes.byref(q.desc())
+    q, stats, (d, pa, ps, *pw) = _quant_out(q, out_fmt, rows, cols, dev, amax, stats, with_stats, ws,
+                                            L.snipop_swiglu_fwd_workspace)
     _S._check(L.snipop_swiglu_fwd(
-        pg, lg, pu, lu, tg, rows, cols, *_mat(y, "y", shape, dev), d, rounding, seed, tensor_id, _S._amax_ptr(amax),
-        _S._ptr(stats), _S._ptr(ws), 0 if ws is None else ws.numel(), _S._stream(None)))
+        pg, lg, pu, lu, tg, rows, cols, *_mat(y, "y", rows, cols, dev), d, rounding, seed, tensor_id, pa, ps, *pw,
+        _current(dev)))
     return y, q, stats
 
 
@@ -219,23 +246,23 @@ def swiglu_bwd(dy: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, dgate: Op
                dup: Optional[torch.Tensor] = None, need_dgate: bool = True, need_dup: bool = True,
                dtype: torch.dtype = torch.bfloat16):
     """snipop_swiglu_bwd: (dgate, dup) from the gradient of swiglu_fwd's y."""
-    shape, dev = dy.shape, dy.device
-    rows, cols = shape
+    rows, cols = dy.shape
+    dev = dy.get_device()
     if up.dtype != gate.dtype:
         raise ValueError("gate and up must have the same type")
-    py = _mat(dy, "dy", shape, dev)
-    pg, tg, lg = _mat(gate, "gate", shape, dev)
-    pu, _, lu = _mat(up, "up", shape, dev)
+    py = _mat(dy, "dy", rows, cols, dev)
+    pg, tg, lg = _mat(gate, "gate", rows, cols, dev)
+    pu, _, lu = _mat(up, "up", rows, cols, dev)
     if dgate is None and need_dgate:
-        dgate = _new(shape, dtype, dev)
+        dgate = _new(rows, cols, dtype, dev)
     if dup is None and need_dup:
-        dup = _new(shape, dtype, dev)
+        dup = _new(rows, cols, dtype, dev)
     if dgate is not None and dup is not None and dgate.dtype != dup.dtype:
         raise ValueError("dgate and dup must have the same type")
-    pdg, tdg, ldg = _mat(dgate, "dgate", shape, dev)
-    pdu, tdu, ldu = _mat(dup, "dup", shape, dev)
+    pdg, tdg, ldg = _mat(dgate, "dgate", rows, cols, dev)
+    pdu, tdu, ldu = _mat(dup, "dup", rows, cols, dev)
     _S._check(_S.lib().snipop_swiglu_bwd(*py, pg, lg, pu, lu, tg, rows, cols, pdg, ldg, pdu, ldu, max(tdg, tdu),
-                                         _S._stream(None)))
+                                         _current(dev)))
     return dgate, dup
 
 
@@ -244,21 +271,20 @@ def qgemv(x: torch.Tensor, w: "_S.QuantizedTensor", y: Optional[torch.Tensor] = 
           y_dtype: torch.dtype = torch.float32) -> torch.Tensor:
     """snipop_qgemv: y [tokens, N] = x [tokens, K] . dequant(w)^T for 1 to 16
     tokens, x in bfloat16, w in any quantized format with K % 32 == 0."""
-    shape, dev = x.shape, x.device
+    m, k = x.shape
+    dev = x.get_device()
     if x.dtype != torch.bfloat16:
         raise ValueError("x must be bfloat16")
-    if shape[1] != w.k:
-        raise ValueError(f"x has {shape[1]} columns, w K={w.k}")
-    if w.codes.device != dev:
-        raise ValueError(f"w must be on {dev}, is on {w.codes.device}")
-    px, _, lx = _mat(x, "x", shape, dev)
-    out = torch.Size((shape[0], w.rows))
+    if k != w.k:
+        raise ValueError(f"x has {k} columns, w K={w.k}")
+    px, _, lx = _mat(x, "x", m, k, dev)
+    n = w.rows
     if y is None:
-        y = torch.empty(out, dtype=y_dtype, device=dev)
+        y = torch.empty((m, n), dtype=y_dtype, device=x.device)
     ty = _TYPES.get(y.dtype)
-    if ty is None or y.shape != out or y.device != dev or (w.rows > 1 and y.stride(1) != 1):
-        raise ValueError(f"y must be a bfloat16 or float32 tensor of shape {tuple(out)} with unit column stride on {dev}")
-    ly = y.stride(0) if shape[0] > 1 else max(y.stride(0), w.rows)
-    _S._check(_S.lib().snipop_qgemv(px, lx, shape[0], ctypes.byref(w.desc()), y.data_ptr(), ty, ly,
-                                    _S._stream(None)))
+    if ty is None or y.shape != (m, n) or y.get_device() != dev or (n > 1 and y.stride(1) != 1):
+        raise ValueError(f"y must be a bfloat16 or float32 tensor of shape ({m}, {n}) with unit column stride on "
+                         f"{x.device}")
+    ly = y.stride(0) if m > 1 else n
+    _S._check(_S.lib().snipop_qgemv(px, lx, m, _operand(w, "w", dev), y.data_ptr(), ty, ly, _current(dev)))
     return y

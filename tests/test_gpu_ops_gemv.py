@@ -138,3 +138,38 @@ def test_refusals_in_the_binding():
     with pytest.raises(S.SnipError) as e:
         S.qgemv(rand((17, 64), BF, 9).cuda(), w)
     assert e.value.code == -2
+
+
+@pytest.mark.parametrize("fmt", [S.FP8, S.NVFP4, S.MXFP4, S.FP4_BF16_B16])
+@pytest.mark.parametrize("n,k", [(8200, 96), (16421, 288), (20, 70016)])
+def test_many_rows_and_long_rows(fmt, n, k):
+    """The widths at which a wave takes two and four row tiles, and a row too
+    long for its scales to be held on chip."""
+    w = raw_weights(fmt, n, k, n + k)
+    for m in (1, 3, 6, 16):
+        say("qgemv", fmt, n, k, m)
+        x = rand((m, k), BF, m).cuda()
+        check(x, w, S.qgemv(x, w))
+
+
+@pytest.mark.parametrize("fmt,code", [(S.MXFP4, 255), (S.FP4_E8M0_B16, 255), (S.NVFP4, 0x7F), (S.FP4_E4M3_B32, 0xFF)])
+def test_nan_scales_reach_their_row_alone(fmt, code):
+    for n, k in ((40, 256), (40, 1056), (8200, 64)):
+        w = raw_weights(fmt, n, k, 11)
+        sc = w.scales.view(n, -1)
+        sc[5, -1] = code
+        sc[n - 1, 0] = code
+        for m in (1, 4, 16):
+            say("nan scale", fmt, n, k, m)
+            bad = torch.isnan(S.qgemv(rand((m, k), BF, m).cuda(), w))
+            assert bad[:, 5].all() and bad[:, n - 1].all() and int(bad.sum()) == 2 * m
+
+
+def test_operands_that_do_not_hold_the_weights_are_refused():
+    w = raw_weights(S.NVFP4, 8, 64, 8)
+    x = rand((1, 64), BF, 9).cuda()
+    for bad in (dict(codes=w.codes[:-1]), dict(codes=w.codes.cpu()), dict(scales=w.scales[:-1]), dict(texp=w.texp.cpu())):
+        a = dict(codes=w.codes, scales=w.scales, texp=w.texp)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            S.qgemv(x, S.QuantizedTensor(S.NVFP4, 8, 64, "cuda", **a))
