@@ -104,7 +104,7 @@ int snipop_rmsnorm_bwd(const void* dy, int dy_type, int64_t lddy, const void* h,
  *              snipop_rmsnorm_fwd; y may be gate or up itself unless the
  *              maximum is computed too (out in NVFP4 or FP8 without amax_in
  *              is fine: the pass for the maximum writes nothing).
- *   rows, cols > 0. One of y and out must be given.
+ *   rows > 0, 0 < cols <= 2^31. One of y and out must be given.
  * Errors: NULL, SHAPE, ALIGN, FORMAT, WORKSPACE, HIP. */
 int snipop_swiglu_fwd(const void* gate, int64_t ldg, const void* up, int64_t ldu, int type,
                       int64_t rows, int64_t cols, void* y, int y_type, int64_t ldy,

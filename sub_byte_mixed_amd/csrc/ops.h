@@ -9,6 +9,12 @@ namespace snip {
 
 constexpr int kOpsAmaxWG = 1024;   // max workgroups of a pass for the maximum
 constexpr int kOpsWG = 2048;       // max workgroups of a pass with statistics
+// SwiGLU: workgroups that come and go spread better than a few that walk far
+// (4096 x 5632 backward: 60 us with 32768, 67 with 1024), but each leaves a
+// partial of the statistics (8192 x 11008 to FP8: 144 us with 1024).
+constexpr int kGateWG = 32768;
+constexpr int kGateStatsWG = 1024;
+static_assert(kGateStatsWG <= kOpsWG, "the workspace holds kOpsWG partials");
 
 // A matrix argument: rows of `ld` elements of `type` (SNIPOP_BF16 / _F32).
 struct Mat {
@@ -51,10 +57,16 @@ struct NormBwd {
   int32_t cols;
 };
 
+// A grid's stride over the chunks of a matrix, in rows and chunks.
+struct GateStride {
+  int64_t rows;
+  int32_t chunks;
+};
+
 struct GateFwd {
   Mat gate, up, y;
   int64_t rows, cols;
-  int64_t drow, dchunk;        // a grid stride in rows and 8-element chunks
+  GateStride d;
   OpQuant q;
   uint32_t* amax_out;
 };
@@ -62,7 +74,7 @@ struct GateFwd {
 struct GateBwd {
   Mat dy, gate, up, dgate, dup;
   int64_t rows, cols;
-  int64_t drow, dchunk;
+  GateStride d;
 };
 
 struct Gemv {
@@ -82,11 +94,12 @@ constexpr int kPassAmax = -1;
 // Grids, and asynchronous launchers that return the launch's hipError_t.
 int norm_fwd_wg(int64_t rows, int64_t cols, bool amax);
 int norm_bwd_wg(int64_t rows, int64_t cols);
-int gate_wg(int64_t rows, int64_t cols, bool amax);
+int gate_wg(const Mat& gate, int64_t rows, int64_t cols, int most);
 hipError_t launch_norm_fwd(int pass, const NormFwd& a, int nwg, hipStream_t s);
 hipError_t launch_norm_bwd(const NormBwd& a, float* dgamma, int nwg, hipStream_t s);
 hipError_t launch_gate_fwd(int pass, GateFwd a, int nwg, hipStream_t s);
 hipError_t launch_gate_bwd(GateBwd a, int nwg, hipStream_t s);
+hipError_t launch_op_stats(const StatPart* part, int n, snip_stats* out, hipStream_t s);
 hipError_t launch_gemv(int format, const Gemv& a, hipStream_t s);
 
 }  // namespace snip

@@ -13,6 +13,7 @@ namespace {
 
 // Rows and leading dimensions beyond this would overflow 64-bit offsets.
 constexpr int64_t kMaxDim = (int64_t)1 << 40;
+constexpr int64_t kMaxGateCols = (int64_t)1 << 31;   // a row's chunks are counted in 32 bits
 
 // Scratch of a quantized output: partials of the pass for the maximum, and
 // of the statistics.
@@ -95,12 +96,8 @@ int check_out(const char* who, const snip_qtensor* out, int64_t rows, int64_t co
 
 int finalize(const OpQuant& q, int nwg, snip_stats* stats, hipStream_t s) {
   if (!stats) return SNIP_OK;
-  FJobs f;
-  std::memset(&f, 0, sizeof(f));
-  f.j[0] = FJob{q.part, nwg, stats};
-  f.n = 1;
   const int slot = timing_begin(LaunchTag{SNIP_LAUNCH_FINALIZE, -1, -1, -1, 1.0}, s);
-  const hipError_t e = launch_finalize(f, s);
+  const hipError_t e = launch_op_stats(q.part, nwg, stats, s);
   timing_end(slot, s);
   return hip_check(e, "finalize launch");
 }
@@ -216,7 +213,7 @@ int snipop_swiglu_fwd(const void* gate, int64_t ldg, const void* up, int64_t ldu
   const char* who = "snipop_swiglu_fwd";
   if (!gate || !up) return fail(SNIP_E_NULL, "%s: gate and up must be non-NULL", who);
   if (!y && !out) return fail(SNIP_E_NULL, "%s: no output given", who);
-  int rc = check_shape(who, rows, cols, kMaxDim);
+  int rc = check_shape(who, rows, cols, kMaxGateCols);
   if (rc) return rc;
   GateFwd a;
   std::memset(&a, 0, sizeof(a));
@@ -232,13 +229,13 @@ int snipop_swiglu_fwd(const void* gate, int64_t ldg, const void* up, int64_t ldu
   const double work = (double)rows * (double)cols;
   if (amax) {
     a.amax_out = amax;
-    a.q.n_amax_part = gate_wg(rows, cols, true);
+    a.q.n_amax_part = gate_wg(a.gate, rows, cols, kOpsAmaxWG);
     const int slot = timing_begin(LaunchTag{SNIP_LAUNCH_AMAX, -1, -1, -1, work}, s);
     const hipError_t e = launch_gate_fwd(kPassAmax, a, a.q.n_amax_part, s);
     timing_end(slot, s);
     if ((rc = hip_check(e, "swiglu amax launch"))) return rc;
   }
-  const int nwg = gate_wg(rows, cols, false);
+  const int nwg = gate_wg(a.gate, rows, cols, stats ? kGateStatsWG : kGateWG);
   const int slot = timing_begin(op_tag(SNIPOP_LAUNCH_GATE, out, rounding, work), s);
   const hipError_t e = launch_gate_fwd(out ? out->format : SNIP_BF16, a, nwg, s);
   timing_end(slot, s);
@@ -253,7 +250,7 @@ int snipop_swiglu_bwd(const void* dy, int dy_type, int64_t lddy, const void* gat
   const char* who = "snipop_swiglu_bwd";
   if (!dy || !gate || !up) return fail(SNIP_E_NULL, "%s: dy, gate and up must be non-NULL", who);
   if (!dgate && !dup) return fail(SNIP_E_NULL, "%s: no output given", who);
-  int rc = check_shape(who, rows, cols, kMaxDim);
+  int rc = check_shape(who, rows, cols, kMaxGateCols);
   if (rc) return rc;
   GateBwd a;
   std::memset(&a, 0, sizeof(a));
@@ -266,7 +263,7 @@ int snipop_swiglu_bwd(const void* dy, int dy_type, int64_t lddy, const void* gat
   a.cols = cols;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int slot = timing_begin(op_tag(SNIPOP_LAUNCH_GATE, nullptr, -1, (double)rows * (double)cols), s);
-  const hipError_t e = launch_gate_bwd(a, gate_wg(rows, cols, false), s);
+  const hipError_t e = launch_gate_bwd(a, gate_wg(a.gate, rows, cols, kGateWG), s);
   timing_end(slot, s);
   if ((rc = hip_check(e, "swiglu backward launch"))) return rc;
   return ok();

@@ -13,17 +13,17 @@
 
 namespace snip {
 
-// Sum over the threads of a row. `red`: the workgroup's wave sums, one set
-// per parity of the call, so that one barrier a call is enough.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float (*red)[TPR / 64], int parity) {
+// Sum over the threads of a row, which are the workgroup's (WG) or a wave's.
+// `red`: the workgroup's wave sums, one set per parity of the call, so that
+// one barrier a call is enough.
+template <bool WG>
+__device__ __forceinline__ float row_sum(float v, float (*red)[16], int parity) {
   v = wave_sum_f(v);
-  if constexpr (TPR > 64) {
+  if constexpr (WG) {
     if ((threadIdx.x & 63) == 0) red[parity][threadIdx.x >> 6] = v;
     __syncthreads();
     v = red[parity][0];
-#pragma unroll
-    for (int w = 1; w < TPR / 64; ++w) v += red[parity][w];
+    for (int w = 1; w < (int)(blockDim.x >> 6); ++w) v += red[parity][w];
   }
   return v;
 }
@@ -31,80 +31,89 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[TPR / 64], int pa
 // The thread's chunks of a row that starts at element `off`. Chunks beyond
 // the row keep what they hold (zeros); a last chunk of cols % 8 elements is
 // the business of one thread.
-template <int TPR, int VPT, bool F32>
-__device__ __forceinline__ void load_row(const void* p, int64_t off, int t, int cols, Raw8<F32> (&r)[VPT]) {
+template <int VPT, bool F32>
+__device__ __forceinline__ void load_row(const void* p, int64_t off, int t, int tpr, int cols, Raw<F32> (&r)[VPT]) {
   const int nch = cols >> 3;
 #pragma unroll
   for (int v = 0; v < VPT; ++v)
-    if (t + v * TPR < nch) load_whole(p, off + 8 * (t + v * TPR), r[v]);
-  if ((cols & 7) && t == nch % TPR) {
+    if (t + v * tpr < nch) load_whole(p, off + 8 * (t + v * tpr), r[v]);
+  if ((cols & 7) && t == nch % tpr) {
+    Raw<F32> last;
+    load_partial(p, off + 8 * nch, cols & 7, last);
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
-      if (v == nch / TPR) load_partial(p, off + 8 * nch, cols & 7, r[v]);
+      if (v == nch / tpr) r[v] = last;
   }
 }
 
 // gamma as fp32, from either type: it is read once, after the loads of the
 // first row, and waited for here.
-template <int TPR, int VPT>
-__device__ __forceinline__ void load_gamma(const Mat& m, int t, int cols, float (&g)[VPT][8]) {
+template <int VPT>
+__device__ __forceinline__ void load_gamma(const Mat& m, int t, int tpr, int cols, float (&g)[VPT][8]) {
   if (m.type == SNIPOP_F32) {
-    Raw8<true> r[VPT] = {};
-    load_row<TPR>(m.p, 0, t, cols, r);
+    Raw<true> r[VPT] = {};
+    load_row(m.p, 0, t, tpr, cols, r);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) raw_to_f32(r[v], g[v]);
   } else {
-    Raw8<false> r[VPT] = {};
-    load_row<TPR>(m.p, 0, t, cols, r);
+    Raw<false> r[VPT] = {};
+    load_row(m.p, 0, t, tpr, cols, r);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) raw_to_f32(r[v], g[v]);
   }
 }
 
-template <int TPR, int VPT>
-__device__ __forceinline__ void store_row(const Mat& m, int64_t row, int t, int cols, const float (&x)[VPT][8]) {
+template <int VPT>
+__device__ __forceinline__ void store_row(const Mat& m, int64_t row, int t, int tpr, int cols, const float (&x)[VPT][8]) {
   const bool f32 = m.type == SNIPOP_F32;
   const int nch = cols >> 3;
   const int64_t off = row * m.ld;
 #pragma unroll
   for (int v = 0; v < VPT; ++v)
-    if (t + v * TPR < nch) store_whole(m.p, f32, off + 8 * (t + v * TPR), x[v]);
-  if ((cols & 7) && t == nch % TPR) {
+    if (t + v * tpr < nch) store_whole(m.p, f32, off + 8 * (t + v * tpr), x[v]);
+  if ((cols & 7) && t == nch % tpr) {
     float p[8];
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
-      if (v == nch / TPR)
+      if (v == nch / tpr)
         for (int i = 0; i < 8; ++i) p[i] = x[v][i];
     store_partial(m.p, f32, off + 8 * nch, cols & 7, p);
   }
 }
 
-constexpr int norm_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+// A row to a workgroup (WG), or to each of a workgroup's four waves.
+template <bool WG>
+struct RowMap {
+  int t, tpr, sub, rpb;
+  __device__ RowMap()
+      : t(WG ? threadIdx.x : threadIdx.x & 63), tpr(WG ? blockDim.x : 64), sub(WG ? 0 : threadIdx.x >> 6),
+        rpb(WG ? 1 : 4) {}
+};
 
 // ------------------------------------------------------------ forward
-template <int TPR, int VPT, int PASS, bool XF, bool RF>
-__global__ __launch_bounds__(norm_threads(TPR)) void rmsnorm_fwd_kernel(NormFwd A) {
-  constexpr int NT = norm_threads(TPR), RPB = NT / TPR, NW = NT / 64;
+template <bool WG, int VPT, int PASS, bool SR, bool XF, bool RF>
+__global__ __launch_bounds__(WG ? 1024 : 256) void rmsnorm_fwd_kernel(NormFwd A) {
   constexpr bool QUANT = PASS == SNIP_FP8_E4M3 || PASS == SNIP_NVFP4 || PASS == SNIP_MXFP4;
-  __shared__ float red[2][TPR / 64];
-  __shared__ uint32_t ured[2 * NW];
-  __shared__ double dred[2 * NW];
+  __shared__ float red[2][16];
+  __shared__ uint32_t ured[32];
+  __shared__ double dred[32];
   __shared__ float inv_lut[PASS == SNIP_NVFP4 ? 128 : 1];
-  const int t = threadIdx.x % TPR;
-  const int64_t step = (int64_t)gridDim.x * RPB;
-  int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  const RowMap<WG> R;
+  const int t = R.t;
+  const int64_t step = (int64_t)gridDim.x * R.rpb;
+  int64_t row = (int64_t)blockIdx.x * R.rpb + R.sub;
 
-  Raw8<XF> rx[VPT] = {};
-  Raw8<RF> rr[VPT] = {};
+  Raw<XF> rx[VPT] = {};
+  Raw<RF> rr[VPT] = {};
   float g[VPT][8];
   auto load = [&](int64_t i) {
     if (i < A.rows) {
-      load_row<TPR>(A.x.p, i * A.x.ld, t, A.cols, rx);
-      if (A.res.p) load_row<TPR>(A.res.p, i * A.res.ld, t, A.cols, rr);
+      load_row(A.x.p, i * A.x.ld, t, R.tpr, A.cols, rx);
+      if (A.res.p) load_row(A.res.p, i * A.res.ld, t, R.tpr, A.cols, rr);
     }
   };
   load(row);
-  load_gamma<TPR>(A.gamma, t, A.cols, g);
+  load_gamma(A.gamma, t, R.tpr, A.cols, g);
 
   const int eS = QUANT ? op_tensor_exp<PASS>(A.q, ured) : 0;
   if constexpr (PASS == SNIP_NVFP4) fill_inv_lut(inv_lut);
@@ -127,10 +136,10 @@ __global__ __launch_bounds__(norm_threads(TPR)) void rmsnorm_fwd_kernel(NormFwd 
       }
     }
     load(row + step);
-    ss = row_sum<TPR>(ss, red, it & 1);
+    ss = row_sum<WG>(ss, red, it & 1);
     const float r = 1.0f / sqrtf(ss / (float)A.cols + A.eps);
     if constexpr (PASS != kPassAmax) {
-      if (A.h.p) store_row<TPR>(A.h, row, t, A.cols, h);
+      if (A.h.p) store_row(A.h, row, t, R.tpr, A.cols, h);
       if (A.rstd && t == 0) A.rstd[row] = r;
     }
 #pragma unroll
@@ -140,13 +149,13 @@ __global__ __launch_bounds__(norm_threads(TPR)) void rmsnorm_fwd_kernel(NormFwd 
     if constexpr (PASS == kPassAmax) {
 #pragma unroll
       for (int v = 0; v < VPT; ++v)
-        if (8 * (t + v * TPR) < A.cols) amax = chunk_max_bits(h[v], amax);
+        if (8 * (t + v * R.tpr) < A.cols) amax = chunk_max_bits(h[v], amax);
     } else {
-      if (A.y.p) store_row<TPR>(A.y, row, t, A.cols, h);
+      if (A.y.p) store_row(A.y, row, t, R.tpr, A.cols, h);
       if constexpr (QUANT) {
 #pragma unroll
         for (int v = 0; v < VPT; ++v)
-          if (t + v * TPR < qch) quant_chunk<PASS>(A.q, eS, inv_lut, row * qch + t + v * TPR, h[v], stats, acc);
+          if (t + v * R.tpr < qch) quant_chunk<PASS, SR>(A.q, eS, inv_lut, row * qch + t + v * R.tpr, h[v], stats, acc);
       }
     }
   }
@@ -166,30 +175,30 @@ __global__ __launch_bounds__(norm_threads(TPR)) void rmsnorm_fwd_kernel(NormFwd 
 // summed in registers; each workgroup leaves one partial row, and a second
 // launch sums those in a fixed order (no atomics: the result does not depend
 // on timing).
-template <int TPR, int VPT, bool YF, bool HF, bool RF>
-__global__ __launch_bounds__(norm_threads(TPR)) void rmsnorm_bwd_kernel(NormBwd A) {
-  constexpr int NT = norm_threads(TPR), RPB = NT / TPR;
-  __shared__ float red[2][TPR / 64];
-  __shared__ float lds[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? VPT * 8 * TPR : 1];
-  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-  const int64_t step = (int64_t)gridDim.x * RPB;
-  int64_t row = (int64_t)blockIdx.x * RPB + sub;
+template <bool WG, int VPT, bool YF, bool HF, bool RF>
+__global__ __launch_bounds__(WG ? 1024 : 256) void rmsnorm_bwd_kernel(NormBwd A) {
+  __shared__ float red[2][16];
+  __shared__ float lds[WG ? 1 : 3][WG ? 1 : VPT * 8 * 64];
+  const RowMap<WG> R;
+  const int t = R.t, sub = R.sub;
+  const int64_t step = (int64_t)gridDim.x * R.rpb;
+  int64_t row = (int64_t)blockIdx.x * R.rpb + sub;
 
-  Raw8<YF> ry[VPT] = {};
-  Raw8<HF> rh[VPT] = {};
-  Raw8<RF> rr[VPT] = {};
+  Raw<YF> ry[VPT] = {};
+  Raw<HF> rh[VPT] = {};
+  Raw<RF> rr[VPT] = {};
   float g[VPT][8];
   float rs = 0.0f;
   auto load = [&](int64_t i) {
     if (i < A.rows) {
-      load_row<TPR>(A.dy.p, i * A.dy.ld, t, A.cols, ry);
-      load_row<TPR>(A.h.p, i * A.h.ld, t, A.cols, rh);
-      if (A.dres.p) load_row<TPR>(A.dres.p, i * A.dres.ld, t, A.cols, rr);
+      load_row(A.dy.p, i * A.dy.ld, t, R.tpr, A.cols, ry);
+      load_row(A.h.p, i * A.h.ld, t, R.tpr, A.cols, rh);
+      if (A.dres.p) load_row(A.dres.p, i * A.dres.ld, t, R.tpr, A.cols, rr);
       rs = A.rstd[i];
     }
   };
   load(row);
-  load_gamma<TPR>(A.gamma, t, A.cols, g);
+  load_gamma(A.gamma, t, R.tpr, A.cols, g);
   float dg[VPT][8];
 #pragma unroll
   for (int v = 0; v < VPT; ++v)
@@ -214,7 +223,7 @@ __global__ __launch_bounds__(norm_threads(TPR)) void rmsnorm_bwd_kernel(NormBwd 
       }
     }
     load(row + step);
-    const float mean = row_sum<TPR>(dot, red, it & 1) / (float)A.cols;
+    const float mean = row_sum<WG>(dot, red, it & 1) / (float)A.cols;
     if (A.dx.p) {
 #pragma unroll
       for (int v = 0; v < VPT; ++v)
@@ -223,43 +232,43 @@ __global__ __launch_bounds__(norm_threads(TPR)) void rmsnorm_bwd_kernel(NormBwd 
           d[v][i] = r * fmaf(-xh[v][i], mean, d[v][i]);
           if (A.dres.p) d[v][i] += res[v][i];
         }
-      store_row<TPR>(A.dx, row, t, A.cols, d);
+      store_row(A.dx, row, t, R.tpr, A.cols, d);
     }
   }
   if (!A.part) return;
-  if constexpr (RPB > 1) {
+  if constexpr (!WG) {
     if (sub > 0) {
 #pragma unroll
       for (int v = 0; v < VPT; ++v)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) lds[sub - 1][(v * 8 + i) * TPR + t] = dg[v][i];
+        for (int i = 0; i < 8; ++i) lds[sub - 1][(v * 8 + i) * 64 + t] = dg[v][i];
     }
     __syncthreads();
     if (sub > 0) return;
 #pragma unroll
-    for (int s = 0; s < RPB - 1; ++s)
+    for (int s = 0; s < 3; ++s)
 #pragma unroll
       for (int v = 0; v < VPT; ++v)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dg[v][i] += lds[s][(v * 8 + i) * TPR + t];
+        for (int i = 0; i < 8; ++i) dg[v][i] += lds[s][(v * 8 + i) * 64 + t];
   }
   float* dst = A.part + (int64_t)blockIdx.x * A.part_ld;
 #pragma unroll
   for (int v = 0; v < VPT; ++v)
-    if (8 * (t + v * TPR) < A.part_ld) store_whole(dst, true, 8 * (t + v * TPR), dg[v]);
+    if (8 * (t + v * R.tpr) < A.part_ld) store_whole(dst, true, 8 * (t + v * R.tpr), dg[v]);
 }
 
-// dgamma[c] = sum over the workgroups' partial rows: 16 threads x 4 columns,
-// 16 slices of the rows joined through LDS.
+// dgamma[c] = sum over the workgroups' partial rows: 8 threads x 4 columns
+// (a 128-byte line of a row), 32 slices of the rows joined through LDS.
 __global__ __launch_bounds__(256) void dgamma_sum_kernel(const float* part, int64_t ld, int nwg, int cols,
                                                          float* dgamma) {
-  __shared__ float4 red[16][16];
-  const int cx = threadIdx.x & 15, slice = threadIdx.x >> 4;
-  const int64_t c = ((int64_t)blockIdx.x * 16 + cx) * 4;
+  __shared__ float red[32][33];
+  const int cx = threadIdx.x & 7, slice = threadIdx.x >> 3;
+  const int64_t c = ((int64_t)blockIdx.x * 8 + cx) * 4;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (c < ld) {
-#pragma unroll 4
-    for (int i = slice; i < nwg; i += 16) {
+#pragma unroll 8
+    for (int i = slice; i < nwg; i += 32) {
       const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)i * ld + c);
       s.x += v.x;
       s.y += v.y;
@@ -267,55 +276,94 @@ __global__ __launch_bounds__(256) void dgamma_sum_kernel(const float* part, int6
       s.w += v.w;
     }
   }
-  red[slice][cx] = s;
+  red[slice][4 * cx] = s.x;
+  red[slice][4 * cx + 1] = s.y;
+  red[slice][4 * cx + 2] = s.z;
+  red[slice][4 * cx + 3] = s.w;
   __syncthreads();
-  if (slice == 0 && c < ld) {
-    for (int k = 1; k < 16; ++k) {
-      const float4 v = red[k][cx];
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
-    }
-    const float o[4] = {s.x, s.y, s.z, s.w};
-    for (int i = 0; i < 4; ++i)
-      if (c + i < cols) dgamma[c + i] = o[i];
+  const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
+  if (threadIdx.x < 32 && col < cols) {
+    float v = red[0][threadIdx.x];
+#pragma unroll
+    for (int k = 1; k < 32; ++k) v += red[k][threadIdx.x];
+    dgamma[col] = v;
   }
+}
+
+// ------------------------------------------------------------ statistics
+// The statistics of a forward launch from its workgroups' partials, in a
+// fixed order. 1024 threads and at most two partials each: the loads are in
+// flight together (2048 partials: 2.4 us, 4.8 with 256 threads in eight
+// rounds).
+__global__ __launch_bounds__(1024) void op_stats_kernel(const StatPart* part, int n, snip_stats* out) {
+  __shared__ double dred[32];
+  __shared__ uint32_t ured[32];
+  static_assert(kOpsWG <= 2 * 1024, "two partials a thread");
+  const StatPart none{0.0, 0.0, 0u, 0u};
+  const int i = threadIdx.x;
+  const StatPart a = i < n ? part[i] : none, b = i + 1024 < n ? part[i + 1024] : none;
+  const double e2 = wave_sum(a.e2 + b.e2), x2 = wave_sum(a.x2 + b.x2);
+  const uint32_t nf = wave_sum_u(a.nf + b.nf), am = wave_max_u(max(a.amax_bits, b.amax_bits));
+  const int wave = i >> 6;
+  if ((i & 63) == 0) {
+    dred[2 * wave] = e2;
+    dred[2 * wave + 1] = x2;
+    ured[2 * wave] = nf;
+    ured[2 * wave + 1] = am;
+  }
+  __syncthreads();
+  if (i == 0) {
+    snip_stats s{0.0, 0.0, 0.0f, 0u};
+    uint32_t m = 0u;
+    for (int w = 0; w < 16; ++w) {
+      s.sum_err2 += dred[2 * w];
+      s.sum_x2 += dred[2 * w + 1];
+      s.n_nonfinite += ured[2 * w];
+      m = max(m, ured[2 * w + 1]);
+    }
+    s.amax = __uint_as_float(m);
+    *out = s;
+  }
+}
+
+hipError_t launch_op_stats(const StatPart* part, int n, snip_stats* out, hipStream_t s) {
+  op_stats_kernel<<<dim3(1), dim3(1024), 0, s>>>(part, n, out);
+  return hipGetLastError();
 }
 
 // ------------------------------------------------------------ shapes
 namespace {
 struct NormShape {
-  int tpr, vpt;
+  bool wg;        // a row to a workgroup
+  int vpt, threads;
 };
 
-// One chunk a thread up to 2048 columns, two beyond: with four, the fp32
-// forms need 170 to 256 VGPRs and scratch.
-NormShape norm_shape(int64_t cols) {
+// A chunk a thread up to `one_up_to` chunks, two beyond. The forward pass
+// takes two from 4096 columns on (4096 x 8192 to FP8: 45 us, 54 with one and
+// 1024 threads); the backward pass, with its column sums, has no registers
+// for two in a workgroup of 1024 and takes them where it must (4096 x 8192:
+// 67 us with one, 93 with two).
+NormShape norm_shape(int64_t cols, int one_up_to) {
   const int64_t ch = ceil_div(cols, 8);
-  if (ch <= 64) return {64, 1};
-  if (ch <= 256) return {256, 1};
-  if (ch <= 512) return {256, 2};
-  if (ch <= 1024) return {512, 2};
-  return {1024, 2};
+  if (ch <= 64) return {false, 1, 256};
+  const int vpt = ch <= one_up_to ? 1 : 2;
+  return {true, vpt, (int)(64 * ceil_div(ch, 64 * vpt))};
 }
+NormShape fwd_shape(int64_t cols) { return norm_shape(cols, 512); }
+NormShape bwd_shape(int64_t cols) { return norm_shape(cols, 1024); }
 
-int norm_wg(int64_t rows, int64_t cols, int most) {
-  const NormShape s = norm_shape(cols);
-  const int64_t wg = ceil_div(rows, norm_threads(s.tpr) / s.tpr);
+int norm_wg(const NormShape& k, int64_t rows, int most) {
+  const int64_t wg = k.wg ? rows : ceil_div(rows, 4);
   return (int)(wg < most ? wg : most);
 }
 
-// f(shape constants) for the row's shape.
+// f(WG, VPT) as constants for the row's shape.
 template <class F>
-void with_shape(int64_t cols, F f) {
-  const NormShape k = norm_shape(cols);
-  using std::integral_constant;
-  if (k.tpr == 64) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-  if (k.vpt == 1) return f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-  if (k.tpr == 256) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-  if (k.tpr == 512) return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
-  return f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+void with_shape(const NormShape& k, F f) {
+  using one = std::integral_constant<int, 1>;
+  if (!k.wg) return f(std::false_type{}, one{});
+  if (k.vpt == 1) return f(std::true_type{}, one{});
+  return f(std::true_type{}, std::integral_constant<int, 2>{});
 }
 
 // f(F32) for a matrix's type; an absent one counts as bf16.
@@ -325,50 +373,62 @@ void with_type(const Mat& m, F f) {
   return f(std::false_type{});
 }
 
-template <int PASS>
+template <int PASS, bool SR>
 hipError_t norm_fwd_pass(const NormFwd& a, int nwg, hipStream_t s) {
-  with_shape(a.cols, [&](auto tpr, auto vpt) {
+  const NormShape k = fwd_shape(a.cols);
+  with_shape(k, [&](auto wg, auto vpt) {
     with_type(a.x, [&](auto xf) {
       with_type(a.res, [&](auto rf) {
-        constexpr int T = decltype(tpr)::value, V = decltype(vpt)::value;
-        rmsnorm_fwd_kernel<T, V, PASS, decltype(xf)::value, decltype(rf)::value>
-            <<<dim3(nwg), dim3(norm_threads(T)), 0, s>>>(a);
+        rmsnorm_fwd_kernel<decltype(wg)::value, decltype(vpt)::value, PASS, SR, decltype(xf)::value,
+                           decltype(rf)::value><<<dim3(nwg), dim3(k.threads), 0, s>>>(a);
       });
     });
   });
   return hipGetLastError();
 }
+template <int FMT>
+hipError_t norm_fwd_quant(const NormFwd& a, int nwg, hipStream_t s) {
+  return a.q.sr ? norm_fwd_pass<FMT, true>(a, nwg, s) : norm_fwd_pass<FMT, false>(a, nwg, s);
+}
 }  // namespace
 
-int norm_fwd_wg(int64_t rows, int64_t cols, bool amax) { return norm_wg(rows, cols, amax ? kOpsAmaxWG : kOpsWG); }
-int norm_bwd_wg(int64_t rows, int64_t cols) { return norm_wg(rows, cols, 512); }
+int norm_fwd_wg(int64_t rows, int64_t cols, bool amax) {
+  return norm_wg(fwd_shape(cols), rows, amax ? kOpsAmaxWG : kOpsWG);
+}
+// Each workgroup leaves a partial row of dgamma, to be written and read
+// again: as few as keep the card busy (1003 x 4104: 14 us with 256, 16 with
+// 512; 4096 x 2048: 24 and 20).
+int norm_bwd_wg(int64_t rows, int64_t cols) {
+  const NormShape k = bwd_shape(cols);
+  return norm_wg(k, rows, k.threads > 512 ? 256 : 512);
+}
 
 hipError_t launch_norm_fwd(int pass, const NormFwd& a, int nwg, hipStream_t s) {
   switch (pass) {
-    case kPassAmax: return norm_fwd_pass<kPassAmax>(a, nwg, s);
-    case SNIP_FP8_E4M3: return norm_fwd_pass<SNIP_FP8_E4M3>(a, nwg, s);
-    case SNIP_NVFP4: return norm_fwd_pass<SNIP_NVFP4>(a, nwg, s);
-    case SNIP_MXFP4: return norm_fwd_pass<SNIP_MXFP4>(a, nwg, s);
-    default: return norm_fwd_pass<SNIP_BF16>(a, nwg, s);
+    case kPassAmax: return norm_fwd_pass<kPassAmax, false>(a, nwg, s);
+    case SNIP_FP8_E4M3: return norm_fwd_quant<SNIP_FP8_E4M3>(a, nwg, s);
+    case SNIP_NVFP4: return norm_fwd_quant<SNIP_NVFP4>(a, nwg, s);
+    case SNIP_MXFP4: return norm_fwd_quant<SNIP_MXFP4>(a, nwg, s);
+    default: return norm_fwd_pass<SNIP_BF16, false>(a, nwg, s);
   }
 }
 
 hipError_t launch_norm_bwd(const NormBwd& a, float* dgamma, int nwg, hipStream_t s) {
-  with_shape(a.cols, [&](auto tpr, auto vpt) {
+  const NormShape k = bwd_shape(a.cols);
+  with_shape(k, [&](auto wg, auto vpt) {
     with_type(a.dy, [&](auto yf) {
       with_type(a.h, [&](auto hf) {
         with_type(a.dres, [&](auto rf) {
-          constexpr int T = decltype(tpr)::value, V = decltype(vpt)::value;
-          rmsnorm_bwd_kernel<T, V, decltype(yf)::value, decltype(hf)::value, decltype(rf)::value>
-              <<<dim3(nwg), dim3(norm_threads(T)), 0, s>>>(a);
+          rmsnorm_bwd_kernel<decltype(wg)::value, decltype(vpt)::value, decltype(yf)::value, decltype(hf)::value,
+                             decltype(rf)::value><<<dim3(nwg), dim3(k.threads), 0, s>>>(a);
         });
       });
     });
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !dgamma) return e;
-  dgamma_sum_kernel<<<dim3((unsigned)ceil_div(a.part_ld, 64)), dim3(256), 0, s>>>(a.part, a.part_ld, nwg, a.cols,
-                                                                                 dgamma);
+  dgamma_sum_kernel<<<dim3((unsigned)ceil_div(a.cols, 32)), dim3(256), 0, s>>>(a.part, a.part_ld, nwg, a.cols,
+                                                                              dgamma);
   return hipGetLastError();
 }
 

@@ -1,89 +1,123 @@
 // SwiGLU, y = gate * sigmoid(gate) * up, forward (with an optional output
 // quantized for the next GEMM) and backward, for gfx950.
 //
-// Elementwise scans bound by HBM. A thread takes chunks of 8 elements along
-// the flattened [rows][ceil(cols / 8)] grid of chunks, so that neighbouring
-// lanes hold neighbouring chunks of a row (the blocks of a quantized output
-// need that); it advances by the grid's stride in rows and chunks that the
-// host has divided once, and the next chunk's loads are issued before the
-// present one is worked on. sigmoid is 1 / (1 + exp(-g)) with the accurate
-// exp and division of fp32: they cost less than the chunk's bytes.
+// Elementwise scans, bound by HBM with the vector ALU not far behind. A
+// thread takes chunks of E elements along the flattened [rows][ceil(cols / E)]
+// grid of chunks, E being 16 bytes of gate (a wave's load is then one run of
+// 1 KB: with two loads of every other 16 bytes, reads past the caches lose a
+// fifth), so that neighbouring lanes hold neighbouring chunks of a
+// row (the blocks of a quantized output need that); it advances by the grid's
+// stride in rows and chunks that the host has divided once, and the next
+// chunk's loads are issued before the present one is worked on.
 #include "row_common.h"
 
 namespace snip {
 
-// A position in the grid of chunks.
-struct ChunkPos {
-  int64_t row, ch;
+// A thread's walk over the grid of chunks.
+struct Walk {
+  int64_t row, at;             // row, and index in the grid of chunks
+  int32_t ch;                  // chunk of the row
+  bool wrapped;                // the last step went past the end of a row
+
+  __device__ Walk(int32_t per_row) : at((int64_t)blockIdx.x * 256 + threadIdx.x), wrapped(false) {
+    row = at / per_row;
+    ch = (int32_t)(at % per_row);
+  }
+  __device__ void step(const GateStride& d, int32_t per_row) {
+    at += (int64_t)gridDim.x * 256;
+    row += d.rows;
+    ch += d.chunks;
+    wrapped = ch >= per_row;
+    if (wrapped) {
+      ch -= per_row;
+      ++row;
+    }
+  }
 };
 
-__device__ __forceinline__ ChunkPos first_chunk(int64_t per_row) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  return ChunkPos{i / per_row, i % per_row};
-}
-__device__ __forceinline__ ChunkPos next_chunk(const ChunkPos& p, int64_t drow, int64_t dchunk, int64_t per_row) {
-  ChunkPos n{p.row + drow, p.ch + dchunk};
-  if (n.ch >= per_row) {
-    n.ch -= per_row;
-    ++n.row;
-  }
-  return n;
-}
+// The element offset of the walk's chunk in one matrix, kept by additions.
+template <int E>
+struct Offset {
+  int64_t off, step, wrap;
+  __device__ Offset(const Mat& m, const Walk& w, const GateStride& d, int32_t per_row)
+      : off(w.row * m.ld + E * (int64_t)w.ch), step(d.rows * m.ld + E * (int64_t)d.chunks),
+        wrap(m.ld - E * (int64_t)per_row) {}
+  __device__ void follow(const Walk& w) { off += step + (w.wrapped ? wrap : 0); }
+};
 
-template <bool F32>
-__device__ __forceinline__ void load_chunk(const Mat& m, const ChunkPos& p, int64_t cols, Raw8<F32>& r) {
-  const int64_t off = p.row * m.ld + 8 * p.ch;
-  if (8 * p.ch + 8 <= cols)
-    load_whole(m.p, off, r);
+// `tail`: cols % E, the elements of a row's last chunk (0: a whole one).
+template <bool NT, bool F32, int E>
+__device__ __forceinline__ void load_chunk(const Mat& m, const Offset<E>& o, bool last, int tail, Raw<F32, E>& r) {
+  if (tail && last)
+    load_partial(m.p, o.off, tail, r);
   else
-    load_partial(m.p, off, (int)(cols - 8 * p.ch), r);
+    load_whole<NT>(m.p, o.off, r);
 }
-__device__ __forceinline__ void store_chunk(const Mat& m, const ChunkPos& p, int64_t cols, const float (&x)[8]) {
-  const int64_t off = p.row * m.ld + 8 * p.ch;
-  if (8 * p.ch + 8 <= cols)
-    store_whole(m.p, m.type == SNIPOP_F32, off, x);
+template <int E>
+__device__ __forceinline__ void store_chunk(const Mat& m, const Offset<E>& o, bool last, int tail,
+                                            const float (&x)[E]) {
+  if (tail && last)
+    store_partial(m.p, m.type == SNIPOP_F32, o.off, tail, x);
   else
-    store_partial(m.p, m.type == SNIPOP_F32, off, (int)(cols - 8 * p.ch), x);
+    store_whole(m.p, m.type == SNIPOP_F32, o.off, x);
 }
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+// 1 / (1 + exp(-g)) within 7 half-ulps (2 each of the hardware's exp2 and
+// reciprocal, 3 of the products and the sum): -g log2(e) in two parts, the
+// second one's share as a factor. Beyond +-150 exp2 is 0 or infinite, and the
+// sigmoid 1 or 0. The library's expf and division, 30 operations to 9, made
+// the forward pass ALU-bound (8192 x 11008 fp32 to FP8: 176 us).
+__device__ __forceinline__ float sigmoid(float g) {
+  const float t = __builtin_amdgcn_fmed3f(-g, -150.0f, 150.0f);
+  const float hi = t * 1.44269502f;
+  const float lo = fmaf(t, 1.92596303e-8f, fmaf(t, 1.44269502f, -hi));
+  const float e = __builtin_amdgcn_exp2f(hi) * fmaf(lo, 0.693147182f, 1.0f);
+  return __builtin_amdgcn_rcpf(1.0f + e);
+}
 
-template <int PASS, bool F32>
+template <int PASS, bool SR, bool F32, bool NT>
 __global__ __launch_bounds__(256) void swiglu_fwd_kernel(GateFwd A) {
   constexpr bool QUANT = PASS == SNIP_FP8_E4M3 || PASS == SNIP_NVFP4 || PASS == SNIP_MXFP4;
   __shared__ uint32_t ured[8];
   __shared__ double dred[8];
   __shared__ float inv_lut[PASS == SNIP_NVFP4 ? 128 : 1];
-  const int64_t per_row = (A.cols + 7) >> 3;
-  ChunkPos p = first_chunk(per_row);
-  Raw8<F32> rg = {}, ru = {};
-  auto load = [&](const ChunkPos& q) {
-    if (q.row < A.rows) {
-      load_chunk(A.gate, q, A.cols, rg);
-      load_chunk(A.up, q, A.cols, ru);
+  constexpr int E = F32 ? 4 : 8;
+  const int32_t per_row = (int32_t)((A.cols + E - 1) / E);
+  const int tail = (int)(A.cols % E);
+  Walk w(per_row);
+  Offset<E> og(A.gate, w, A.d, per_row), ou(A.up, w, A.d, per_row), oy(A.y, w, A.d, per_row);
+  Raw<F32, E> rg = {}, ru = {};
+  auto load = [&]() {
+    if (w.row < A.rows) {
+      load_chunk<NT>(A.gate, og, w.ch == per_row - 1, tail, rg);
+      load_chunk<NT>(A.up, ou, w.ch == per_row - 1, tail, ru);
     }
   };
-  load(p);
+  load();
   const int eS = QUANT ? op_tensor_exp<PASS>(A.q, ured) : 0;
   if constexpr (PASS == SNIP_NVFP4) fill_inv_lut(inv_lut);
   const bool stats = QUANT && A.q.part != nullptr;
   QAcc acc;
   uint32_t amax = 0u;
-  while (p.row < A.rows) {
-    float g[8], u[8];
+  while (w.row < A.rows) {
+    float g[E], u[E];
     raw_to_f32(rg, g);
     raw_to_f32(ru, u);
-    const ChunkPos n = next_chunk(p, A.drow, A.dchunk, per_row);
-    load(n);
+    const bool last = w.ch == per_row - 1;
+    const int64_t at = w.at;
+    w.step(A.d, per_row);
+    og.follow(w);
+    ou.follow(w);
+    load();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = g[i] * sigmoid(g[i]) * u[i];
+    for (int i = 0; i < E; ++i) g[i] = g[i] * sigmoid(g[i]) * u[i];
     if constexpr (PASS == kPassAmax) {
       amax = chunk_max_bits(g, amax);
     } else {
-      if (A.y.p) store_chunk(A.y, p, A.cols, g);
-      if constexpr (QUANT) quant_chunk<PASS>(A.q, eS, inv_lut, p.row * per_row + p.ch, g, stats, acc);
+      if (A.y.p) store_chunk(A.y, oy, last, tail, g);
+      oy.follow(w);
+      if constexpr (QUANT) quant_chunk<PASS, SR>(A.q, eS, inv_lut, at, g, stats, acc);
     }
-    p = n;
   }
   if constexpr (PASS == kPassAmax) {
     amax = wg_max_u(amax, ured);
@@ -98,86 +132,126 @@ __global__ __launch_bounds__(256) void swiglu_fwd_kernel(GateFwd A) {
 
 // dgate = dy u s (1 + g (1 - s)), dup = dy g s: every input once, both
 // outputs once.
-template <bool YF, bool F32>
+template <bool YF, bool F32, bool NT>
 __global__ __launch_bounds__(256) void swiglu_bwd_kernel(GateBwd A) {
-  const int64_t per_row = (A.cols + 7) >> 3;
-  ChunkPos p = first_chunk(per_row);
-  Raw8<YF> ry = {};
-  Raw8<F32> rg = {}, ru = {};
-  auto load = [&](const ChunkPos& q) {
-    if (q.row < A.rows) {
-      load_chunk(A.dy, q, A.cols, ry);
-      load_chunk(A.gate, q, A.cols, rg);
-      load_chunk(A.up, q, A.cols, ru);
+  constexpr int E = F32 ? 4 : 8;
+  const int32_t per_row = (int32_t)((A.cols + E - 1) / E);
+  const int tail = (int)(A.cols % E);
+  Walk w(per_row);
+  Offset<E> od(A.dy, w, A.d, per_row), og(A.gate, w, A.d, per_row), ou(A.up, w, A.d, per_row);
+  Offset<E> oa(A.dgate, w, A.d, per_row), ob(A.dup, w, A.d, per_row);
+  Raw<YF, E> ry = {};
+  Raw<F32, E> rg = {}, ru = {};
+  auto load = [&]() {
+    if (w.row < A.rows) {
+      const bool last = w.ch == per_row - 1;
+      load_chunk<NT>(A.dy, od, last, tail, ry);
+      load_chunk<NT>(A.gate, og, last, tail, rg);
+      load_chunk<NT>(A.up, ou, last, tail, ru);
     }
   };
-  load(p);
-  while (p.row < A.rows) {
-    float d[8], g[8], u[8];
+  load();
+  while (w.row < A.rows) {
+    float d[E], g[E], u[E];
     raw_to_f32(ry, d);
     raw_to_f32(rg, g);
     raw_to_f32(ru, u);
-    const ChunkPos n = next_chunk(p, A.drow, A.dchunk, per_row);
-    load(n);
+    const bool last = w.ch == per_row - 1;
+    w.step(A.d, per_row);
+    od.follow(w);
+    og.follow(w);
+    ou.follow(w);
+    load();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < E; ++i) {
       const float s = sigmoid(g[i]);
       const float gs = g[i] * s;
       u[i] = d[i] * u[i] * (s + gs * (1.0f - s));
       g[i] = d[i] * gs;
     }
-    if (A.dgate.p) store_chunk(A.dgate, p, A.cols, u);
-    if (A.dup.p) store_chunk(A.dup, p, A.cols, g);
-    p = n;
+    if (A.dgate.p) store_chunk(A.dgate, oa, last, tail, u);
+    if (A.dup.p) store_chunk(A.dup, ob, last, tail, g);
+    oa.follow(w);
+    ob.follow(w);
   }
 }
 
 namespace {
-int64_t chunks_per_row(int64_t cols) { return ceil_div(cols, 8); }
+int64_t chunks_per_row(const Mat& gate, int64_t cols) { return ceil_div(cols, gate.type == SNIPOP_F32 ? 4 : 8); }
 
-template <int PASS>
+GateStride stride_of(int nwg, const Mat& gate, int64_t cols) {
+  const int64_t stride = (int64_t)nwg * 256, per_row = chunks_per_row(gate, cols);
+  return GateStride{stride / per_row, (int32_t)(stride % per_row)};
+}
+
+// Inputs beyond the last-level cache (256 MB) are read past the caches:
+// 4096 x 5632 backward, 369 MB: 71 -> 68 us; smaller ones may still lie there
+// from the GEMM that wrote them.
+bool beyond_cache(int64_t rows, int64_t cols, int bytes) {
+  return (double)rows * (double)cols * bytes > 256.0 * 1024 * 1024;
+}
+
+int elem(const Mat& m) { return m.type == SNIPOP_F32 ? 4 : 2; }
+
+template <int PASS, bool SR>
 hipError_t gate_fwd_pass(const GateFwd& a, int nwg, hipStream_t s) {
-  if (a.gate.type == SNIPOP_F32)
-    swiglu_fwd_kernel<PASS, true><<<dim3(nwg), dim3(256), 0, s>>>(a);
-  else
-    swiglu_fwd_kernel<PASS, false><<<dim3(nwg), dim3(256), 0, s>>>(a);
+  const dim3 grid(nwg), block(256);
+  const bool nt = beyond_cache(a.rows, a.cols, 2 * elem(a.gate));
+  if (a.gate.type == SNIPOP_F32) {
+    if (nt)
+      swiglu_fwd_kernel<PASS, SR, true, true><<<grid, block, 0, s>>>(a);
+    else
+      swiglu_fwd_kernel<PASS, SR, true, false><<<grid, block, 0, s>>>(a);
+  } else {
+    if (nt)
+      swiglu_fwd_kernel<PASS, SR, false, true><<<grid, block, 0, s>>>(a);
+    else
+      swiglu_fwd_kernel<PASS, SR, false, false><<<grid, block, 0, s>>>(a);
+  }
   return hipGetLastError();
+}
+template <int FMT>
+hipError_t gate_fwd_quant(const GateFwd& a, int nwg, hipStream_t s) {
+  return a.q.sr ? gate_fwd_pass<FMT, true>(a, nwg, s) : gate_fwd_pass<FMT, false>(a, nwg, s);
+}
+
+template <bool NT>
+void gate_bwd_pass(const GateBwd& a, int nwg, hipStream_t s) {
+  const dim3 grid(nwg), block(256);
+  const bool yf = a.dy.type == SNIPOP_F32, f = a.gate.type == SNIPOP_F32;
+  if (yf && f)
+    swiglu_bwd_kernel<true, true, NT><<<grid, block, 0, s>>>(a);
+  else if (yf)
+    swiglu_bwd_kernel<true, false, NT><<<grid, block, 0, s>>>(a);
+  else if (f)
+    swiglu_bwd_kernel<false, true, NT><<<grid, block, 0, s>>>(a);
+  else
+    swiglu_bwd_kernel<false, false, NT><<<grid, block, 0, s>>>(a);
 }
 }  // namespace
 
-int gate_wg(int64_t rows, int64_t cols, bool amax) {
-  const int64_t wg = ceil_div(rows * chunks_per_row(cols), 256);
-  const int most = amax ? kOpsAmaxWG : kOpsWG;
+int gate_wg(const Mat& gate, int64_t rows, int64_t cols, int most) {
+  const int64_t wg = ceil_div(rows * chunks_per_row(gate, cols), 256);
   return (int)(wg < most ? wg : most);
 }
 
 hipError_t launch_gate_fwd(int pass, GateFwd a, int nwg, hipStream_t s) {
-  const int64_t stride = (int64_t)nwg * 256, per_row = chunks_per_row(a.cols);
-  a.drow = stride / per_row;
-  a.dchunk = stride % per_row;
+  a.d = stride_of(nwg, a.gate, a.cols);
   switch (pass) {
-    case kPassAmax: return gate_fwd_pass<kPassAmax>(a, nwg, s);
-    case SNIP_FP8_E4M3: return gate_fwd_pass<SNIP_FP8_E4M3>(a, nwg, s);
-    case SNIP_NVFP4: return gate_fwd_pass<SNIP_NVFP4>(a, nwg, s);
-    case SNIP_MXFP4: return gate_fwd_pass<SNIP_MXFP4>(a, nwg, s);
-    default: return gate_fwd_pass<SNIP_BF16>(a, nwg, s);
+    case kPassAmax: return gate_fwd_pass<kPassAmax, false>(a, nwg, s);
+    case SNIP_FP8_E4M3: return gate_fwd_quant<SNIP_FP8_E4M3>(a, nwg, s);
+    case SNIP_NVFP4: return gate_fwd_quant<SNIP_NVFP4>(a, nwg, s);
+    case SNIP_MXFP4: return gate_fwd_quant<SNIP_MXFP4>(a, nwg, s);
+    default: return gate_fwd_pass<SNIP_BF16, false>(a, nwg, s);
   }
 }
 
 hipError_t launch_gate_bwd(GateBwd a, int nwg, hipStream_t s) {
-  const int64_t stride = (int64_t)nwg * 256, per_row = chunks_per_row(a.cols);
-  a.drow = stride / per_row;
-  a.dchunk = stride % per_row;
-  const dim3 grid(nwg), block(256);
-  const bool yf = a.dy.type == SNIPOP_F32, f = a.gate.type == SNIPOP_F32;
-  if (yf && f)
-    swiglu_bwd_kernel<true, true><<<grid, block, 0, s>>>(a);
-  else if (yf)
-    swiglu_bwd_kernel<true, false><<<grid, block, 0, s>>>(a);
-  else if (f)
-    swiglu_bwd_kernel<false, true><<<grid, block, 0, s>>>(a);
+  a.d = stride_of(nwg, a.gate, a.cols);
+  if (beyond_cache(a.rows, a.cols, 2 * elem(a.gate) + elem(a.dy)))
+    gate_bwd_pass<true>(a, nwg, s);
   else
-    swiglu_bwd_kernel<false, false><<<grid, block, 0, s>>>(a);
+    gate_bwd_pass<false>(a, nwg, s);
   return hipGetLastError();
 }
 
