@@ -1,0 +1,123 @@
+"""The MLP half of a Llama-like block out of the library's calls: RMS norm with
+the residual's addition, Gate and Up as one quantized linear layer, SwiGLU,
+Down -- a training step over a batch, and a decode step of a few tokens.
+
+[SNIP, Fig. 4]: the block's linear layers; between them stand the operators
+of include/snip_ops.h.
+
+  python -m sub_byte_mixed_amd.mlp [--workload tinyllama1b] [--fmt nvfp4] [--reps 20]
+
+times both steps on random weights of a workload's shapes.
+"""
+from __future__ import annotations
+
+import argparse
+import os
+import sys
+
+import torch
+
+import sub_byte_mixed_amd as S
+
+
+class GatedMLP:
+    """w_gate_up bf16 [2 * ffn, hidden] (Gate's rows, then Up's), w_down bf16
+    [hidden, ffn], gamma [hidden]. All three GEMMs of a linear layer run in
+    `fmt`. hidden and ffn are multiples of 128."""
+
+    def __init__(self, gamma: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, fmt: int = S.NVFP4,
+                 eps: float = 1e-5, layer_id: int = 0):
+        hidden, ffn = w_down.shape
+        if w_gate_up.shape != (2 * ffn, hidden) or gamma.shape != (hidden,):
+            raise ValueError(f"w_gate_up must be [{2 * ffn}, {hidden}] and gamma [{hidden}] for w_down [{hidden}, {ffn}]")
+        self.gamma, self.w_gate_up, self.w_down = gamma, w_gate_up, w_down
+        self.fmt, self.eps, self.ffn = fmt, eps, ffn
+        self.ids = (2 * layer_id, 2 * layer_id + 1)     # random-stream namespaces of the two layers
+
+    # ---- training
+    def forward(self, x: torch.Tensor, res: torch.Tensor, seed: int = 0):
+        """x: what joins the residual stream res, both [T, hidden], T a
+        multiple of 128. Returns (output fp32, the new stream bf16, what
+        backward needs)."""
+        y, h, rstd, _, _ = S.rmsnorm_fwd(x, self.gamma, self.eps, res=res)
+        gu, saved_gu, _ = S.linear_fwd_save(y, self.w_gate_up, self.fmt, seed, self.ids[0])
+        a, _, _ = S.swiglu_fwd(gu[:, :self.ffn], gu[:, self.ffn:])
+        out, saved_down, _ = S.linear_fwd_save(a, self.w_down, self.fmt, seed, self.ids[1])
+        return out, h, (h, rstd, gu, saved_gu, saved_down, seed)
+
+    def backward(self, dout: torch.Tensor, dh: torch.Tensor, saved):
+        """dout bf16: the gradient of the output; dh: that of the new stream.
+        Returns (the gradient of x and of res in bf16, dgamma, dw_gate_up,
+        dw_down in fp32)."""
+        h, rstd, gu, saved_gu, saved_down, seed = saved
+        da, dw_down, _ = S.linear_bwd_saved(dout, saved_down, seed, self.ids[1])
+        dgu = torch.empty(gu.shape, dtype=torch.bfloat16, device=gu.device)
+        S.swiglu_bwd(da, gu[:, :self.ffn], gu[:, self.ffn:], dgate=dgu[:, :self.ffn], dup=dgu[:, self.ffn:])
+        dy, dw_gate_up, _ = S.linear_bwd_saved(dgu, saved_gu, seed, self.ids[0])
+        dx, dgamma = S.rmsnorm_bwd(dy, h, self.gamma, rstd, dres=dh)
+        return dx, dgamma, dw_gate_up, dw_down
+
+    # ---- decode
+    def quantize_weights(self) -> None:
+        """The weights as decode reads them, once per set of weights."""
+        self.q_gate_up, _ = S.quantize(self.w_gate_up, S.ROWWISE, self.fmt, with_stats=False)
+        self.q_down, _ = S.quantize(self.w_down, S.ROWWISE, self.fmt, with_stats=False)
+
+    def decode(self, x: torch.Tensor, res: torch.Tensor) -> torch.Tensor:
+        """1 to 16 tokens: res [m, hidden] becomes the new stream; returns the
+        output [m, hidden] in fp32."""
+        y, _, _, _, _ = S.rmsnorm_fwd(x, self.gamma, self.eps, res=res, h=res, with_rstd=False)
+        gu = S.qgemv(y, self.q_gate_up)
+        a, _, _ = S.swiglu_fwd(gu[:, :self.ffn], gu[:, self.ffn:])
+        return S.qgemv(a, self.q_down)
+
+
+def _time(fn, reps: int) -> float:
+    fn()
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    for _ in range(reps):
+        fn()
+    b.record()
+    b.synchronize()
+    return a.elapsed_time(b) * 1e3 / reps
+
+
+def main(argv=None) -> None:
+    sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    import synth
+    ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
+    ap.add_argument("--workload", default="tinyllama1b", choices=[w for w in synth.WORKLOAD_ORDER if len(synth.WORKLOADS[w].layers) == 7])
+    ap.add_argument("--fmt", default="nvfp4", choices=[S.FORMAT_NAMES[f] for f in (S.FP8, S.NVFP4, S.MXFP4)])
+    ap.add_argument("--reps", type=int, default=20)
+    args = ap.parse_args(argv)
+    wl = synth.WORKLOADS[args.workload]
+    fmt = {v: k for k, v in S.FORMAT_NAMES.items()}[args.fmt]
+    T, hidden, ffn = wl.tokens, wl.layer("Gate").d_in, wl.layer("Gate").d_out
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+
+    def randn(*shape, scale=1.0):
+        return (scale * torch.randn(shape, generator=g, device="cuda")).to(torch.bfloat16)
+
+    mlp = GatedMLP(1.0 + randn(hidden, scale=0.1), randn(2 * ffn, hidden, scale=0.02), randn(hidden, ffn, scale=0.02), fmt)
+    x, res, dout, dh = randn(T, hidden), randn(T, hidden), randn(T, hidden, scale=1e-3), randn(T, hidden, scale=1e-3)
+
+    def train():
+        _, _, saved = mlp.forward(x, res)
+        mlp.backward(dout, dh, saved)
+    print(f"{wl.name} MLP, {args.fmt}: training step of {T} tokens {_time(train, args.reps):.0f} us", flush=True)
+    mlp.quantize_weights()
+    for m in (1, 4, 16):
+        xd, rd = x[:m].clone(), res[:m].clone()
+        mlp.decode(xd, rd)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            mlp.decode(xd, rd)
+        print(f"{wl.name} MLP, {args.fmt}: decode step of {m} tokens {_time(lambda: mlp.decode(xd, rd), args.reps):.1f} us, "
+              f"as a graph {_time(graph.replay, args.reps):.1f} us", flush=True)
+
+
+if __name__ == "__main__":
+    main()
