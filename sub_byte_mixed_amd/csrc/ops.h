@@ -7,14 +7,13 @@
 
 namespace snip {
 
-constexpr int kOpsAmaxWG = 1024;   // max workgroups of a pass for the maximum
-constexpr int kOpsWG = 2048;       // max workgroups of a pass with statistics
-// SwiGLU: workgroups that come and go spread better than a few that walk far
-// (4096 x 5632 backward: 60 us with 32768, 67 with 1024), but each leaves a
-// partial of the statistics (8192 x 11008 to FP8: 144 us with 1024).
+// Most workgroups of a pass that leaves a partial each: the maximum's, and the
+// statistics' (norm 4096 x 2048 to FP8: 18.0 us with 1024, 18.3 with 2048, and
+// the launch that sums the partials is the shorter for it).
+constexpr int kOpsWG = 1024;
+// SwiGLU without statistics: workgroups that come and go spread better than a
+// few that walk far (4096 x 5632 backward: 60 us with 32768, 67 with 1024).
 constexpr int kGateWG = 32768;
-constexpr int kGateStatsWG = 1024;
-static_assert(kGateStatsWG <= kOpsWG, "the workspace holds kOpsWG partials");
 
 // A matrix argument: rows of `ld` elements of `type` (SNIPOP_BF16 / _F32).
 struct Mat {
@@ -92,7 +91,7 @@ struct Gemv {
 constexpr int kPassAmax = -1;
 
 // Grids, and asynchronous launchers that return the launch's hipError_t.
-int norm_fwd_wg(int64_t rows, int64_t cols, bool amax);
+int norm_fwd_wg(int64_t rows, int64_t cols);
 int norm_bwd_wg(int64_t rows, int64_t cols);
 int gate_wg(const Mat& gate, int64_t rows, int64_t cols, int most);
 hipError_t launch_norm_fwd(int pass, const NormFwd& a, int nwg, hipStream_t s);

@@ -17,7 +17,7 @@ constexpr int64_t kMaxGateCols = (int64_t)1 << 31;   // a row's chunks are count
 
 // Scratch of a quantized output: partials of the pass for the maximum, and
 // of the statistics.
-constexpr size_t kOpsAmaxBytes = align_up(kOpsAmaxWG * sizeof(uint32_t), kAlign);
+constexpr size_t kOpsAmaxBytes = align_up(kOpsWG * sizeof(uint32_t), kAlign);
 constexpr size_t kOpsQuantWS = kOpsAmaxBytes + align_up(kOpsWG * sizeof(StatPart), kAlign);
 
 bool out_format(int f) { return f == SNIP_FP8_E4M3 || f == SNIP_NVFP4 || f == SNIP_MXFP4; }
@@ -157,13 +157,13 @@ int snipop_rmsnorm_fwd(const void* x, int x_type, int64_t ldx, const void* res, 
   const double work = (double)rows * (double)cols;
   if (amax) {
     a.amax_out = amax;
-    a.q.n_amax_part = norm_fwd_wg(rows, cols, true);
+    a.q.n_amax_part = norm_fwd_wg(rows, cols);
     const int slot = timing_begin(LaunchTag{SNIP_LAUNCH_AMAX, -1, -1, -1, work}, s);
     const hipError_t e = launch_norm_fwd(kPassAmax, a, a.q.n_amax_part, s);
     timing_end(slot, s);
     if ((rc = hip_check(e, "norm amax launch"))) return rc;
   }
-  const int nwg = norm_fwd_wg(rows, cols, false);
+  const int nwg = norm_fwd_wg(rows, cols);
   const int slot = timing_begin(op_tag(SNIPOP_LAUNCH_NORM, out, rounding, work), s);
   const hipError_t e = launch_norm_fwd(out ? out->format : SNIP_BF16, a, nwg, s);
   timing_end(slot, s);
@@ -229,13 +229,13 @@ int snipop_swiglu_fwd(const void* gate, int64_t ldg, const void* up, int64_t ldu
   const double work = (double)rows * (double)cols;
   if (amax) {
     a.amax_out = amax;
-    a.q.n_amax_part = gate_wg(a.gate, rows, cols, kOpsAmaxWG);
+    a.q.n_amax_part = gate_wg(a.gate, rows, cols, kOpsWG);
     const int slot = timing_begin(LaunchTag{SNIP_LAUNCH_AMAX, -1, -1, -1, work}, s);
     const hipError_t e = launch_gate_fwd(kPassAmax, a, a.q.n_amax_part, s);
     timing_end(slot, s);
     if ((rc = hip_check(e, "swiglu amax launch"))) return rc;
   }
-  const int nwg = gate_wg(a.gate, rows, cols, stats ? kGateStatsWG : kGateWG);
+  const int nwg = gate_wg(a.gate, rows, cols, stats ? kOpsWG : kGateWG);
   const int slot = timing_begin(op_tag(SNIPOP_LAUNCH_GATE, out, rounding, work), s);
   const hipError_t e = launch_gate_fwd(out ? out->format : SNIP_BF16, a, nwg, s);
   timing_end(slot, s);

@@ -291,19 +291,16 @@ __global__ __launch_bounds__(256) void dgamma_sum_kernel(const float* part, int6
 }
 
 // ------------------------------------------------------------ statistics
-// The statistics of a forward launch from its workgroups' partials, in a
-// fixed order. 1024 threads and at most two partials each: the loads are in
-// flight together (2048 partials: 2.4 us, 4.8 with 256 threads in eight
-// rounds).
+// The statistics of a forward launch from its workgroups' partials, one a
+// thread, in a fixed order.
 __global__ __launch_bounds__(1024) void op_stats_kernel(const StatPart* part, int n, snip_stats* out) {
   __shared__ double dred[32];
   __shared__ uint32_t ured[32];
-  static_assert(kOpsWG <= 2 * 1024, "two partials a thread");
-  const StatPart none{0.0, 0.0, 0u, 0u};
+  static_assert(kOpsWG <= 1024, "one partial a thread");
   const int i = threadIdx.x;
-  const StatPart a = i < n ? part[i] : none, b = i + 1024 < n ? part[i + 1024] : none;
-  const double e2 = wave_sum(a.e2 + b.e2), x2 = wave_sum(a.x2 + b.x2);
-  const uint32_t nf = wave_sum_u(a.nf + b.nf), am = wave_max_u(max(a.amax_bits, b.amax_bits));
+  const StatPart p = i < n ? part[i] : StatPart{0.0, 0.0, 0u, 0u};
+  const double e2 = wave_sum(p.e2), x2 = wave_sum(p.x2);
+  const uint32_t nf = wave_sum_u(p.nf), am = wave_max_u(p.amax_bits);
   const int wave = i >> 6;
   if ((i & 63) == 0) {
     dred[2 * wave] = e2;
@@ -392,9 +389,7 @@ hipError_t norm_fwd_quant(const NormFwd& a, int nwg, hipStream_t s) {
 }
 }  // namespace
 
-int norm_fwd_wg(int64_t rows, int64_t cols, bool amax) {
-  return norm_wg(fwd_shape(cols), rows, amax ? kOpsAmaxWG : kOpsWG);
-}
+int norm_fwd_wg(int64_t rows, int64_t cols) { return norm_wg(fwd_shape(cols), rows, kOpsWG); }
 // Each workgroup leaves a partial row of dgamma, to be written and read
 // again: as few as keep the card busy (1003 x 4104: 14 us with 256, 16 with
 // 512; 4096 x 2048: 24 and 20).
