@@ -233,7 +233,7 @@ class QuantizedTensor:
         L = lib()
         self.format, self.rows, self.k = fmt, rows, k
         nc = L.snip_qtensor_bytes(fmt, rows, k, 0)
-        ns = L.snip_qtensor_bytes(fmt, rows, k, 1)
+        ns = 0 if scales is not None else L.snip_qtensor_bytes(fmt, rows, k, 1)
         if nc < 0:
             raise SnipError(-2, f"invalid quantized tensor shape [{rows}][{k}] for format {fmt}")
         self.codes = codes if codes is not None else torch.empty(nc, dtype=torch.uint8, device=device)

@@ -11,8 +11,9 @@ using namespace snip;
 
 namespace {
 
-// Rows and leading dimensions beyond this would overflow 64-bit offsets.
+// Rows, leading dimensions and elements of a matrix: 64-bit byte offsets.
 constexpr int64_t kMaxDim = (int64_t)1 << 40;
+constexpr double kMaxElems = 1152921504606846976.0;   // 2^60
 constexpr int64_t kMaxGateCols = (int64_t)1 << 31;   // a row's chunks are counted in 32 bits
 
 // Scratch of a quantized output: partials of the pass for the maximum, and
@@ -29,7 +30,8 @@ int check_type(const char* who, const char* name, int type) {
 }
 
 // A matrix argument that may be absent (p NULL), into `m`.
-int check_mat(const char* who, const char* name, const void* p, int type, int64_t ld, int64_t cols, Mat* m) {
+int check_mat(const char* who, const char* name, const void* p, int type, int64_t ld, int64_t rows, int64_t cols,
+              Mat* m) {
   *m = Mat{nullptr, 0, SNIPOP_BF16};
   if (!p) return SNIP_OK;
   int rc = check_type(who, name, type);
@@ -37,6 +39,9 @@ int check_mat(const char* who, const char* name, const void* p, int type, int64_
   if (ld < cols || ld > kMaxDim || ld % (type == SNIPOP_F32 ? 4 : 8))
     return fail(SNIP_E_SHAPE, "%s: %s: leading dimension %lld must be >= %lld and a multiple of %d", who, name,
                 (long long)ld, (long long)cols, type == SNIPOP_F32 ? 4 : 8);
+  if ((double)rows * (double)ld > kMaxElems)
+    return fail(SNIP_E_SHAPE, "%s: %s: %lld rows of %lld elements are too many", who, name, (long long)rows,
+                (long long)ld);
   if (!aligned(p, 16)) return fail(SNIP_E_ALIGN, "%s: %s is not 16-byte aligned", who, name);
   *m = Mat{const_cast<void*>(p), ld, type};
   return SNIP_OK;
@@ -47,9 +52,6 @@ int check_shape(const char* who, int64_t rows, int64_t cols, int64_t max_cols) {
     return fail(SNIP_E_SHAPE, "%s: rows=%lld cols=%lld must be > 0", who, (long long)rows, (long long)cols);
   if (cols > max_cols)
     return fail(SNIP_E_SHAPE, "%s: cols=%lld above the limit of %lld", who, (long long)cols, (long long)max_cols);
-  // rows * ld <= 2^60: every byte offset fits
-  if ((double)rows * (double)cols > 1152921504606846976.0)
-    return fail(SNIP_E_SHAPE, "%s: %lld x %lld elements are too many", who, (long long)rows, (long long)cols);
   return SNIP_OK;
 }
 
@@ -138,10 +140,10 @@ int snipop_rmsnorm_fwd(const void* x, int x_type, int64_t ldx, const void* res, 
   if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(SNIP_E_SHAPE, "%s: eps must be finite and >= 0", who);
   NormFwd a;
   std::memset(&a, 0, sizeof(a));
-  if ((rc = check_mat(who, "x", x, x_type, ldx, cols, &a.x))) return rc;
-  if ((rc = check_mat(who, "res", res, res_type, ldr, cols, &a.res))) return rc;
-  if ((rc = check_mat(who, "h", h, h_type, ldh, cols, &a.h))) return rc;
-  if ((rc = check_mat(who, "y", y, y_type, ldy, cols, &a.y))) return rc;
+  if ((rc = check_mat(who, "x", x, x_type, ldx, rows, cols, &a.x))) return rc;
+  if ((rc = check_mat(who, "res", res, res_type, ldr, rows, cols, &a.res))) return rc;
+  if ((rc = check_mat(who, "h", h, h_type, ldh, rows, cols, &a.h))) return rc;
+  if ((rc = check_mat(who, "y", y, y_type, ldy, rows, cols, &a.y))) return rc;
   if ((rc = check_type(who, "gamma", gamma_type))) return rc;
   if (!aligned(gamma, 16) || !aligned(rstd, 4)) return fail(SNIP_E_ALIGN, "%s: misaligned pointer", who);
   a.gamma = Mat{const_cast<void*>(gamma), 0, gamma_type};
@@ -183,10 +185,10 @@ int snipop_rmsnorm_bwd(const void* dy, int dy_type, int64_t lddy, const void* h,
   if (rc) return rc;
   NormBwd a;
   std::memset(&a, 0, sizeof(a));
-  if ((rc = check_mat(who, "dy", dy, dy_type, lddy, cols, &a.dy))) return rc;
-  if ((rc = check_mat(who, "h", h, h_type, ldh, cols, &a.h))) return rc;
-  if ((rc = check_mat(who, "dres", dres, dres_type, lddres, cols, &a.dres))) return rc;
-  if ((rc = check_mat(who, "dx", dx, dx_type, lddx, cols, &a.dx))) return rc;
+  if ((rc = check_mat(who, "dy", dy, dy_type, lddy, rows, cols, &a.dy))) return rc;
+  if ((rc = check_mat(who, "h", h, h_type, ldh, rows, cols, &a.h))) return rc;
+  if ((rc = check_mat(who, "dres", dres, dres_type, lddres, rows, cols, &a.dres))) return rc;
+  if ((rc = check_mat(who, "dx", dx, dx_type, lddx, rows, cols, &a.dx))) return rc;
   if ((rc = check_type(who, "gamma", gamma_type))) return rc;
   if (!aligned(gamma, 16) || !aligned(rstd, 4) || !aligned(dgamma, 4) || !aligned(ws, 16))
     return fail(SNIP_E_ALIGN, "%s: misaligned pointer", who);
@@ -217,9 +219,9 @@ int snipop_swiglu_fwd(const void* gate, int64_t ldg, const void* up, int64_t ldu
   if (rc) return rc;
   GateFwd a;
   std::memset(&a, 0, sizeof(a));
-  if ((rc = check_mat(who, "gate", gate, type, ldg, cols, &a.gate))) return rc;
-  if ((rc = check_mat(who, "up", up, type, ldu, cols, &a.up))) return rc;
-  if ((rc = check_mat(who, "y", y, y_type, ldy, cols, &a.y))) return rc;
+  if ((rc = check_mat(who, "gate", gate, type, ldg, rows, cols, &a.gate))) return rc;
+  if ((rc = check_mat(who, "up", up, type, ldu, rows, cols, &a.up))) return rc;
+  if ((rc = check_mat(who, "y", y, y_type, ldy, rows, cols, &a.y))) return rc;
   uint32_t* amax;
   if ((rc = check_out(who, out, rows, cols, rounding, seed, tensor_id, amax_in, stats, ws, ws_bytes, &a.q, &amax)))
     return rc;
@@ -254,11 +256,11 @@ int snipop_swiglu_bwd(const void* dy, int dy_type, int64_t lddy, const void* gat
   if (rc) return rc;
   GateBwd a;
   std::memset(&a, 0, sizeof(a));
-  if ((rc = check_mat(who, "dy", dy, dy_type, lddy, cols, &a.dy))) return rc;
-  if ((rc = check_mat(who, "gate", gate, type, ldg, cols, &a.gate))) return rc;
-  if ((rc = check_mat(who, "up", up, type, ldu, cols, &a.up))) return rc;
-  if ((rc = check_mat(who, "dgate", dgate, d_type, lddg, cols, &a.dgate))) return rc;
-  if ((rc = check_mat(who, "dup", dup, d_type, lddu, cols, &a.dup))) return rc;
+  if ((rc = check_mat(who, "dy", dy, dy_type, lddy, rows, cols, &a.dy))) return rc;
+  if ((rc = check_mat(who, "gate", gate, type, ldg, rows, cols, &a.gate))) return rc;
+  if ((rc = check_mat(who, "up", up, type, ldu, rows, cols, &a.up))) return rc;
+  if ((rc = check_mat(who, "dgate", dgate, d_type, lddg, rows, cols, &a.dgate))) return rc;
+  if ((rc = check_mat(who, "dup", dup, d_type, lddu, rows, cols, &a.dup))) return rc;
   a.rows = rows;
   a.cols = cols;
   hipStream_t s = static_cast<hipStream_t>(stream);

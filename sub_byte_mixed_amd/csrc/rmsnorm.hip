@@ -41,8 +41,13 @@ __device__ __forceinline__ void load_row(const void* p, int64_t off, int t, int 
     Raw<F32> last;
     load_partial(p, off + 8 * nch, cols & 7, last);
 #pragma unroll
-    for (int v = 0; v < VPT; ++v)
-      if (v == nch / tpr) r[v] = last;
+    for (int k = 0; k < Raw<F32>::NV; ++k) {
+      // a value from here on: the compiler would choose among the chunks'
+      // addresses, and keep them in scratch for it (twice the time)
+      asm("" : "+v"(last.w[k]));
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) r[v].w[k] = v == nch / tpr ? last.w[k] : r[v].w[k];
+    }
   }
 }
 
@@ -205,7 +210,11 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void rmsnorm_bwd_kernel(NormBwd A)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dg[v][i] = 0.0f;
 
+  // the next row's loads run while this one is worked on, where the registers
+  // suffice for both (two chunks a thread of 1024 spill)
+  constexpr bool AHEAD = VPT == 1;
   for (int it = 0; row < A.rows; ++it, row += step) {
+    if (!AHEAD && it > 0) load(row);
     float d[VPT][8], xh[VPT][8], res[VPT][8];
     const float r = rs;
     float dot = 0.0f;
@@ -222,7 +231,7 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void rmsnorm_bwd_kernel(NormBwd A)
         dot = fmaf(d[v][i], xh[v][i], dot);
       }
     }
-    load(row + step);
+    if (AHEAD) load(row + step);
     const float mean = row_sum<WG>(dot, red, it & 1) / (float)A.cols;
     if (A.dx.p) {
 #pragma unroll
@@ -336,10 +345,10 @@ struct NormShape {
 };
 
 // A chunk a thread up to `one_up_to` chunks, two beyond. The forward pass
-// takes two from 4096 columns on (4096 x 8192 to FP8: 45 us, 54 with one and
-// 1024 threads); the backward pass, with its column sums, has no registers
-// for two in a workgroup of 1024 and takes them where it must (4096 x 8192:
-// 67 us with one, 93 with two).
+// takes two from 4096 columns on (4096 x 8192 bf16 to FP8: 44.7 us, 45.8 with
+// one and 1024 threads); the backward pass, with its column sums, is short of
+// registers then and takes two where it must (4096 x 8192: 67 us with one, 93
+// with two).
 NormShape norm_shape(int64_t cols, int one_up_to) {
   const int64_t ch = ceil_div(cols, 8);
   if (ch <= 64) return {false, 1, 256};
@@ -350,8 +359,8 @@ NormShape fwd_shape(int64_t cols) { return norm_shape(cols, 512); }
 NormShape bwd_shape(int64_t cols) { return norm_shape(cols, 1024); }
 
 int norm_wg(const NormShape& k, int64_t rows, int most) {
-  const int64_t wg = k.wg ? rows : ceil_div(rows, 4);
-  return (int)(wg < most ? wg : most);
+  const int64_t n = k.wg ? rows : ceil_div(rows, 4);
+  return (int)(n < most ? n : most);
 }
 
 // f(WG, VPT) as constants for the row's shape.
@@ -389,7 +398,16 @@ hipError_t norm_fwd_quant(const NormFwd& a, int nwg, hipStream_t s) {
 }
 }  // namespace
 
-int norm_fwd_wg(int64_t rows, int64_t cols) { return norm_wg(fwd_shape(cols), rows, kOpsWG); }
+// As many workgroups as are resident, 16 waves on each of the 256 CUs: a row's
+// loads then run while the row before is worked on (4096 x 4096: 32.6 us with
+// 512 workgroups of 8 waves, 34.4 with 1024; 4096 x 2048: 18.0 us with 1024 of
+// 4 waves, 21.2 with 512).
+int norm_fwd_wg(int64_t rows, int64_t cols) {
+  const NormShape k = fwd_shape(cols);
+  const int per_cu = 1024 / k.threads;
+  static_assert(256 * 4 <= kOpsWG, "threads are 256 or more a workgroup, or rows are few");
+  return norm_wg(k, rows, 256 * (per_cu < 1 ? 1 : per_cu > 4 ? 4 : per_cu));
+}
 // Each workgroup leaves a partial row of dgamma, to be written and read
 // again: as few as keep the card busy (1003 x 4104: 14 us with 256, 16 with
 // 512; 4096 x 2048: 24 and 20).

@@ -17,7 +17,6 @@ stream= (default: the current one of the tensors' device).
 from __future__ import annotations
 
 import ctypes
-import functools
 from typing import Optional, Tuple
 
 import torch
@@ -80,16 +79,23 @@ def _new(rows: int, cols: int, dtype, dev: int) -> torch.Tensor:
     return t if pad == cols else t[:, :cols]
 
 
+# (codes, scales) of a quantized format in bytes, as multiples of 1/32 byte an element
+_SIZES = {f: (16, 32 // blk * (2 if kind == "bf16" else 1)) for f, (blk, kind) in _S.FP4_LAYOUT.items()}
+_SIZES.update({_S.FP8: (32, 0), _S.BF16: (64, 0)})
+
+
+def _holds(t: Optional[torch.Tensor], size: int, dev: int) -> bool:
+    return t is not None and t.get_device() == dev and t.nbytes >= size and t.is_contiguous()
+
+
 def _operand(q: "_S.QuantizedTensor", name: str, dev: int):
     """Reference to a quantized operand's descriptor, once its buffers are known to hold it."""
-    blk, kind = _S.FP4_LAYOUT.get(q.format, (0, ""))
+    codes, scales = _SIZES.get(q.format, (64, 0))
     n = q.rows * q.k
-    need = ((q.codes, n // 2 if blk else n if q.format == _S.FP8 else 2 * n),
-            (q.scales, 0 if not blk else n // blk * (2 if kind == "bf16" else 1)), (q.texp, 4))
-    for t, size in need:
-        if size and (t is None or t.get_device() != dev or t.nbytes < size or not t.is_contiguous()):
-            raise ValueError(f"{name}: codes, scales and texp must be contiguous on GPU {dev} and hold "
-                             f"[{q.rows}][{q.k}] in format {q.format}")
+    if not (_holds(q.codes, n * codes // 32, dev) and (not scales or _holds(q.scales, n * scales // 32, dev))
+            and _holds(q.texp, 4, dev)):
+        raise ValueError(f"{name}: codes, scales and texp must be contiguous on GPU {dev} and hold "
+                         f"[{q.rows}][{q.k}] in format {q.format}")
     return ctypes.byref(q.desc())
 
 
@@ -102,30 +108,28 @@ def _scratch(ws: Optional[torch.Tensor], dev: int) -> Tuple[Optional[int], int]:
     return ws.data_ptr(), ws.nbytes
 
 
-def _placed(fn):
-    """Run fn on its first argument's device and on `stream` (a torch stream
-    or a handle; default: the current one): what it allocates then belongs to
-    the stream that its kernels run on."""
-    @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
-        dev = first.get_device() if isinstance(first, torch.Tensor) and first.dim() == 2 else -1
-        if dev < 0:
-            raise ValueError(f"the first argument of {fn.__name__} must be a 2-D GPU tensor")
-        if stream is not None:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), dev) if int(stream) else torch.cuda.default_stream(dev)
-            with torch.cuda.stream(stream):
-                return fn(first, *args, **kw)
-        if dev != torch.cuda.current_device():
-            with torch.cuda.device(dev):
-                return fn(first, *args, **kw)
-        return fn(first, *args, **kw)
-    return call
+_current_device = getattr(torch._C, "_cuda_getDevice", None)             # absent from a build of torch without GPUs
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # handle of a device's current stream
 
 
-def _current(dev: int) -> int:
-    """Handle of the device's current stream."""
-    return torch._C._cuda_getCurrentRawStream(dev)
+def _device(t: torch.Tensor, fn) -> int:
+    """Index of the GPU that the first argument of fn lies on."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"the first argument of {fn.__name__} must be a 2-D GPU tensor")
+    return t.get_device()
+
+
+def _elsewhere(fn, dev: int, stream, *args):
+    """fn(*args) on device `dev` and on `stream` (a torch stream, a handle, or
+    None for the device's current one): what it allocates then belongs to the
+    stream that its kernels run on."""
+    if stream is None:
+        with torch.cuda.device(dev):
+            return fn(*args)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), dev) if int(stream) else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        return fn(*args)
 
 
 _F32 = (torch.float32,)
@@ -148,18 +152,17 @@ def _quant_out(q, out_fmt, rows, cols, dev, amax, stats, with_stats, ws, sizer):
     elif stats.get_device() != dev or stats.nbytes < _S.STATS_BYTES or not stats.is_contiguous():
         raise ValueError(f"stats must be a statistics tensor (new_stats) on GPU {dev}")
     if ws is None:
-        ws = _S._workspace(sizer(rows, cols, q.format), dev)
+        ws = torch.empty(sizer(rows, cols, q.format), dtype=torch.uint8, device=dev)
     return q, stats, (_operand(q, "q", dev), _S._amax_ptr(amax), _S._ptr(stats), *_scratch(ws, dev))
 
 
-@_placed
 def rmsnorm_fwd(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, res: Optional[torch.Tensor] = None,
                 h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
                 rstd: Optional[torch.Tensor] = None, q: Optional["_S.QuantizedTensor"] = None,
                 with_y: bool = True, with_rstd: bool = True, h_dtype: torch.dtype = torch.bfloat16,
                 y_dtype: torch.dtype = torch.bfloat16, out_fmt: Optional[int] = None, rounding: int = 0,
                 seed: int = 0, tensor_id: int = 0, amax=None, stats: Optional[torch.Tensor] = None,
-                with_stats: bool = True, ws: Optional[torch.Tensor] = None):
+                with_stats: bool = True, ws: Optional[torch.Tensor] = None, stream=None):
     """snipop_rmsnorm_fwd: h = x + res, y = h / sqrt(mean h^2 + eps) * gamma.
 
     Returns (y, h, rstd, q, stats). h is the new residual stream (None where
@@ -168,8 +171,11 @@ def rmsnorm_fwd(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, res: Op
     or MXFP4, or a QuantizedTensor to write into; None otherwise). amax: a
     supplied max|y| for its tensor scale, as in linear_fwd_save (unused without
     q)."""
+    dev = _device(x, rmsnorm_fwd)
+    if stream is not None or dev != _current_device():
+        return _elsewhere(rmsnorm_fwd, dev, stream, x, gamma, eps, res, h, y, rstd, q, with_y, with_rstd, h_dtype, y_dtype,
+                          out_fmt, rounding, seed, tensor_id, amax, stats, with_stats, ws)
     rows, cols = x.shape
-    dev = x.get_device()
     px = _mat(x, "x", rows, cols, dev)
     pr = _mat(res, "res", rows, cols, dev)
     pg = _vec(gamma, "gamma", cols, _ANY, dev)
@@ -185,20 +191,22 @@ def rmsnorm_fwd(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, res: Op
     _S._check(L.snipop_rmsnorm_fwd(
         *px, *pr, pg, _TYPES[gamma.dtype], rows, cols, eps, *_mat(h, "h", rows, cols, dev),
         *_mat(y, "y", rows, cols, dev), _vec(rstd, "rstd", rows, _F32, dev), d, rounding, seed, tensor_id, pa, ps, *pw,
-        _current(dev)))
+        _current_stream(dev)))
     return y, h, rstd, q, stats
 
 
-@_placed
 def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, rstd: torch.Tensor,
                 dres: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
                 dgamma: Optional[torch.Tensor] = None, need_dx: bool = True, need_dgamma: bool = True,
-                dx_dtype: torch.dtype = torch.bfloat16, ws: Optional[torch.Tensor] = None):
+                dx_dtype: torch.dtype = torch.bfloat16, ws: Optional[torch.Tensor] = None, stream=None):
     """snipop_rmsnorm_bwd: the gradients of y from rmsnorm_fwd. h: its h (x
     where there was no res); dres: the gradient that reaches h along the
     residual stream. Returns (dx, dgamma); dx is the gradient of x and of res."""
+    dev = _device(dy, rmsnorm_bwd)
+    if stream is not None or dev != _current_device():
+        return _elsewhere(rmsnorm_bwd, dev, stream, dy, h, gamma, rstd, dres, dx, dgamma, need_dx, need_dgamma, dx_dtype,
+                          ws)
     rows, cols = dy.shape
-    dev = dy.get_device()
     py = _mat(dy, "dy", rows, cols, dev)
     ph = _mat(h, "h", rows, cols, dev)
     if dx is None and need_dx:
@@ -207,25 +215,27 @@ def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, rstd: to
         dgamma = torch.empty(cols, dtype=torch.float32, device=dev)
     L = _S.lib()
     if ws is None and dgamma is not None:
-        ws = _S._workspace(L.snipop_rmsnorm_bwd_workspace(rows, cols), dev)
+        ws = torch.empty(L.snipop_rmsnorm_bwd_workspace(rows, cols), dtype=torch.uint8, device=dev)
     _S._check(L.snipop_rmsnorm_bwd(
         *py, *ph, _vec(gamma, "gamma", cols, _ANY, dev), _TYPES[gamma.dtype], _vec(rstd, "rstd", rows, _F32, dev),
         *_mat(dres, "dres", rows, cols, dev), rows, cols, *_mat(dx, "dx", rows, cols, dev),
-        _vec(dgamma, "dgamma", cols, _F32, dev), *_scratch(ws, dev), _current(dev)))
+        _vec(dgamma, "dgamma", cols, _F32, dev), *_scratch(ws, dev), _current_stream(dev)))
     return dx, dgamma
 
 
-@_placed
 def swiglu_fwd(gate: torch.Tensor, up: torch.Tensor, y: Optional[torch.Tensor] = None,
                q: Optional["_S.QuantizedTensor"] = None, with_y: bool = True,
                y_dtype: torch.dtype = torch.bfloat16, out_fmt: Optional[int] = None, rounding: int = 0,
                seed: int = 0, tensor_id: int = 0, amax=None, stats: Optional[torch.Tensor] = None,
-               with_stats: bool = True, ws: Optional[torch.Tensor] = None):
+               with_stats: bool = True, ws: Optional[torch.Tensor] = None, stream=None):
     """snipop_swiglu_fwd: y = gate * sigmoid(gate) * up. Returns (y, q,
     stats), with q, amax and stats as in rmsnorm_fwd. gate and up may be the
     two halves of one tensor's columns."""
+    dev = _device(gate, swiglu_fwd)
+    if stream is not None or dev != _current_device():
+        return _elsewhere(swiglu_fwd, dev, stream, gate, up, y, q, with_y, y_dtype, out_fmt, rounding, seed, tensor_id, amax,
+                          stats, with_stats, ws)
     rows, cols = gate.shape
-    dev = gate.get_device()
     if up.dtype != gate.dtype:
         raise ValueError("gate and up must have the same type")
     pg, tg, lg = _mat(gate, "gate", rows, cols, dev)
@@ -237,17 +247,18 @@ def swiglu_fwd(gate: torch.Tensor, up: torch.Tensor, y: Optional[torch.Tensor] =
                                             L.snipop_swiglu_fwd_workspace)
     _S._check(L.snipop_swiglu_fwd(
         pg, lg, pu, lu, tg, rows, cols, *_mat(y, "y", rows, cols, dev), d, rounding, seed, tensor_id, pa, ps, *pw,
-        _current(dev)))
+        _current_stream(dev)))
     return y, q, stats
 
 
-@_placed
 def swiglu_bwd(dy: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, dgate: Optional[torch.Tensor] = None,
                dup: Optional[torch.Tensor] = None, need_dgate: bool = True, need_dup: bool = True,
-               dtype: torch.dtype = torch.bfloat16):
+               dtype: torch.dtype = torch.bfloat16, stream=None):
     """snipop_swiglu_bwd: (dgate, dup) from the gradient of swiglu_fwd's y."""
+    dev = _device(dy, swiglu_bwd)
+    if stream is not None or dev != _current_device():
+        return _elsewhere(swiglu_bwd, dev, stream, dy, gate, up, dgate, dup, need_dgate, need_dup, dtype)
     rows, cols = dy.shape
-    dev = dy.get_device()
     if up.dtype != gate.dtype:
         raise ValueError("gate and up must have the same type")
     py = _mat(dy, "dy", rows, cols, dev)
@@ -262,17 +273,18 @@ def swiglu_bwd(dy: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, dgate: Op
     pdg, tdg, ldg = _mat(dgate, "dgate", rows, cols, dev)
     pdu, tdu, ldu = _mat(dup, "dup", rows, cols, dev)
     _S._check(_S.lib().snipop_swiglu_bwd(*py, pg, lg, pu, lu, tg, rows, cols, pdg, ldg, pdu, ldu, max(tdg, tdu),
-                                         _current(dev)))
+                                         _current_stream(dev)))
     return dgate, dup
 
 
-@_placed
 def qgemv(x: torch.Tensor, w: "_S.QuantizedTensor", y: Optional[torch.Tensor] = None,
-          y_dtype: torch.dtype = torch.float32) -> torch.Tensor:
+          y_dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
     """snipop_qgemv: y [tokens, N] = x [tokens, K] . dequant(w)^T for 1 to 16
     tokens, x in bfloat16, w in any quantized format with K % 32 == 0."""
+    dev = _device(x, qgemv)
+    if stream is not None or dev != _current_device():
+        return _elsewhere(qgemv, dev, stream, x, w, y, y_dtype)
     m, k = x.shape
-    dev = x.get_device()
     if x.dtype != torch.bfloat16:
         raise ValueError("x must be bfloat16")
     if k != w.k:
@@ -286,5 +298,5 @@ def qgemv(x: torch.Tensor, w: "_S.QuantizedTensor", y: Optional[torch.Tensor] = 
         raise ValueError(f"y must be a bfloat16 or float32 tensor of shape ({m}, {n}) with unit column stride on "
                          f"{x.device}")
     ly = y.stride(0) if m > 1 else n
-    _S._check(_S.lib().snipop_qgemv(px, lx, m, _operand(w, "w", dev), y.data_ptr(), ty, ly, _current(dev)))
+    _S._check(_S.lib().snipop_qgemv(px, lx, m, _operand(w, "w", dev), y.data_ptr(), ty, ly, _current_stream(dev)))
     return y
