@@ -2,11 +2,17 @@
 //
 //   y[m][n] = 2^e sum_b s[n][b] sum_{k in block b} c[n][k] x[m][k]
 //
-// Bound by the weights' bytes (0.53 to 1 byte each). A lane loads 16 bytes of
-// codes of a row (32 E2M1 or 16 E4M3 weights), decodes them to bf16 pairs
-// (exact: 2 or 4 significant bits) and multiplies them with the tokens' bf16
-// by v_dot2_f32_bf16: exact products, fp32 sums. The block scale multiplies
-// the block's sum, so it costs one operation a block.
+// Bound by the weights' bytes (0.53 to 1 byte each), read once; at a few MB by
+// latency. Both forms below take the codes in 1 KB loads that run ahead of
+// their use and multiply in bf16 with fp32 sums; codes are exact in bf16.
+//  - dot: a wave has one or two rows and the whole K; v_dot2_f32_bf16 on the
+//    decoded pairs, the block scale on the block's sum. 36 VALU operations per
+//    KB of codes and token, so it is for one or two tokens.
+//  - MFMA: tiles of 16 rows x 16 tokens, the waves of a workgroup share K;
+//    scales are applied as the codes are decoded (64 VALU operations per KB of
+//    NVFP4, 16 of MXFP4, for all tokens).
+// NVFP4, one token, dot / MFMA: 2048 x 2048 2.7 / 3.9 us, 4096 x 11008 7.4 /
+// 9.0, 28672 x 8192 27.2 / 29.9 (4.9 TB/s; of 132 MB, a bare read takes 21.3).
 #include "row_common.h"
 
 namespace snip {
@@ -39,20 +45,6 @@ __device__ __forceinline__ float scale_val(int sc, uint32_t raw, int i) {
   return __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7FC00000u : b << 23);
 }
 
-// The scales of the NB blocks of chunk `c` (PER weights) of row `n`.
-template <int FMT>
-__device__ __forceinline__ uint32_t load_scales(const Gemv& A, int64_t n, int64_t c) {
-  using W = WFmt<FMT>;
-  if constexpr (W::SC == 0) return 0u;
-  const int64_t i = (n * (A.K / W::PER) + c) * W::NB;  // K % PER == 0
-  if constexpr (W::SC == 3) {
-    if constexpr (W::NB == 2) return *reinterpret_cast<const uint32_t*>(A.scales + 2 * i);
-    return *reinterpret_cast<const uint16_t*>(A.scales + 2 * i);
-  }
-  if constexpr (W::NB == 2) return *reinterpret_cast<const uint16_t*>(A.scales + i);
-  return A.scales[i];
-}
-
 // Pair `j` (weights 2j, 2j + 1) of a code word.
 template <bool FP8>
 __device__ __forceinline__ bf16x2_t decode_pair(uint32_t w, int j) {
@@ -77,46 +69,123 @@ __device__ __forceinline__ void store_y(const Gemv& A, int64_t m, int64_t n, flo
     static_cast<uint16_t*>(A.y)[i] = (uint16_t)pack_bf16(v, 0.0f);
 }
 
-// One wave per row, one token per blockIdx.y. Bound by the vector memory
-// unit rather than by HBM (a lane's 64 bytes of x are four scattered
-// accesses), but with nothing to set up: 2.2 us for 256 x 2048 where the MFMA
-// form takes 3.4, 3.0 for 2048 x 2048 (3.8); behind from 2^23 weights on
-// (4096 x 11008: 10 us for 8.5).
-template <int FMT>
-__global__ __launch_bounds__(256) void qgemv_dot_kernel(Gemv A) {
+// Buffer descriptor over `bytes` of p: a load whose offset lies beyond them
+// returns zero, which stands in for rows and columns outside the operands.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(bytes > 0 ? bytes : 0), 0x00027000);
+}
+constexpr uint32_t kOutside = 0x80000000u;             // beyond every descriptor
+
+// ------------------------------------------------------------ dot form
+constexpr int kRowWaves = 8;
+constexpr int kRowSlab = 32768;                        // the tokens' values held in LDS (64 KB)
+
+// MT tokens (group blockIdx.y), R rows a wave. A wave's load is 1 KB of a row;
+// the tokens' values of the same chunk come from LDS, in pieces of 8 swizzled
+// so that the lanes' 64-byte strides meet no bank twice, and serve the R rows.
+// A row's next chunk is loaded before the present one is used; beyond K the
+// descriptors give zeros.
+template <int FMT, int MT, int R>
+__global__ __launch_bounds__(64 * kRowWaves) void qgemv_row_kernel(Gemv A) {
   using W = WFmt<FMT>;
-  const int lane = threadIdx.x & 63;
-  const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int m = blockIdx.y;
-  if (n >= A.N) return;
-  const int64_t nch = A.K / W::PER;
-  const uint8_t* codes = A.codes + n * (W::FP8 ? A.K : A.K / 2);
-  const uint16_t* xm = A.x + m * A.ldx;
-  float acc = 0.0f;
-  for (int64_t c = lane; c < nch; c += 64) {
-    const u32x4_t w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(codes + 16 * c));
-    const uint32_t sc = load_scales<FMT>(A, n, c);
-    const u32x4_t* xp = reinterpret_cast<const u32x4_t*>(xm + c * W::PER);
-    float part[W::NB];
+  constexpr int NP = W::PER / 8;                       // pieces of a chunk
+  constexpr int SB = W::SC == 0 ? 0 : W::NB * (W::SC == 3 ? 2 : 1);   // scale bytes of a chunk
+  constexpr int SLAB = kRowSlab / MT;
+  extern __shared__ u32x4_t smem[];                    // [MT][pieces of a slab]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = ((int64_t)blockIdx.x * kRowWaves + wave) * R;
+  const int K = (int)A.K, nch = K / W::PER;
+  const int64_t crow = W::FP8 ? K : K / 2, srow = (int64_t)SB * nch;
+  __amdgpu_buffer_rsrc_t cb[R], sb[R];
 #pragma unroll
-    for (int b = 0; b < W::NB; ++b) part[b] = 0.0f;
+  for (int t = 0; t < R; ++t) {
+    const bool in = n0 + t < A.N;
+    cb[t] = buffer_of(A.codes + (in ? n0 + t : 0) * crow, in ? crow : 0);
+    if constexpr (SB > 0) sb[t] = buffer_of(A.scales + (in ? n0 + t : 0) * srow, in ? srow : 0);
+  }
+  u32x4_t w[R];
+  uint32_t sc[R];
+  auto load = [&](int c) {
 #pragma unroll
-    for (int q = 0; q < W::PER / 8; ++q) {
-      const u32x4_t x = xp[q];                         // values of the pairs 4q .. 4q+3
+    for (int t = 0; t < R; ++t) {
+      w[t] = __builtin_amdgcn_raw_buffer_load_b128(cb[t], 16 * c, 0, 2);
+      sc[t] = 0u;
+      if constexpr (SB == 1) sc[t] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(sb[t], c, 0, 0);
+      if constexpr (SB == 2) sc[t] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(sb[t], 2 * c, 0, 0);
+      if constexpr (SB == 4) sc[t] = __builtin_amdgcn_raw_buffer_load_b32(sb[t], 4 * c, 0, 0);
+    }
+  };
+  float acc[R][MT];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int pair = 4 * q + j, per = W::FP8 ? 2 : 4;
-        float& p = part[pair * 2 * W::NB / W::PER];
-        p = __builtin_amdgcn_fdot2_f32_bf16(decode_pair<W::FP8>(w[pair / per], pair % per),
-                                            __builtin_bit_cast(bf16x2_t, (uint32_t)x[j]), p, false);
+  for (int t = 0; t < R; ++t)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[t][m] = 0.0f;
+  load(lane);
+  const int m0 = blockIdx.y * MT;
+  for (int k0 = 0; k0 < K; k0 += SLAB) {
+    const int end = K - k0 < SLAB ? K - k0 : SLAB;
+    const int steps = (end / W::PER + 63) / 64;        // of 64 chunks, the last one filled up with zeros
+    const int pieces = steps * 64 * NP;
+    if (k0) __syncthreads();
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const u32x4_t* x = reinterpret_cast<const u32x4_t*>(A.x + (m0 + m < A.M ? m0 + m : 0) * A.ldx + k0);
+      for (int i = threadIdx.x; i < pieces; i += 64 * kRowWaves) {
+        const int c = i / NP, j = i % NP;
+        smem[m * pieces + c * NP + (j ^ (c / (16 / NP) % NP))] = 8 * i < end ? x[i] : u32x4_t{0u, 0u, 0u, 0u};
       }
     }
+    __syncthreads();
+    for (int s = 0; s < steps; ++s) {
+      const int c = 64 * s + lane;
+      u32x4_t v[R], xp[MT][NP];
+      uint32_t q[R];
 #pragma unroll
-    for (int b = 0; b < W::NB; ++b)
-      acc = W::SC == 0 ? acc + part[b] : fmaf(part[b], scale_val(W::SC, sc, b), acc);
+      for (int t = 0; t < R; ++t) {
+        v[t] = w[t];
+        q[t] = sc[t];
+      }
+      load(k0 / W::PER + c + 64);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NP; ++j) xp[m][j] = smem[m * pieces + c * NP + (j ^ (c / (16 / NP) % NP))];
+#pragma unroll
+      for (int t = 0; t < R; ++t) {
+        float part[W::NB][MT];
+#pragma unroll
+        for (int b = 0; b < W::NB; ++b)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) part[b][m] = 0.0f;
+#pragma unroll
+        for (int pair = 0; pair < W::PER / 2; ++pair) {
+          constexpr int per = W::FP8 ? 2 : 4;
+          const bf16x2_t d = decode_pair<W::FP8>(v[t][pair / per], pair % per);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            float& p = part[pair * 2 * W::NB / W::PER][m];
+            p = __builtin_amdgcn_fdot2_f32_bf16(
+                d, __builtin_bit_cast(bf16x2_t, (uint32_t)xp[m][pair / 4][pair % 4]), p, false);
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < W::NB; ++b) {
+          const float f = W::SC == 0 ? 1.0f : scale_val(W::SC, q[t], b);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            acc[t][m] = W::SC == 0 ? acc[t][m] + part[b][m] : fmaf(part[b][m], f, acc[t][m]);
+        }
+      }
+    }
   }
-  const float v = wave_sum_f(acc);
-  if (lane == 0) store_y(A, m, n, ldexpf(v, A.texp ? *A.texp : 0));
+  const int e = A.texp ? *A.texp : 0;
+#pragma unroll
+  for (int t = 0; t < R; ++t)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const float v = wave_sum_f(acc[t][m]);
+      if (lane == 0 && n0 + t < A.N && m0 + m < A.M) store_y(A, m0 + m, n0 + t, ldexpf(v, e));
+    }
 }
 
 // ------------------------------------------------------------ MFMA form
@@ -154,15 +223,9 @@ __device__ __forceinline__ void decode8(const u32x4_t& w, int i, float s, bf16x8
   if constexpr (W::SC == 3) lo = __builtin_bit_cast(bf16x8_t, l);
 }
 
-// Buffer descriptor over `bytes` of p: a load whose offset lies beyond them
-// returns zero, which stands in for rows and columns outside the operands.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(bytes > 0 ? bytes : 0), 0x00027000);
-}
 // Orders the LDS accesses of a wave's lanes: LDS serves a wave's instructions
 // in order, so only the compiler has to be told.
 __device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
-constexpr uint32_t kOutside = 0x80000000u;             // beyond every descriptor
 
 // RT tiles of 16 rows per wave, the workgroup's waves splitting K in stages
 // of 128 code bytes a row; XT loads bring a stage of the tokens.
@@ -305,6 +368,7 @@ __global__ __launch_bounds__(RT == 1 ? 1024 : 512) void qgemv_mfma_kernel(Gemv A
 
 namespace {
 constexpr size_t kMaxLds = 160 * 1024;
+constexpr int64_t kPairMost = 1 << 25;                // weights up to which two tokens take the dot form
 
 // LDS of a workgroup: the waves' pieces and the tile's scales, or the sums.
 template <int FMT>
@@ -321,21 +385,41 @@ hipError_t gemv_mfma(const Gemv& a, int waves, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int FMT, int MT, int R>
+hipError_t gemv_row(const Gemv& a, hipStream_t s) {
+  constexpr int64_t step = 64 * WFmt<FMT>::PER, slab = kRowSlab / MT;
+  const int64_t held = a.K < slab ? ceil_div(a.K, step) * step : slab;
+  qgemv_row_kernel<FMT, MT, R><<<dim3((unsigned)ceil_div(a.N, kRowWaves * R), (unsigned)ceil_div(a.M, MT)),
+                                 dim3(64 * kRowWaves), (size_t)held * MT * 2, s>>>(a);
+  return hipGetLastError();
+}
+
 template <int FMT>
 hipError_t gemv_fmt(const Gemv& a, hipStream_t s) {
+  // One token: two rows a wave halve the reads of the token's values in LDS but
+  // leave half the waves (8192 x 28672 NVFP4 23.9 us with two, 26.5 with one;
+  // 4096 x 11008 7.7 and 7.4; 2048 x 2048 3.2 and 2.7).
+  if (a.M == 1) return a.N >= 8192 ? gemv_row<FMT, 1, 2>(a, s) : gemv_row<FMT, 1, 1>(a, s);
+  // Two tokens: the dot form while the time is mostly latency (NVFP4, dot and
+  // MFMA: 4096 x 4096 4.6 and 5.6 us, 11008 x 4096 9.0 and 8.7, 28672 x 8192
+  // 31.9 and 29.0). With three or four it is never ahead.
+  if (a.M == 2 && a.N * a.K <= kPairMost) return gemv_row<FMT, 2, 1>(a, s);
   constexpr int TPI = WFmt<FMT>::FP8 ? 4 : 2;          // tokens per load
   const int64_t tiles = ceil_div(a.N, 16), stages = ceil_div(a.K, WFmt<FMT>::FP8 ? 128 : 256);
-  // More rows a wave spare reads of the tokens' values, which are as many
+  // More tiles a wave spare reads of the tokens' values, which are as many
   // bytes as the codes of 64 rows at 16 tokens and next to nothing at 4; but
-  // the 256 CUs want a workgroup each. Few tiles: more waves along K.
-  const int rt = a.M <= 4 || tiles < 512 ? 1 : tiles < 1024 ? 2 : 4;
+  // the 256 CUs want a workgroup each. NVFP4, 16 tokens, one, two and four
+  // tiles: 4096 x 4096 7.5, 9.1, 13.6 us; 16384 x 4096 16.8, 14.4, 16.0;
+  // 28672 x 8192 48.4, 42.8, 40.1.
+  const int rt = a.M <= 4 || tiles < 512 ? 1 : tiles <= 1536 ? 2 : 4;
+  // Few tiles: more waves along K (2048 x 28672, 3 tokens: 16.3 us with 16
+  // waves, 18.6 with 8; 11008 x 4096: 12.3 and 9.6). Four tiles a wave: its
+  // loads are long enough (28672 x 8192, 16 tokens: 40.1 us with 4, 46.5 with 8).
   int waves = rt == 4 ? 4 : tiles <= 256 ? 16 : 8;
   if (waves > stages) waves = (int)stages;
   const int xt = a.M <= TPI ? 1 : a.M <= 4 ? 2 : a.M <= 8 ? 8 / TPI : 16 / TPI;
-  if ((a.M == 1 && a.N * a.K <= (int64_t)1 << 23) || mfma_lds<FMT>(a.K, rt, xt, waves) > kMaxLds) {
-    qgemv_dot_kernel<FMT><<<dim3((unsigned)ceil_div(a.N, 4), a.M), dim3(256), 0, s>>>(a);
-    return hipGetLastError();
-  }
+  // A tile's scales stay in LDS; where K is too long for that, token by token.
+  if (mfma_lds<FMT>(a.K, rt, xt, waves) > kMaxLds) return gemv_row<FMT, 1, 1>(a, s);
   if (a.M <= TPI) return gemv_mfma<FMT, 1, 1>(a, waves, s);
   if constexpr (TPI == 2)
     if (a.M <= 4) return gemv_mfma<FMT, 1, 2>(a, waves, s);

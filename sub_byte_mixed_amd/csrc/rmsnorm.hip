@@ -345,10 +345,10 @@ struct NormShape {
 };
 
 // A chunk a thread up to `one_up_to` chunks, two beyond. The forward pass
-// takes two from 4096 columns on (4096 x 8192 bf16 to FP8: 44.7 us, 45.8 with
+// takes two beyond 4096 columns (4096 x 8192 bf16 to FP8: 44.4 us, 46.4 with
 // one and 1024 threads); the backward pass, with its column sums, is short of
-// registers then and takes two where it must (4096 x 8192: 67 us with one, 93
-// with two).
+// registers then and takes two where it must (4096 x 8192, fp32 residual: 67 us
+// with one, 83 with two; 1003 x 4104: 14.1 and 16.3).
 NormShape norm_shape(int64_t cols, int one_up_to) {
   const int64_t ch = ceil_div(cols, 8);
   if (ch <= 64) return {false, 1, 256};
@@ -399,13 +399,13 @@ hipError_t norm_fwd_quant(const NormFwd& a, int nwg, hipStream_t s) {
 }  // namespace
 
 // As many workgroups as are resident, 16 waves on each of the 256 CUs: a row's
-// loads then run while the row before is worked on (4096 x 4096: 32.6 us with
-// 512 workgroups of 8 waves, 34.4 with 1024; 4096 x 2048: 18.0 us with 1024 of
-// 4 waves, 21.2 with 512).
+// loads then run while the row before is worked on (fp32 residual, to FP8, 4096 x
+// 4096: 30.2 us with 512 workgroups of 8 waves, 31.2 with 1024; 4096 x 2048:
+// 18.0 us with 1024 of 4 waves, 21.2 with 512).
 int norm_fwd_wg(int64_t rows, int64_t cols) {
   const NormShape k = fwd_shape(cols);
   const int per_cu = 1024 / k.threads;
-  static_assert(256 * 4 <= kOpsWG, "threads are 256 or more a workgroup, or rows are few");
+  static_assert(256 * 4 <= kOpsWG, "one partial a workgroup, at most 4 workgroups a CU");
   return norm_wg(k, rows, 256 * (per_cu < 1 ? 1 : per_cu > 4 ? 4 : per_cu));
 }
 // Each workgroup leaves a partial row of dgamma, to be written and read
