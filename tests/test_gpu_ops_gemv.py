@@ -173,3 +173,16 @@ def test_operands_that_do_not_hold_the_weights_are_refused():
         a.update(bad)
         with pytest.raises(ValueError):
             S.qgemv(x, S.QuantizedTensor(S.NVFP4, 8, 64, "cuda", **a))
+
+
+@pytest.mark.parametrize("fmt", [S.FP8, S.NVFP4, S.MXFP4, S.FP4_BF16_B16])
+@pytest.mark.parametrize("n,k,tokens", [(24593, 64, (4, 7, 16)), (8201, 4128, (1, 2, 3)), (10, 49248, (1, 2))])
+def test_every_form_of_a_launch(fmt, n, k, tokens):
+    """Each rule on N, K and the tokens from its other side: many tiles a
+    wave, two rows a wave, two tokens in a weight too large for the dot form,
+    and a token's values in more than one slab."""
+    w = raw_weights(fmt, n, k, n)
+    for m in tokens:
+        say("gemv forms", S.FORMAT_NAMES[fmt], n, k, m)
+        x = rand((m, k), BF, 31 + m).cuda()
+        check(x, w, S.qgemv(x, w))
