@@ -408,10 +408,12 @@ hipError_t gemv_fmt(const Gemv& a, hipStream_t s) {
   const int64_t tiles = ceil_div(a.N, 16), stages = ceil_div(a.K, WFmt<FMT>::FP8 ? 128 : 256);
   // More tiles a wave spare reads of the tokens' values, which are as many
   // bytes as the codes of 64 rows at 16 tokens and next to nothing at 4; but
-  // the 256 CUs want a workgroup each. NVFP4, 16 tokens, one, two and four
-  // tiles: 4096 x 4096 7.5, 9.1, 13.6 us; 16384 x 4096 16.8, 14.4, 16.0;
-  // 28672 x 8192 48.4, 42.8, 40.1.
-  const int rt = a.M <= 4 || tiles < 512 ? 1 : tiles <= 1536 ? 2 : 4;
+  // the 256 CUs want a workgroup each, and beyond that two workgroups a CU hide
+  // more latency than one with twice the tiles, until the reads weigh more.
+  // NVFP4, 16 tokens, one, two, three and four tiles: 4096 x 4096 7.5, 9.1, -,
+  // 13.6 us; 7168 x 4096 10.6, 9.5, 11.5, 16.6; 11008 x 4096 14.9, 13.8, 12.4,
+  // 14.6; 16384 x 4096 16.8, 14.4, 22.0, 15.9; 28672 x 8192 52.9, 42.8, 51.7, 40.0.
+  const int rt = a.M <= 4 || tiles <= 256 ? 1 : tiles <= 512 ? 2 : tiles <= 768 ? 3 : tiles <= 1536 ? 2 : 4;
   // Few tiles: more waves along K (2048 x 28672, 3 tokens: 16.3 us with 16
   // waves, 18.6 with 8; 11008 x 4096: 12.3 and 9.6). Four tiles a wave: its
   // loads are long enough (28672 x 8192, 16 tokens: 40.1 us with 4, 46.5 with 8).
@@ -426,10 +428,12 @@ hipError_t gemv_fmt(const Gemv& a, hipStream_t s) {
   if (a.M <= 8) {
     if (rt == 1) return gemv_mfma<FMT, 1, 8 / TPI>(a, waves, s);
     if (rt == 2) return gemv_mfma<FMT, 2, 8 / TPI>(a, waves, s);
+    if (rt == 3) return gemv_mfma<FMT, 3, 8 / TPI>(a, waves, s);
     return gemv_mfma<FMT, 4, 8 / TPI>(a, waves, s);
   }
   if (rt == 1) return gemv_mfma<FMT, 1, 16 / TPI>(a, waves, s);
   if (rt == 2) return gemv_mfma<FMT, 2, 16 / TPI>(a, waves, s);
+  if (rt == 3) return gemv_mfma<FMT, 3, 16 / TPI>(a, waves, s);
   return gemv_mfma<FMT, 4, 16 / TPI>(a, waves, s);
 }
 }  // namespace

@@ -176,7 +176,7 @@ def test_operands_that_do_not_hold_the_weights_are_refused():
 
 
 @pytest.mark.parametrize("fmt", [S.FP8, S.NVFP4, S.MXFP4, S.FP4_BF16_B16])
-@pytest.mark.parametrize("n,k,tokens", [(24593, 64, (4, 7, 16)), (8201, 4128, (1, 2, 3)), (10, 49248, (1, 2))])
+@pytest.mark.parametrize("n,k,tokens", [(24593, 64, (4, 7, 16)), (8201, 4128, (1, 2, 3)), (10, 49248, (1, 2)), (4117, 288, (5, 16)), (12275, 160, (5, 16))])
 def test_every_form_of_a_launch(fmt, n, k, tokens):
     """Each rule on N, K and the tokens from its other side: many tiles a
     wave, two rows a wave, two tokens in a weight too large for the dot form,
