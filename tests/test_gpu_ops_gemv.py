@@ -186,3 +186,42 @@ def test_every_form_of_a_launch(fmt, n, k, tokens):
         say("gemv forms", S.FORMAT_NAMES[fmt], n, k, m)
         x = rand((m, k), BF, 31 + m).cuda()
         check(x, w, S.qgemv(x, w))
+
+
+def test_nan_codes_of_fp8_reach_their_row_alone():
+    for n, k in ((40, 256), (40, 1056), (8200, 64)):
+        w = raw_weights(S.FP8, n, k, 12)
+        codes = w.codes.view(n, k)
+        codes[3, k - 1], codes[n - 1, 0] = 0x7F, 0xFF
+        for m in (1, 2, 4, 16):
+            say("nan code", n, k, m)
+            bad = torch.isnan(S.qgemv(rand((m, k), BF, m).cuda(), w))
+            assert bad[:, 3].all() and bad[:, n - 1].all() and int(bad.sum()) == 2 * m
+
+
+@pytest.mark.parametrize("m", [1, 3, 16])
+def test_weights_beyond_4_gib(m):
+    """Rows that start past 2^32 bytes of codes, after rows of zeros."""
+    n, k, last = (1 << 19) + 11, 8192 + 32, 27
+    w = S.QuantizedTensor(S.FP8, n, k, "cuda")
+    w.codes.zero_()
+    small = raw_weights(S.FP8, last, k, 13)
+    w.codes.view(n, k)[-last:] = small.codes.view(last, k)
+    w.texp.copy_(small.texp)
+    x = rand((m, k), BF, 60).cuda()
+    say("4 GiB", m)
+    y = S.qgemv(x, w)
+    assert not y[:, :-last].any()
+    check(x, small, y[:, -last:])
+
+
+def test_other_stream():
+    w = raw_weights(S.NVFP4, 300, 2048, 14)
+    x = rand((4, 2048), BF, 61).cuda()
+    want = S.qgemv(x, w)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for handle in (side, side.cuda_stream):
+        y = S.qgemv(x, w, stream=handle)
+        side.synchronize()
+        assert torch.equal(y, want)

@@ -113,3 +113,37 @@ def test_gradient_against_differences():
     nu = (y(g, u + step) - y(g, u - step)) / (2 * step) * f64(dy)
     lim = 2e-3 * (1.0 + np.abs(f64(u))) * (1.0 + np.abs(f64(dy)))
     assert (np.abs(ng - f64(dg)) < lim).all() and (np.abs(nu - f64(du)) < lim).all()
+
+
+def test_long_batch_passes_32_bit_offsets():
+    """More than 2^31 elements of a matrix: the last rows against themselves
+    in a small call, forward and backward, in place to save memory."""
+    rows, cols = 195105, 11008
+    g, u = (torch.zeros((rows, cols), dtype=BF, device="cuda") for _ in range(2))
+    tg, tu, td = (rand((3, cols), BF, 70 + i).cuda() for i in range(3))
+    g[-3:], u[-3:] = tg, tu
+    say("swiglu", rows, cols)
+    _, q, _ = S.swiglu_fwd(g, u, with_y=False, out_fmt=S.FP8, amax=torch.tensor([8.0], device="cuda"), with_stats=False)
+    _, q2, _ = S.swiglu_fwd(tg, tu, with_y=False, out_fmt=S.FP8, amax=torch.tensor([8.0], device="cuda"),
+                            with_stats=False)
+    assert torch.equal(q.codes[-3 * cols:], q2.codes) and not q.codes[:-3 * cols].any()
+    dy = torch.ones((rows, cols), dtype=BF, device="cuda")
+    dy[-3:] = td
+    say("swiglu_bwd", rows, cols)
+    S.swiglu_bwd(dy, g, u, dgate=g, dup=u)
+    dg, du = S.swiglu_bwd(td, tg, tu)
+    assert torch.equal(g[-3:], dg) and torch.equal(u[-3:], du) and not g[:-3].any() and not u[:-3].any()
+
+
+def test_other_stream():
+    g, u, dy = (rand((300, 2048), F32, 80 + i).cuda() for i in range(3))
+    y0, q0, st0 = S.swiglu_fwd(g, u, out_fmt=S.MXFP4)
+    dg0, du0 = S.swiglu_bwd(dy, g, u)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for handle in (side, side.cuda_stream):
+        y, q, st = S.swiglu_fwd(g, u, out_fmt=S.MXFP4, stream=handle)
+        dg, du = S.swiglu_bwd(dy, g, u, stream=handle)
+        side.synchronize()
+        assert torch.equal(y, y0) and torch.equal(q.codes, q0.codes) and torch.equal(st, st0)
+        assert torch.equal(dg, dg0) and torch.equal(du, du0)
