@@ -60,8 +60,8 @@ extern "C" {
  *   rounding, seed, tensor_id, amax_in, stats  as snip_quantize, for `out`.
  *              amax_in NULL (NVFP4, FP8): max|y| comes from an extra pass
  *              that reads x, res and gamma.
- *   ws         device, snipop_rmsnorm_fwd_workspace() bytes; needed only with
- *              `out`.
+ *   ws         device, snipop_rmsnorm_fwd_workspace() bytes; needed only for
+ *              stats, or to find max|y|.
  *   rows > 0; 0 < cols <= SNIPOP_NORM_MAX_COLS. At least one of h, y, rstd,
  *   out must be given.
  * Errors: NULL, SHAPE, ALIGN, FORMAT, WORKSPACE, HIP. */

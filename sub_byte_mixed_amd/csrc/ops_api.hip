@@ -78,18 +78,19 @@ int check_out(const char* who, const snip_qtensor* out, int64_t rows, int64_t co
                 (long long)out->k, (long long)rows, (long long)cols);
   if (!aligned(amax_in, 4) || !aligned(stats, 8) || !aligned(ws, 16))
     return fail(SNIP_E_ALIGN, "%s: misaligned pointer", who);
-  if (!ws || ws_bytes < kOpsQuantWS)
+  const bool find = needs_amax(out->format) && !amax_in;
+  if ((find || stats) && (!ws || ws_bytes < kOpsQuantWS))
     return fail(SNIP_E_WORKSPACE, "%s: workspace of %zu bytes needed", who, kOpsQuantWS);
   Carver cv(ws);
-  uint32_t* ap = reinterpret_cast<uint32_t*>(cv.take(kOpsAmaxBytes));
-  StatPart* sp = reinterpret_cast<StatPart*>(cv.take(kOpsWG * sizeof(StatPart)));
-  if (needs_amax(out->format) && !amax_in) *amax = ap;
+  uint32_t* ap = find ? reinterpret_cast<uint32_t*>(cv.take(kOpsAmaxBytes)) : nullptr;
+  StatPart* sp = stats ? reinterpret_cast<StatPart*>(cv.take(kOpsWG * sizeof(StatPart))) : nullptr;
+  *amax = ap;
   q->codes = static_cast<uint8_t*>(out->codes);
   q->scales = static_cast<uint8_t*>(out->scales);
   q->texp = has_texp(out->format) ? out->tensor_exp : nullptr;
   q->amax_in = amax_in;
   q->amax_part = ap;
-  q->part = stats ? sp : nullptr;
+  q->part = sp;
   q->seed = seed;
   q->tensor_id = tensor_id;
   q->sr = rounding == SNIP_SR;

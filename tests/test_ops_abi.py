@@ -180,3 +180,14 @@ def test_binding_wants_gpu_matrices():
                  lambda: S.swiglu_fwd(x, x), lambda: S.swiglu_bwd(x, x, x), lambda: S.qgemv(x, None)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_workspace_is_wanted_for_the_maximum_and_the_statistics(L):
+    """Without either a call goes past the workspace's check: here to the
+    error of a launch without a GPU, or none at all."""
+    if torch.cuda.is_available():
+        pytest.skip("would launch on made-up addresses")
+    for fmt, amax, stats, wanted in ((S.FP8, None, None, True), (S.FP8, at(7), None, False), (S.NVFP4, at(7), at(9), True),
+                                     (S.MXFP4, None, None, False), (S.MXFP4, None, at(9), True)):
+        rc = norm_fwd(L, out=qdesc(fmt, 4, 64), amax=amax, stats=stats, ws=None, n=0)
+        assert (rc == -5) == wanted, (fmt, amax, stats, rc)
