@@ -5,14 +5,14 @@
 // Bound by the weights' bytes (0.53 to 1 byte each), read once; at a few MB by
 // latency. Both forms below take the codes in 1 KB loads that run ahead of
 // their use and multiply in bf16 with fp32 sums; codes are exact in bf16.
-//  - dot: a wave has one or two rows and the whole K; v_dot2_f32_bf16 on the
+//  - dot: a wave has a row and the whole K; v_dot2_f32_bf16 on the
 //    decoded pairs, the block scale on the block's sum. 36 VALU operations per
 //    KB of codes and token, so it is for one or two tokens.
 //  - MFMA: tiles of 16 rows x 16 tokens, the waves of a workgroup share K;
 //    scales are applied as the codes are decoded (64 VALU operations per KB of
 //    NVFP4, 16 of MXFP4, for all tokens).
 // NVFP4, one token, dot / MFMA: 2048 x 2048 2.7 / 3.9 us, 4096 x 11008 7.4 /
-// 9.0, 28672 x 8192 27.2 / 29.9 (4.9 TB/s; of 132 MB, a bare read takes 21.3).
+// 9.0, 28672 x 8192 25.1 / 29.9 (5.3 TB/s; of 132 MB, a bare read takes 21.3).
 #include "row_common.h"
 
 namespace snip {
@@ -80,53 +80,43 @@ constexpr uint32_t kOutside = 0x80000000u;             // beyond every descripto
 constexpr int kRowWaves = 8;
 constexpr int kRowSlab = 32768;                        // the tokens' values held in LDS (64 KB)
 
-// MT tokens (group blockIdx.y), R rows a wave. A wave's load is 1 KB of a row;
+// MT tokens (group blockIdx.y), a row a wave. A wave's load is 1 KB of the row;
 // the tokens' values of the same chunk come from LDS, in pieces of 8 swizzled
-// so that the lanes' 64-byte strides meet no bank twice, and serve the R rows.
-// A row's next chunk is loaded before the present one is used; beyond K the
-// descriptors give zeros.
-template <int FMT, int MT, int R>
-__global__ __launch_bounds__(64 * kRowWaves) void qgemv_row_kernel(Gemv A) {
+// so that the lanes' 64-byte strides meet no bank twice. The next chunk is
+// loaded before the present one is used; beyond K the descriptors give zeros.
+// WALK: the tokens fit in one slab, and a wave goes on to the row `stride`
+// further, its loads running on from row to row.
+template <int FMT, int MT, bool WALK>
+__global__ __launch_bounds__(64 * kRowWaves) void qgemv_row_kernel(Gemv A, int64_t stride) {
   using W = WFmt<FMT>;
   constexpr int NP = W::PER / 8;                       // pieces of a chunk
   constexpr int SB = W::SC == 0 ? 0 : W::NB * (W::SC == 3 ? 2 : 1);   // scale bytes of a chunk
   constexpr int SLAB = kRowSlab / MT;
   extern __shared__ u32x4_t smem[];                    // [MT][pieces of a slab]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t n0 = ((int64_t)blockIdx.x * kRowWaves + wave) * R;
+  int64_t n = (int64_t)blockIdx.x * kRowWaves + wave;
+  const int m0 = blockIdx.y * MT;
   const int K = (int)A.K, nch = K / W::PER;
   const int64_t crow = W::FP8 ? K : K / 2, srow = (int64_t)SB * nch;
-  __amdgpu_buffer_rsrc_t cb[R], sb[R];
-#pragma unroll
-  for (int t = 0; t < R; ++t) {
-    const bool in = n0 + t < A.N;
-    cb[t] = buffer_of(A.codes + (in ? n0 + t : 0) * crow, in ? crow : 0);
-    if constexpr (SB > 0) sb[t] = buffer_of(A.scales + (in ? n0 + t : 0) * srow, in ? srow : 0);
-  }
-  u32x4_t w[R];
-  uint32_t sc[R];
-  auto load = [&](int c) {
-#pragma unroll
-    for (int t = 0; t < R; ++t) {
-      w[t] = __builtin_amdgcn_raw_buffer_load_b128(cb[t], 16 * c, 0, 2);
-      sc[t] = 0u;
-      if constexpr (SB == 1) sc[t] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(sb[t], c, 0, 0);
-      if constexpr (SB == 2) sc[t] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(sb[t], 2 * c, 0, 0);
-      if constexpr (SB == 4) sc[t] = __builtin_amdgcn_raw_buffer_load_b32(sb[t], 4 * c, 0, 0);
-    }
+  __amdgpu_buffer_rsrc_t cb, sb;
+  auto turn_to = [&](int64_t row) {
+    const bool in = row < A.N;
+    cb = buffer_of(A.codes + (in ? row : 0) * crow, in ? crow : 0);
+    if constexpr (SB > 0) sb = buffer_of(A.scales + (in ? row : 0) * srow, in ? srow : 0);
   };
-  float acc[R][MT];
-#pragma unroll
-  for (int t = 0; t < R; ++t)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[t][m] = 0.0f;
-  load(lane);
-  const int m0 = blockIdx.y * MT;
-  for (int k0 = 0; k0 < K; k0 += SLAB) {
-    const int end = K - k0 < SLAB ? K - k0 : SLAB;
-    const int steps = (end / W::PER + 63) / 64;        // of 64 chunks, the last one filled up with zeros
-    const int pieces = steps * 64 * NP;
-    if (k0) __syncthreads();
+  struct Chunk {
+    u32x4_t w;
+    uint32_t sc;
+  };
+  auto load = [&](Chunk& d, int c) {
+    d.w = __builtin_amdgcn_raw_buffer_load_b128(cb, 16 * c, 0, 2);
+    d.sc = 0u;
+    if constexpr (SB == 1) d.sc = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(sb, c, 0, 0);
+    if constexpr (SB == 2) d.sc = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(sb, 2 * c, 0, 0);
+    if constexpr (SB == 4) d.sc = __builtin_amdgcn_raw_buffer_load_b32(sb, 4 * c, 0, 0);
+  };
+  // the tokens' values k0 .. k0 + end into LDS, filled up with zeros
+  auto stage = [&](int k0, int end, int pieces) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const u32x4_t* x = reinterpret_cast<const u32x4_t*>(A.x + (m0 + m < A.M ? m0 + m : 0) * A.ldx + k0);
@@ -135,57 +125,89 @@ __global__ __launch_bounds__(64 * kRowWaves) void qgemv_row_kernel(Gemv A) {
         smem[m * pieces + c * NP + (j ^ (c / (16 / NP) % NP))] = 8 * i < end ? x[i] : u32x4_t{0u, 0u, 0u, 0u};
       }
     }
-    __syncthreads();
-    for (int s = 0; s < steps; ++s) {
-      const int c = 64 * s + lane;
-      u32x4_t v[R], xp[MT][NP];
-      uint32_t q[R];
+  };
+  float acc[MT];
 #pragma unroll
-      for (int t = 0; t < R; ++t) {
-        v[t] = w[t];
-        q[t] = sc[t];
-      }
-      load(k0 / W::PER + c + 64);
+  for (int m = 0; m < MT; ++m) acc[m] = 0.0f;
+  auto use = [&](const Chunk& d, int c, int pieces) {  // chunk c of the slab
+    u32x4_t xp[MT][NP];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int j = 0; j < NP; ++j) xp[m][j] = smem[m * pieces + c * NP + (j ^ (c / (16 / NP) % NP))];
+      for (int j = 0; j < NP; ++j) xp[m][j] = smem[m * pieces + c * NP + (j ^ (c / (16 / NP) % NP))];
+    float part[W::NB][MT];
 #pragma unroll
-      for (int t = 0; t < R; ++t) {
-        float part[W::NB][MT];
+    for (int b = 0; b < W::NB; ++b)
 #pragma unroll
-        for (int b = 0; b < W::NB; ++b)
+      for (int m = 0; m < MT; ++m) part[b][m] = 0.0f;
 #pragma unroll
-          for (int m = 0; m < MT; ++m) part[b][m] = 0.0f;
+    for (int pair = 0; pair < W::PER / 2; ++pair) {
+      constexpr int per = W::FP8 ? 2 : 4;
+      const bf16x2_t v = decode_pair<W::FP8>(d.w[pair / per], pair % per);
 #pragma unroll
-        for (int pair = 0; pair < W::PER / 2; ++pair) {
-          constexpr int per = W::FP8 ? 2 : 4;
-          const bf16x2_t d = decode_pair<W::FP8>(v[t][pair / per], pair % per);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            float& p = part[pair * 2 * W::NB / W::PER][m];
-            p = __builtin_amdgcn_fdot2_f32_bf16(
-                d, __builtin_bit_cast(bf16x2_t, (uint32_t)xp[m][pair / 4][pair % 4]), p, false);
-          }
-        }
-#pragma unroll
-        for (int b = 0; b < W::NB; ++b) {
-          const float f = W::SC == 0 ? 1.0f : scale_val(W::SC, q[t], b);
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-            acc[t][m] = W::SC == 0 ? acc[t][m] + part[b][m] : fmaf(part[b][m], f, acc[t][m]);
-        }
+      for (int m = 0; m < MT; ++m) {
+        float& p = part[pair * 2 * W::NB / W::PER][m];
+        p = __builtin_amdgcn_fdot2_f32_bf16(v, __builtin_bit_cast(bf16x2_t, (uint32_t)xp[m][pair / 4][pair % 4]), p,
+                                            false);
       }
     }
-  }
-  const int e = A.texp ? *A.texp : 0;
 #pragma unroll
-  for (int t = 0; t < R; ++t)
+    for (int b = 0; b < W::NB; ++b) {
+      const float f = W::SC == 0 ? 1.0f : scale_val(W::SC, d.sc, b);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[m] = W::SC == 0 ? acc[m] + part[b][m] : fmaf(part[b][m], f, acc[m]);
+    }
+  };
+  auto finish = [&] {
+    const int e = A.texp ? *A.texp : 0;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const float v = wave_sum_f(acc[t][m]);
-      if (lane == 0 && n0 + t < A.N && m0 + m < A.M) store_y(A, m0 + m, n0 + t, ldexpf(v, e));
+      const float v = wave_sum_f(acc[m]);
+      if (lane == 0 && n < A.N && m0 + m < A.M) store_y(A, m0 + m, n, ldexpf(v, e));
+      acc[m] = 0.0f;
     }
+  };
+
+  turn_to(n);
+  Chunk a, b;
+  load(a, lane);
+  if constexpr (WALK) {
+    const int steps = (nch + 63) / 64;                 // of 64 chunks, the last one filled up with zeros
+    const int pieces = steps * 64 * NP;
+    stage(0, K, pieces);
+    __syncthreads();
+    int s = 0;
+    // by turns into a and b, so that no load is waited for to be copied;
+    // true where the wave's last row is done
+    auto step = [&](const Chunk& d, Chunk& ahead) {
+      const bool turn = s + 1 == steps;
+      if (turn) turn_to(n + stride);
+      load(ahead, turn ? lane : 64 * (s + 1) + lane);
+      use(d, 64 * s + lane, pieces);
+      ++s;
+      if (!turn) return false;
+      finish();
+      s = 0;
+      n += stride;
+      return n >= A.N;
+    };
+    while (!step(a, b) && !step(b, a)) {
+    }
+  } else {
+    for (int k0 = 0; k0 < K; k0 += SLAB) {
+      const int end = K - k0 < SLAB ? K - k0 : SLAB;
+      const int steps = (end / W::PER + 63) / 64, pieces = steps * 64 * NP;
+      if (k0) __syncthreads();
+      stage(k0, end, pieces);
+      __syncthreads();
+      for (int s = 0; s < steps; ++s) {
+        b = a;
+        load(a, k0 / W::PER + 64 * (s + 1) + lane);
+        use(b, 64 * s + lane, pieces);
+      }
+    }
+    finish();
+  }
 }
 
 // ------------------------------------------------------------ MFMA form
@@ -368,6 +390,7 @@ __global__ __launch_bounds__(RT == 1 ? 1024 : 512) void qgemv_mfma_kernel(Gemv A
 
 namespace {
 constexpr size_t kMaxLds = 160 * 1024;
+constexpr int64_t kWalkWG = 768;                      // three a CU
 constexpr int64_t kPairMost = 1 << 25;                // weights up to which two tokens take the dot form
 
 // LDS of a workgroup: the waves' pieces and the tile's scales, or the sums.
@@ -385,25 +408,28 @@ hipError_t gemv_mfma(const Gemv& a, int waves, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int FMT, int MT, int R>
+template <int FMT, int MT, bool WALK>
 hipError_t gemv_row(const Gemv& a, hipStream_t s) {
   constexpr int64_t step = 64 * WFmt<FMT>::PER, slab = kRowSlab / MT;
   const int64_t held = a.K < slab ? ceil_div(a.K, step) * step : slab;
-  qgemv_row_kernel<FMT, MT, R><<<dim3((unsigned)ceil_div(a.N, kRowWaves * R), (unsigned)ceil_div(a.M, MT)),
-                                 dim3(64 * kRowWaves), (size_t)held * MT * 2, s>>>(a);
+  int64_t wg = ceil_div(a.N, kRowWaves);
+  if (WALK) wg = ceil_div(wg, ceil_div(wg, kWalkWG));  // as many rounds, the same for nearly all
+  qgemv_row_kernel<FMT, MT, WALK><<<dim3((unsigned)wg, (unsigned)ceil_div(a.M, MT)), dim3(64 * kRowWaves),
+                                    (size_t)held * MT * 2, s>>>(a, wg * kRowWaves);
   return hipGetLastError();
 }
 
 template <int FMT>
 hipError_t gemv_fmt(const Gemv& a, hipStream_t s) {
-  // One token: two rows a wave halve the reads of the token's values in LDS but
-  // leave half the waves (8192 x 28672 NVFP4 23.9 us with two, 26.5 with one;
-  // 4096 x 11008 7.7 and 7.4; 2048 x 2048 3.2 and 2.7).
-  if (a.M == 1) return a.N >= 8192 ? gemv_row<FMT, 1, 2>(a, s) : gemv_row<FMT, 1, 1>(a, s);
+  // One token: a row a wave; beyond what is resident the waves stay and walk on,
+  // with the token in LDS (28672 x 8192 NVFP4 25.1 us, 30.3 as separate
+  // workgroups; 16384 x 4096 9.0 and 11.6; 11008 x 4096 7.1 and 8.3).
+  const bool more = a.N > kWalkWG * kRowWaves;
+  if (a.M == 1) return more && a.K <= kRowSlab ? gemv_row<FMT, 1, true>(a, s) : gemv_row<FMT, 1, false>(a, s);
   // Two tokens: the dot form while the time is mostly latency (NVFP4, dot and
-  // MFMA: 4096 x 4096 4.6 and 5.6 us, 11008 x 4096 9.0 and 8.7, 28672 x 8192
-  // 31.9 and 29.0). With three or four it is never ahead.
-  if (a.M == 2 && a.N * a.K <= kPairMost) return gemv_row<FMT, 2, 1>(a, s);
+  // MFMA: 4096 x 4096 4.7 and 5.6 us, 11264 x 2048 7.0 and 6.2, 28672 x 8192
+  // 31.9 and 29.7). With three or four it is never ahead.
+  if (a.M == 2 && !more && a.N * a.K <= kPairMost) return gemv_row<FMT, 2, false>(a, s);
   constexpr int TPI = WFmt<FMT>::FP8 ? 4 : 2;          // tokens per load
   const int64_t tiles = ceil_div(a.N, 16), stages = ceil_div(a.K, WFmt<FMT>::FP8 ? 128 : 256);
   // More tiles a wave spare reads of the tokens' values, which are as many
@@ -421,7 +447,7 @@ hipError_t gemv_fmt(const Gemv& a, hipStream_t s) {
   if (waves > stages) waves = (int)stages;
   const int xt = a.M <= TPI ? 1 : a.M <= 4 ? 2 : a.M <= 8 ? 8 / TPI : 16 / TPI;
   // A tile's scales stay in LDS; where K is too long for that, token by token.
-  if (mfma_lds<FMT>(a.K, rt, xt, waves) > kMaxLds) return gemv_row<FMT, 1, 1>(a, s);
+  if (mfma_lds<FMT>(a.K, rt, xt, waves) > kMaxLds) return gemv_row<FMT, 1, false>(a, s);
   if (a.M <= TPI) return gemv_mfma<FMT, 1, 1>(a, waves, s);
   if constexpr (TPI == 2)
     if (a.M <= 4) return gemv_mfma<FMT, 1, 2>(a, waves, s);

@@ -225,3 +225,16 @@ def test_other_stream():
         y = S.qgemv(x, w, stream=handle)
         side.synchronize()
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n,k", [(6145, 96), (6152, 2080), (20011, 64), (12296, 4128), (6200, 33024)])
+def test_rows_that_a_wave_walks(fmt, n, k):
+    """One token and more rows than waves: some waves with a row less, rows of
+    one chunk and of several, and a token too long to stay on chip."""
+    if n * k > 1 << 27 and fmt not in (S.FP8, S.NVFP4):
+        pytest.skip("the longest in two formats")
+    w = raw_weights(fmt, n, k, n)
+    say("gemv walk", S.FORMAT_NAMES[fmt], n, k)
+    x = rand((1, k), BF, 62).cuda()
+    check(x, w, S.qgemv(x, w))
