@@ -441,9 +441,12 @@ hipError_t gemv_fmt(const Gemv& a, hipStream_t s) {
   // 14.6; 16384 x 4096 16.8, 14.4, 22.0, 15.9; 28672 x 8192 52.9, 42.8, 51.7, 40.0.
   const int rt = a.M <= 4 || tiles <= 256 ? 1 : tiles <= 512 ? 2 : tiles <= 768 ? 3 : tiles <= 1536 ? 2 : 4;
   // Few tiles: more waves along K (2048 x 28672, 3 tokens: 16.3 us with 16
-  // waves, 18.6 with 8; 11008 x 4096: 12.3 and 9.6). Four tiles a wave: its
-  // loads are long enough (28672 x 8192, 16 tokens: 40.1 us with 4, 46.5 with 8).
-  int waves = rt == 4 ? 4 : tiles <= 256 ? 16 : 8;
+  // waves, 18.6 with 8; 11008 x 4096: 12.3 and 9.6). Four where their loads are
+  // long enough: four tiles a wave (28672 x 8192, 16 tokens: 40.1 us with 4,
+  // 46.5 with 8), or many workgroups of up to 8 stages a wave (4 tokens, 16384 x
+  // 4096: 11.9 us with 4, 14.3 with 8; FP8 28672 x 8192, 16 stages: 45.7 and 41.8).
+  const bool few = rt == 4 || (a.M <= 4 && tiles > 768 && stages <= 32);
+  int waves = few ? 4 : tiles <= 256 ? 16 : 8;
   if (waves > stages) waves = (int)stages;
   const int xt = a.M <= TPI ? 1 : a.M <= 4 ? 2 : a.M <= 8 ? 8 / TPI : 16 / TPI;
   // A tile's scales stay in LDS; where K is too long for that, token by token.
