@@ -286,15 +286,17 @@ __global__ __launch_bounds__(RT == 1 ? 1024 : 512) void qgemv_mfma_kernel(Gemv A
   const int nst = (K + SK - 1) / SK;
 
   u32x4_t wv[RT][2], xv[XT];
-  auto load = [&](int st) {
-    const int k0 = st * SK;
+  auto load_w = [&](int st) {
     const uint32_t co = 128 * st + 16 * (lane & 7) < crow ? coff + 128 * st : kOutside;
-    const uint32_t xo = k0 + 8 * (lane % XP) < K ? xoff + 2 * k0 : kOutside;
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       wv[t][0] = __builtin_amdgcn_raw_buffer_load_b128(cb[t], co, 0, 2);
       wv[t][1] = __builtin_amdgcn_raw_buffer_load_b128(cb[t], co + 8 * crow, 0, 2);
     }
+  };
+  auto load_x = [&](int st) {
+    const int k0 = st * SK;
+    const uint32_t xo = k0 + 8 * (lane % XP) < K ? xoff + 2 * k0 : kOutside;
 #pragma unroll
     for (int i = 0; i < XT; ++i)
       xv[i] = __builtin_amdgcn_raw_buffer_load_b128(xb, xo + i * TPI * (uint32_t)A.ldx * 2, 0, 0);
@@ -305,7 +307,8 @@ __global__ __launch_bounds__(RT == 1 ? 1024 : 512) void qgemv_mfma_kernel(Gemv A
   for (int t = 0; t < RT; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   auto swz = [](int tk) { return HP == 16 ? tk : (tk >> 1) & 7; };
   const int tok = r < TOK ? r : TOK - 1;               // columns beyond the tokens are not stored
-  load(wave);
+  load_w(wave);
+  load_x(wave);
   if constexpr (UB > 0) {
     const int64_t rows = A.N - n0 < 16 * RT ? A.N - n0 : 16 * RT;
     const int bytes = (int)rows * srow;                // a multiple of 16 in every tile but the last
@@ -337,12 +340,13 @@ __global__ __launch_bounds__(RT == 1 ? 1024 : 512) void qgemv_mfma_kernel(Gemv A
       lw[128 * t + row * 8 + (pc ^ (row >> 1))] = wv[t][0];
       lw[128 * t + (row + 8) * 8 + (pc ^ ((row + 8) >> 1 & 7))] = wv[t][1];
     }
+    load_w(st + nwave);                                // beyond K: zeros, not used
     const int sk = st * (SK / 32) + kg * (SK / 128);   // the lane's first 32 weights of the stage
     u32x4_t xf[NJ / 2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       put_x(second == (h == 1));
-      if (h == 1) load(st + nwave);                    // beyond K: zeros, not used
+      if (h == 1) load_x(st + nwave);
 #pragma unroll
       for (int i = 0; i < NJ / 2; ++i) xf[i] = lx[tok * HP + ((NJ / 2 * kg + i) ^ swz(tok))];
       wave_fence();
