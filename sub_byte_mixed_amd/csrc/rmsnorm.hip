@@ -216,7 +216,7 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void rmsnorm_bwd_kernel(NormBwd A)
 
   // the next row's loads run while this one is worked on, where the registers
   // suffice for both (two chunks a thread of 1024 spill)
-  constexpr bool AHEAD = VPT == 1;
+  constexpr bool AHEAD = VPT == 1 || !WG;
   for (int it = 0; row < A.rows; ++it, row += step) {
     if (!AHEAD && it > 0) load(row);
     float d[VPT][8], xh[VPT][8], res[VPT][8];
@@ -304,28 +304,37 @@ __global__ __launch_bounds__(256) void dgamma_sum_kernel(const float* part, int6
 }
 
 // ------------------------------------------------------------ statistics
-// The statistics of a forward launch from its workgroups' partials, one a
-// thread, in a fixed order.
-__global__ __launch_bounds__(1024) void op_stats_kernel(const StatPart* part, int n, snip_stats* out) {
-  __shared__ double dred[32];
-  __shared__ uint32_t ured[32];
-  static_assert(kOpsWG <= 1024, "one partial a thread");
-  const int i = threadIdx.x;
-  const StatPart p = i < n ? part[i] : StatPart{0.0, 0.0, 0u, 0u};
+// The statistics of a forward launch from its workgroups' partials, in a fixed
+// order.
+__global__ __launch_bounds__(256) void op_stats_kernel(const StatPart* part, int n, snip_stats* out) {
+  __shared__ double dred[8];
+  __shared__ uint32_t ured[8];
+  StatPart p{0.0, 0.0, 0u, 0u};
+#pragma unroll
+  for (int j = 0; j < kOpsWG / 256; ++j) {
+    const int i = threadIdx.x + 256 * j;
+    if (i < n) {
+      const StatPart o = part[i];
+      p.e2 += o.e2;
+      p.x2 += o.x2;
+      p.nf += o.nf;
+      p.amax_bits = max(p.amax_bits, o.amax_bits);
+    }
+  }
   const double e2 = wave_sum(p.e2), x2 = wave_sum(p.x2);
   const uint32_t nf = wave_sum_u(p.nf), am = wave_max_u(p.amax_bits);
-  const int wave = i >> 6;
-  if ((i & 63) == 0) {
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) {
     dred[2 * wave] = e2;
     dred[2 * wave + 1] = x2;
     ured[2 * wave] = nf;
     ured[2 * wave + 1] = am;
   }
   __syncthreads();
-  if (i == 0) {
+  if (threadIdx.x == 0) {
     snip_stats s{0.0, 0.0, 0.0f, 0u};
     uint32_t m = 0u;
-    for (int w = 0; w < 16; ++w) {
+    for (int w = 0; w < 4; ++w) {
       s.sum_err2 += dred[2 * w];
       s.sum_x2 += dred[2 * w + 1];
       s.n_nonfinite += ured[2 * w];
@@ -337,7 +346,7 @@ __global__ __launch_bounds__(1024) void op_stats_kernel(const StatPart* part, in
 }
 
 hipError_t launch_op_stats(const StatPart* part, int n, snip_stats* out, hipStream_t s) {
-  op_stats_kernel<<<dim3(1), dim3(1024), 0, s>>>(part, n, out);
+  op_stats_kernel<<<dim3(1), dim3(256), 0, s>>>(part, n, out);
   return hipGetLastError();
 }
 
@@ -348,14 +357,17 @@ struct NormShape {
   int vpt, threads;
 };
 
-// A chunk a thread up to `one_up_to` chunks, two beyond. The forward pass
-// takes two beyond 4096 columns (4096 x 8192 bf16 to FP8: 44.4 us, 46.4 with
-// one and 1024 threads); the backward pass, with its column sums, is short of
-// registers then and takes two where it must (4096 x 8192, fp32 residual: 67 us
-// with one, 83 with two; 1003 x 4104: 14.1 and 16.3).
+// A wave to a row up to 1024 columns, two chunks a lane beyond 512 (16384 x 640,
+// fp32 residual: forward to bf16 and FP8 27.6 us, 33.0 as workgroups of 128;
+// backward 24.6 and 36.6). Wider, a workgroup with a chunk a thread up to
+// `one_up_to` chunks, two beyond. The forward pass takes two beyond 4096 columns
+// (4096 x 8192 bf16 to FP8: 44.4 us, 46.4 with one and 1024 threads); the
+// backward pass, with its column sums, is short of registers then and takes two
+// where it must (4096 x 8192, fp32 residual: 67 us with one, 83 with two; 1003 x
+// 4104: 14.1 and 16.3).
 NormShape norm_shape(int64_t cols, int one_up_to) {
   const int64_t ch = ceil_div(cols, 8);
-  if (ch <= 64) return {false, 1, 256};
+  if (ch <= 128) return {false, ch <= 64 ? 1 : 2, 256};
   const int vpt = ch <= one_up_to ? 1 : 2;
   return {true, vpt, (int)(64 * ceil_div(ch, 64 * vpt))};
 }
@@ -371,9 +383,10 @@ int norm_wg(const NormShape& k, int64_t rows, int most) {
 template <class F>
 void with_shape(const NormShape& k, F f) {
   using one = std::integral_constant<int, 1>;
-  if (!k.wg) return f(std::false_type{}, one{});
+  using two = std::integral_constant<int, 2>;
+  if (!k.wg) return k.vpt == 1 ? f(std::false_type{}, one{}) : f(std::false_type{}, two{});
   if (k.vpt == 1) return f(std::true_type{}, one{});
-  return f(std::true_type{}, std::integral_constant<int, 2>{});
+  return f(std::true_type{}, two{});
 }
 
 // f(F32) for a matrix's type; an absent one counts as bf16.

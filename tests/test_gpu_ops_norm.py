@@ -210,3 +210,12 @@ def test_other_stream():
         side.synchronize()
         assert torch.equal(y, y0) and torch.equal(q.codes, q0.codes) and torch.equal(st, st0)
         assert torch.equal(dx, dx0) and torch.equal(dg, dg0)
+
+
+@pytest.mark.parametrize("rows,cols", [(7, 513), (300, 520), (41, 777), (1030, 1008), (9, 1024), (3, 1025)])
+@pytest.mark.parametrize("xt,rt,gt", [(BF, F32, BF), (F32, None, F32)])
+def test_widths_of_two_chunks_a_lane(rows, cols, xt, rt, gt):
+    """Rows that a wave holds in two chunks a lane, and the width just beyond."""
+    test_forward(rows, cols, xt, rt, gt)
+    test_backward(rows, cols, xt, BF, rt, gt)
+    test_backward(rows, cols, xt, F32, rt, gt)
