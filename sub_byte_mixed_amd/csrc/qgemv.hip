@@ -443,7 +443,7 @@ hipError_t gemv_fmt(const Gemv& a, hipStream_t s) {
   // NVFP4, 16 tokens, one, two, three and four tiles: 4096 x 4096 7.5, 9.1, -,
   // 13.6 us; 7168 x 4096 10.6, 9.5, 11.5, 16.6; 11008 x 4096 14.9, 13.8, 12.4,
   // 14.6; 16384 x 4096 16.8, 14.4, 22.0, 15.9; 28672 x 8192 52.9, 42.8, 51.7, 40.0.
-  const int rt = a.M <= 4 || tiles <= 256 ? 1 : tiles <= 512 ? 2 : tiles <= 768 ? 3 : tiles <= 1536 ? 2 : 4;
+  int rt = a.M <= 4 || tiles <= 256 ? 1 : tiles <= 512 ? 2 : tiles <= 768 ? 3 : tiles <= 1536 ? 2 : 4;
   // Few tiles: more waves along K (2048 x 28672, 3 tokens: 16.3 us with 16
   // waves, 18.6 with 8; 11008 x 4096: 12.3 and 9.6). Four where their loads are
   // long enough: four tiles a wave (28672 x 8192, 16 tokens: 40.1 us with 4,
@@ -453,8 +453,13 @@ hipError_t gemv_fmt(const Gemv& a, hipStream_t s) {
   int waves = few ? 4 : tiles <= 256 ? 16 : 8;
   if (waves > stages) waves = (int)stages;
   const int xt = a.M <= TPI ? 1 : a.M <= 4 ? 2 : a.M <= 8 ? 8 / TPI : 16 / TPI;
-  // A tile's scales stay in LDS; where K is too long for that, token by token.
-  if (mfma_lds<FMT>(a.K, rt, xt, waves) > kMaxLds) return gemv_row<FMT, 1, false>(a, s);
+  // The tiles' scales stay in LDS: for a long K fewer tiles, then fewer waves
+  // (bf16 scales of 16, 28672 x 28672, 16 tokens: 254 us, 1220 token by token;
+  // 24593 x 14400: 152 and 601), and where that does not do, token by token.
+  const auto over = [&] { return mfma_lds<FMT>(a.K, rt, xt, waves) > kMaxLds; };
+  while (over() && rt > 1) --rt;
+  while (over() && waves > 4) waves /= 2;
+  if (over()) return gemv_row<FMT, 1, false>(a, s);
   if (a.M <= TPI) return gemv_mfma<FMT, 1, 1>(a, waves, s);
   if constexpr (TPI == 2)
     if (a.M <= 4) return gemv_mfma<FMT, 1, 2>(a, waves, s);

@@ -238,3 +238,23 @@ def test_rows_that_a_wave_walks(fmt, n, k):
     say("gemv walk", S.FORMAT_NAMES[fmt], n, k)
     x = rand((1, k), BF, 62).cuda()
     check(x, w, S.qgemv(x, w))
+
+
+@pytest.mark.parametrize("fmt,n,k,m", [(S.FP4_BF16_B16, 24593, 14400, 16), (S.NVFP4, 24593, 26112, 7), (S.NVFP4, 4001, 73728, 16),
+                                       (S.FP4_BF16_B16, 8209, 33024, 5)])
+def test_scales_of_long_rows(fmt, n, k, m):
+    """Rows so long that the scales of as many tiles, or beside as many waves,
+    as usual do not fit on chip: the first and the last rows of the result."""
+    w = S.QuantizedTensor(fmt, n, k, "cuda")
+    block, kind, *_ = S.FP4_LAYOUT[fmt]
+    per = (k // block) * (2 if kind == "bf16" else 1)
+    small = raw_weights(fmt, 50, k, 15)
+    at = torch.arange(n, device="cuda") % 50                          # row i holds row i % 50
+    w.codes.view(n, k // 2).copy_(small.codes.view(50, k // 2)[at])
+    w.scales.view(n, per).copy_(small.scales.view(50, per)[at])
+    w.texp.copy_(small.texp)
+    x = rand((m, k), BF, 63).cuda()
+    say("long rows", S.FORMAT_NAMES[fmt], n, k, m)
+    y = S.qgemv(x, w)
+    check(x, small, y[:, :50])
+    assert torch.equal(y, y[:, :50][:, at])
