@@ -429,7 +429,13 @@ hipError_t gemv_fmt(const Gemv& a, hipStream_t s) {
   // with the token in LDS (28672 x 8192 NVFP4 25.1 us, 30.3 as separate
   // workgroups; 16384 x 4096 9.0 and 11.6; 11008 x 4096 7.1 and 8.3).
   const bool more = a.N > kWalkWG * kRowWaves;
-  if (a.M == 1) return more && a.K <= kRowSlab ? gemv_row<FMT, 1, true>(a, s) : gemv_row<FMT, 1, false>(a, s);
+  // Many rows that fill no more than half of a wave's load go to the MFMA form
+  // (50000 x 1024: 13.1 us here and 10.4 there; 100000 x 512: 21.4 and 10.6, FP8
+  // 18.3 and 13.5), but for bf16 scales, which it pays twice (16384 x 1024: 5.9
+  // and 6.9).
+  const bool half = WFmt<FMT>::SC != 3 && 2 * a.K <= 64 * WFmt<FMT>::PER;
+  if (a.M == 1 && !(more && half))
+    return more && a.K <= kRowSlab ? gemv_row<FMT, 1, true>(a, s) : gemv_row<FMT, 1, false>(a, s);
   // Two tokens: the dot form while the time is mostly latency (NVFP4, dot and
   // MFMA: 4096 x 4096 4.7 and 5.6 us, 11264 x 2048 7.0 and 6.2, 28672 x 8192
   // 31.9 and 29.7). With three or four it is never ahead.
