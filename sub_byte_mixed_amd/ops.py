@@ -137,12 +137,14 @@ _ANY = (torch.bfloat16, torch.float32)
 
 
 def _quant_out(q, out_fmt, rows, cols, dev, amax, stats, with_stats, ws, sizer):
-    """The quantized output of a forward call: (q, stats, their arguments of
-    the C call: descriptor, maximum, statistics, workspace address and size)."""
+    """The quantized output of a forward call: (q, stats, ws, their arguments
+    of the C call: descriptor, maximum, statistics, workspace address and
+    size). The caller holds ws until that call has returned: memory given back
+    before its kernels are enqueued may be another call's by then."""
     if q is None and out_fmt is None:
         if stats is not None:
             raise ValueError("stats belong to a quantized output (out_fmt or q)")
-        return None, None, (None, None, None, None, 0)
+        return None, None, ws, (None, None, None, None, 0)
     if q is None:
         q = _S.QuantizedTensor(out_fmt, rows, cols, dev)
     elif out_fmt is not None and q.format != out_fmt:
@@ -153,7 +155,7 @@ def _quant_out(q, out_fmt, rows, cols, dev, amax, stats, with_stats, ws, sizer):
         raise ValueError(f"stats must be a statistics tensor (new_stats) on GPU {dev}")
     if ws is None and (stats is not None or (amax is None and q.format != _S.MXFP4)):
         ws = torch.empty(sizer(rows, cols, q.format), dtype=torch.uint8, device=dev)
-    return q, stats, (_operand(q, "q", dev), _S._amax_ptr(amax), _S._ptr(stats), *_scratch(ws, dev))
+    return q, stats, ws, (_operand(q, "q", dev), _S._amax_ptr(amax), _S._ptr(stats), *_scratch(ws, dev))
 
 
 def rmsnorm_fwd(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, res: Optional[torch.Tensor] = None,
@@ -186,8 +188,8 @@ def rmsnorm_fwd(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, res: Op
     if rstd is None and with_rstd:
         rstd = torch.empty(rows, dtype=torch.float32, device=dev)
     L = _S.lib()
-    q, stats, (d, pa, ps, *pw) = _quant_out(q, out_fmt, rows, cols, dev, amax, stats, with_stats, ws,
-                                            L.snipop_rmsnorm_fwd_workspace)
+    q, stats, ws, (d, pa, ps, *pw) = _quant_out(q, out_fmt, rows, cols, dev, amax, stats, with_stats, ws,
+                                                L.snipop_rmsnorm_fwd_workspace)
     _S._check(L.snipop_rmsnorm_fwd(
         *px, *pr, pg, _TYPES[gamma.dtype], rows, cols, eps, *_mat(h, "h", rows, cols, dev),
         *_mat(y, "y", rows, cols, dev), _vec(rstd, "rstd", rows, _F32, dev), d, rounding, seed, tensor_id, pa, ps, *pw,
@@ -243,8 +245,8 @@ def swiglu_fwd(gate: torch.Tensor, up: torch.Tensor, y: Optional[torch.Tensor] =
     if y is None and with_y:
         y = _new(rows, cols, y_dtype, dev)
     L = _S.lib()
-    q, stats, (d, pa, ps, *pw) = _quant_out(q, out_fmt, rows, cols, dev, amax, stats, with_stats, ws,
-                                            L.snipop_swiglu_fwd_workspace)
+    q, stats, ws, (d, pa, ps, *pw) = _quant_out(q, out_fmt, rows, cols, dev, amax, stats, with_stats, ws,
+                                                L.snipop_swiglu_fwd_workspace)
     _S._check(L.snipop_swiglu_fwd(
         pg, lg, pu, lu, tg, rows, cols, *_mat(y, "y", rows, cols, dev), d, rounding, seed, tensor_id, pa, ps, *pw,
         _current_stream(dev)))

@@ -1,0 +1,92 @@
+"""The operators' binding (sub_byte_mixed_amd/ops.py) without a GPU: the calls
+on CPU stand-ins for GPU tensors, with the library's launching entries stubbed
+and its sizers real."""
+import os
+import weakref
+
+import pytest
+import torch
+
+import sub_byte_mixed_amd as S
+from sub_byte_mixed_amd import ops
+
+BF, F32 = torch.bfloat16, torch.float32
+HERE = -1                                              # what get_device() says of a CPU tensor
+
+
+class Library:
+    """libsnip with its launching entries replaced by `launch(name, args)`."""
+
+    def __init__(self, real, launch):
+        self.real, self.launch = real, launch
+
+    def __getattr__(self, name):
+        if name.startswith("snipop_") and not name.endswith("_workspace"):
+            return lambda *a: self.launch(name, a)
+        return getattr(self.real, name)
+
+
+class Stand:
+    """CPU tensors taken for those of device -1; `made`: what was allocated."""
+
+    def __init__(self, monkeypatch):
+        if not os.path.exists(S.LIB_PATH):
+            from sub_byte_mixed_amd import build
+            build.build()
+        self.made, self.calls, self.during = [], [], None
+        real, empty, zeros = S.lib(), torch.empty, torch.zeros
+
+        def cpu(make):
+            def f(*a, device=None, **k):
+                t = make(*a, device="cpu" if device == HERE else device, **k)
+                self.made.append((weakref.ref(t), t.data_ptr(), t.nbytes))
+                return t
+            return f
+
+        def launch(name, args):
+            self.calls.append((name, args))
+            if self.during:
+                self.during(name, args)
+            return 0
+        monkeypatch.setattr(torch, "empty", cpu(empty))
+        monkeypatch.setattr(torch, "zeros", cpu(zeros))
+        monkeypatch.setattr(S, "lib", lambda: Library(real, launch))
+        monkeypatch.setattr(ops, "_device", lambda t, fn: t.get_device())
+        monkeypatch.setattr(ops, "_current_device", lambda: HERE)
+        monkeypatch.setattr(ops, "_current_stream", lambda dev: 0)
+
+    def alive(self, address, size):
+        return any(r() is not None and p == address and n >= size for r, p, n in self.made)
+
+
+@pytest.fixture
+def stand(monkeypatch):
+    return Stand(monkeypatch)
+
+
+@pytest.mark.parametrize("fmt", [S.FP8, S.NVFP4, S.MXFP4])
+def test_workspace_lives_until_the_launches_are_enqueued(stand, fmt):
+    """A workspace that a call allocates for itself is still held when the
+    library runs: memory given back earlier may be another call's by then."""
+    def during(name, args):
+        ws, size = args[-3:-1]
+        assert ws and size and stand.alive(ws, size), name
+    stand.during = during
+    x, gamma = torch.ones((4, 64), dtype=BF), torch.ones(64, dtype=BF)
+    S.rmsnorm_fwd(x, gamma, out_fmt=fmt)
+    S.rmsnorm_fwd(x, gamma, with_y=False, with_rstd=False, out_fmt=fmt)
+    S.swiglu_fwd(x, x, out_fmt=fmt)
+    S.swiglu_fwd(x, x, with_y=False, q=S.QuantizedTensor(fmt, 4, 64, HERE))
+    if fmt != S.MXFP4:                                 # to find the maximum alone
+        S.rmsnorm_fwd(x, gamma, out_fmt=fmt, with_stats=False)
+        S.swiglu_fwd(x, x, out_fmt=fmt, with_stats=False)
+    assert len(stand.calls) == (4 if fmt == S.MXFP4 else 6)
+
+
+def test_workspace_of_the_backward_norm_lives_as_long(stand):
+    def during(name, args):
+        assert stand.alive(*args[-3:-1]), name
+    stand.during = during
+    x = torch.ones((4, 64), dtype=BF)
+    S.rmsnorm_bwd(x, x, torch.ones(64, dtype=BF), torch.ones(4))
+    assert len(stand.calls) == 1
