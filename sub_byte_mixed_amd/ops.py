@@ -120,14 +120,18 @@ def _device(t: torch.Tensor, fn) -> int:
 
 
 def _elsewhere(fn, dev: int, stream, *args):
-    """fn(*args) on device `dev` and on `stream` (a torch stream, a handle, or
-    None for the device's current one): what it allocates then belongs to the
-    stream that its kernels run on."""
+    """fn(*args) on device `dev` and on `stream` (a torch stream of that
+    device, an object with a stream's handle as cuda_stream, a handle, or None
+    for the device's current one): what it allocates then belongs to the stream
+    that its kernels run on."""
     if stream is None:
         with torch.cuda.device(dev):
             return fn(*args)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), dev) if int(stream) else torch.cuda.default_stream(dev)
+        handle = int(getattr(stream, "cuda_stream", stream))
+        stream = torch.cuda.ExternalStream(handle, dev) if handle else torch.cuda.default_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream= is a stream of GPU {stream.device_index}, the tensors of {fn.__name__} lie on GPU {dev}")
     with torch.cuda.stream(stream):
         return fn(*args)
 

@@ -1,6 +1,7 @@
 """The operators' binding (sub_byte_mixed_amd/ops.py) without a GPU: the calls
 on CPU stand-ins for GPU tensors, with the library's launching entries stubbed
 and its sizers real."""
+import contextlib
 import os
 import weakref
 
@@ -90,3 +91,73 @@ def test_workspace_of_the_backward_norm_lives_as_long(stand):
     x = torch.ones((4, 64), dtype=BF)
     S.rmsnorm_bwd(x, x, torch.ones(64, dtype=BF), torch.ones(4))
     assert len(stand.calls) == 1
+
+
+class Streams:
+    """torch.cuda's streams for the stand-ins: `stream(s)` makes s the current
+    one and its device the current device, as torch's does."""
+
+    class Stream:
+        def __init__(self, handle, device_index):
+            self.cuda_stream, self.device_index = handle, device_index
+            self.device = torch.device("cpu")
+
+    class ExternalStream(Stream):
+        pass
+
+    def __init__(self, monkeypatch):
+        self.device, self.current = HERE, {HERE: 0, 3: 30}
+        monkeypatch.setattr(torch.cuda, "Stream", self.Stream)
+        monkeypatch.setattr(torch.cuda, "ExternalStream", self.ExternalStream)
+        monkeypatch.setattr(torch.cuda, "default_stream", lambda dev: self.Stream(0, dev))
+        monkeypatch.setattr(torch.cuda, "stream", lambda s: self.switch(s.device_index, s.cuda_stream))
+        monkeypatch.setattr(torch.cuda, "device", lambda dev: self.switch(dev, self.current[dev]))
+        monkeypatch.setattr(ops, "_current_device", lambda: self.device)
+        monkeypatch.setattr(ops, "_current_stream", lambda dev: self.current[dev])
+
+    @contextlib.contextmanager
+    def switch(self, device, handle):
+        was = self.device, dict(self.current)
+        self.device, self.current[device] = device, handle
+        yield
+        self.device, self.current = was
+
+
+def calls_with(stream):
+    """Each entry of the binding on `stream`."""
+    x, gamma, rstd = torch.ones((4, 64), dtype=BF), torch.ones(64, dtype=BF), torch.ones(4)
+    w = S.QuantizedTensor(S.NVFP4, 8, 64, HERE)
+    return [lambda: S.rmsnorm_fwd(x, gamma, out_fmt=S.FP8, stream=stream), lambda: S.rmsnorm_bwd(x, x, gamma, rstd, stream=stream),
+            lambda: S.swiglu_fwd(x, x, stream=stream), lambda: S.swiglu_bwd(x, x, x, stream=stream),
+            lambda: S.qgemv(x, w, stream=stream)]
+
+
+def test_a_stream_of_another_device_is_refused(stand, monkeypatch):
+    streams = Streams(monkeypatch)
+    for call in calls_with(streams.Stream(31, 3)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+    assert not stand.calls and streams.device == HERE
+
+
+def test_streams_and_handles_reach_the_library(stand, monkeypatch):
+    """A stream, its handle, the default stream's handle, and any object with
+    the attribute that the package's other calls read."""
+    class Foreign:
+        cuda_stream = 77
+    streams = Streams(monkeypatch)
+    for stream, handle in ((streams.Stream(11, HERE), 11), (12, 12), (0, 0), (Foreign(), 77)):
+        stand.calls.clear()
+        for call in calls_with(stream):
+            call()
+        assert [a[-1] for _, a in stand.calls] == [handle] * 5
+    assert streams.device == HERE and streams.current[HERE] == 0
+
+
+def test_tensors_of_another_device_run_there(stand, monkeypatch):
+    streams = Streams(monkeypatch)
+    streams.device = 3
+    stand.calls.clear()
+    for call in calls_with(None):
+        call()
+    assert [a[-1] for _, a in stand.calls] == [0] * 5 and streams.device == 3
