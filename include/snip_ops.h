@@ -129,8 +129,12 @@ int snipop_swiglu_bwd(const void* dy, int dy_type, int64_t lddy, const void* gat
  *              (FP8_E4M3, NVFP4, MXFP4 and the FP4 variants); K % 32 == 0;
  *              N <= 2^31, K and ldx <= 2^25.
  *   y          device, y_type, ldy >= N.
- * Products are exact and sums are fp32 in a fixed order that depends on the
- * shapes alone. No workspace.
+ * Products are exact, over the whole range of a scale, and sums are fp32, in a
+ * fixed order that depends on the shapes, and for E8M0 and bf16 scales on
+ * whether some of 16 to 64 neighbouring rows lie at the ends of their range
+ * (E8M0 from 2^126, bf16 from 2^125 and below 2^-125). A block is summed before
+ * its scale, and a row before 2^tensor_exp: |x| below 2^90 keeps these sums
+ * within fp32 at any length. No workspace.
  * Errors: NULL, SHAPE, ALIGN, FORMAT, HIP. */
 int snipop_qgemv(const void* x, int64_t ldx, int64_t tokens, const snip_qtensor* w,
                  void* y, int y_type, int64_t ldy, void* stream);

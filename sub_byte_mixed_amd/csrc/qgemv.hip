@@ -217,7 +217,8 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 // 8 weights (one code word of E2M1, two of E4M3) with their block scale ->
 // 8 bf16. E4M3 codes, and E2M1 times an E4M3 or E8M0 scale (6 and 2
 // significant bits), are exact in bf16. E2M1 times a bf16 scale has up to 9
-// bits: it is the exact sum of `hi` and `lo`.
+// bits: it is the exact sum of `hi` and `lo`. Scales for which that does not
+// hold (beyond_bf16) do not come here.
 template <int FMT>
 __device__ __forceinline__ void decode8(const u32x4_t& w, int i, float s, bf16x8_t& hi, bf16x8_t& lo) {
   using W = WFmt<FMT>;
@@ -243,6 +244,60 @@ __device__ __forceinline__ void decode8(const u32x4_t& w, int i, float s, bf16x8
   }
   hi = __builtin_bit_cast(bf16x8_t, h);
   if constexpr (W::SC == 3) lo = __builtin_bit_cast(bf16x8_t, l);
+}
+
+// Nonzero at 0x80808080 (E8M0) or 0x80008000 (bf16) where a scale of the word
+// has no exact product with every code: E8M0 from 2^126 on, where 4 times it
+// leaves bf16 (and NaN); bf16 from 2^125 on, and below 2^-125, where the last
+// of the 9 bits does. A scale of 0 (a block of zeros) is none of them. 1 and 3
+// operations a scale, once a workgroup.
+template <int SC>
+__device__ __forceinline__ uint32_t beyond_bf16(uint32_t w) {
+  if constexpr (SC == 2) return ~(w + 0x03030303u) & w;      // a byte of 253 or more
+  const uint32_t v = w & 0x7FFF7FFFu;
+  return (v + 0x02000200u) | (~(v + 0x7F007F00u) & (v + 0x7FFF7FFFu));
+}
+template <int SC>
+constexpr uint32_t beyond_mask() {
+  return SC == 2 ? 0x80808080u : 0x80008000u;
+}
+
+// The tile of 16 RT rows from n0 on without that product, as the dot form: a
+// row and token a wave, sums of codes times tokens and the scale on them. For
+// tiles with a scale beyond_bf16: no quantizer writes one for finite values,
+// unless they are below 2^-122 and have bf16 scales.
+template <int FMT, int RT>
+__device__ __forceinline__ void tile_by_dots(const Gemv& A, int64_t n0, const uint8_t* lsc, int srow, int lane, int wave,
+                                             int nwave) {
+  using W = WFmt<FMT>;
+  constexpr int PB = W::BLK / 8;                       // code words of a block
+  const int words = (int)A.K / 8;
+  for (int i = wave; i < 16 * RT * A.M; i += nwave) {
+    const int row = i / A.M, m = i % A.M;
+    if (n0 + row >= A.N) break;
+    const uint32_t* codes = reinterpret_cast<const uint32_t*>(A.codes + (n0 + row) * (A.K / 2));
+    const u32x4_t* x = reinterpret_cast<const u32x4_t*>(A.x + m * A.ldx);
+    float sum = 0.0f;
+#pragma unroll 1                                       // no more registers than the usual path
+    for (int c = lane; c < words; c += 64) {
+      const uint8_t* q = lsc + row * srow + c / PB * (W::SC == 3 ? 2 : 1);
+      uint32_t sc;
+      if constexpr (W::SC == 3)
+        sc = *reinterpret_cast<const uint16_t*>(q);
+      else
+        sc = *q;
+      const u32x4_t xp = x[c];
+      const uint32_t w = codes[c];
+      float part = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        part = __builtin_amdgcn_fdot2_f32_bf16(decode_pair<false>(w, j), __builtin_bit_cast(bf16x2_t, (uint32_t)xp[j]),
+                                               part, false);
+      sum = fmaf(part, scale_val(W::SC, sc, 0), sum);
+    }
+    sum = wave_sum_f(sum);
+    if (lane == 0) store_y(A, m, n0 + row, sum);
+  }
 }
 
 // Orders the LDS accesses of a wave's lanes: LDS serves a wave's instructions
@@ -313,11 +368,38 @@ __global__ __launch_bounds__(RT == 1 ? 1024 : 512) void qgemv_mfma_kernel(Gemv A
     const int64_t rows = A.N - n0 < 16 * RT ? A.N - n0 : 16 * RT;
     const int bytes = (int)rows * srow;                // a multiple of 16 in every tile but the last
     const uint8_t* src = A.scales + n0 * srow;         // 16-byte aligned: n0 % 16 == 0
-    for (int i = threadIdx.x; i < bytes / 16; i += blockDim.x)
-      reinterpret_cast<u32x4_t*>(lsc)[i] = reinterpret_cast<const u32x4_t*>(src)[i];
-    for (int i = (bytes & ~15) + threadIdx.x; i < 16 * RT * srow; i += blockDim.x)
+    uint32_t odd = 0u;
+    for (int i = threadIdx.x; i < bytes / 16; i += blockDim.x) {
+      const u32x4_t v = reinterpret_cast<const u32x4_t*>(src)[i];
+      reinterpret_cast<u32x4_t*>(lsc)[i] = v;
+      if constexpr (W::SC >= 2) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) odd |= beyond_bf16<W::SC>(v[j]);
+      }
+    }
+    for (int i = (bytes & ~15) + threadIdx.x; i < 16 * RT * srow; i += blockDim.x) {
       lsc[i] = i < bytes ? src[i] : 0;                 // rows beyond N: zeros
-    __syncthreads();
+      if constexpr (W::SC == 2)
+        if (i < bytes) odd |= beyond_bf16<2>(src[i]);
+      if constexpr (W::SC == 3)
+        if (i < bytes && i % 2 == 0) odd |= beyond_bf16<3>(src[i] | (uint32_t)src[i + 1] << 8);
+    }
+    if constexpr (W::SC >= 2) {
+      // each wave's word goes into every wave's own pieces, which that wave
+      // alone overwrites later: 16 bytes more of LDS would cost a workgroup a
+      // CU (E8M0 of 16, 28672 x 8192, 16 tokens: 34.2 us, 41.8 with them)
+      const bool any = __any((odd & beyond_mask<W::SC>()) != 0u);
+      if (lane < nwave) reinterpret_cast<uint32_t*>(smem + lane * (TOK * HP + 128 * RT))[wave] = any;
+      __syncthreads();
+      const bool beyond = __any(lane < nwave && reinterpret_cast<const uint32_t*>(lx)[lane < nwave ? lane : 0] != 0u);
+      wave_fence();
+      if (beyond) {
+        tile_by_dots<FMT, RT>(A, n0, lsc, srow, lane, wave, nwave);
+        return;
+      }
+    } else {
+      __syncthreads();
+    }
   }
   // piece p of a token's stage belongs to k group p / NJ, and to half
   // (p % NJ) / (NJ / 2) of it
