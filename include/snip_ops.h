@@ -127,7 +127,7 @@ int snipop_swiglu_bwd(const void* dy, int dy_type, int64_t lddy, const void* gat
  *   x          device bf16, ldx; 1 <= tokens <= SNIPOP_QGEMV_MAX_TOKENS.
  *   w          host descriptor: N = w->rows, K = w->k; any format but BF16
  *              (FP8_E4M3, NVFP4, MXFP4 and the FP4 variants); K % 32 == 0;
- *              N <= 2^31, K and ldx <= 2^25.
+ *              N <= 2^31, K and ldx <= 2^25, N K <= 2^40.
  *   y          device, y_type, ldy >= N.
  * Products are exact, over the whole range of a scale, and sums are fp32, in a
  * fixed order that depends on the shapes, and for E8M0 and bf16 scales on

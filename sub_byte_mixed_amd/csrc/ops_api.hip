@@ -286,6 +286,8 @@ int snipop_qgemv(const void* x, int64_t ldx, int64_t tokens, const snip_qtensor*
   if (w->rows > (int64_t)1 << 31 || w->k > kMaxK || ldx > kMaxK)
     return fail(SNIP_E_SHAPE, "%s: N=%lld above 2^31, or K=%lld or ldx=%lld above 2^25", who, (long long)w->rows,
                 (long long)w->k, (long long)ldx);
+  if (w->rows > ((int64_t)1 << 40) / w->k)              // a workgroup for 8 rows of a long K: 2^32 threads a grid
+    return fail(SNIP_E_SHAPE, "%s: N=%lld times K=%lld above 2^40", who, (long long)w->rows, (long long)w->k);
   if ((rc = check_type(who, "y", y_type))) return rc;
   if (ldx < w->k || ldx % 8)
     return fail(SNIP_E_SHAPE, "%s: ldx=%lld must be >= K=%lld and a multiple of 8", who, (long long)ldx,

@@ -325,7 +325,8 @@ __global__ __launch_bounds__(RT == 1 ? 1024 : 512) void qgemv_mfma_kernel(Gemv A
   u32x4_t* lw = lx + TOK * HP;                         // [RT][16][8] pieces, swizzled by the row
   const int K = (int)A.K;
   const int crow = W::FP8 ? K : K / 2, srow = UB * (K / 32);
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
+  const int64_t n0 = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (16 * RT);
+  if (n0 >= A.N) return;                               // the grid's last row is filled up
 
   __amdgpu_buffer_rsrc_t cb[RT];
 #pragma unroll
@@ -478,6 +479,7 @@ namespace {
 constexpr size_t kMaxLds = 160 * 1024;
 constexpr int64_t kWalkWG = 768;                      // three a CU
 constexpr int64_t kPairMost = 1 << 25;                // weights up to which two tokens take the dot form
+constexpr int64_t kGridRow = 1 << 20;                 // workgroups of a grid's row: fewer than 2^32 threads
 
 // LDS of a workgroup: the waves' pieces and the tile's scales, or the sums.
 template <int FMT>
@@ -489,7 +491,8 @@ size_t mfma_lds(int64_t K, int rt, int xt, int waves) {
 
 template <int FMT, int RT, int XT>
 hipError_t gemv_mfma(const Gemv& a, int waves, hipStream_t s) {
-  qgemv_mfma_kernel<FMT, RT, XT><<<dim3((unsigned)ceil_div(a.N, 16 * RT)), dim3(64 * waves),
+  const int64_t wg = ceil_div(a.N, 16 * RT), row = wg < kGridRow ? wg : kGridRow;
+  qgemv_mfma_kernel<FMT, RT, XT><<<dim3((unsigned)row, (unsigned)ceil_div(wg, row)), dim3(64 * waves),
                                    mfma_lds<FMT>(a.K, RT, XT, waves), s>>>(a);
   return hipGetLastError();
 }

@@ -161,3 +161,17 @@ def test_tensors_of_another_device_run_there(stand, monkeypatch):
     for call in calls_with(None):
         call()
     assert [a[-1] for _, a in stand.calls] == [0] * 5 and streams.device == 3
+
+
+def test_qgemv_weights_beyond_a_grid_are_refused(stand):
+    """2^40 weights are more than a card holds; within them every launch's
+    grid has fewer than 2^32 threads a dimension."""
+    import ctypes
+    at = 0x7F0000000000                                # made up, never touched
+    L = S.lib().real
+
+    def gemv(n, k):
+        w = S.QTensorDesc(S.NVFP4, 0, n, k, at, at, at)
+        return L.snipop_qgemv(at, k, 1, ctypes.byref(w), at, 0, n, None)
+    assert gemv(1 << 31, 544) == -2 and "2^40" in L.snip_last_error().decode()
+    assert gemv((1 << 15) + 1, 1 << 25) == -2
