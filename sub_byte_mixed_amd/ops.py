@@ -157,9 +157,12 @@ def _quant_out(q, out_fmt, rows, cols, dev, amax, stats, with_stats, ws, sizer):
         stats = _S.new_stats(1, dev) if with_stats else None
     elif stats.get_device() != dev or stats.nbytes < _S.STATS_BYTES or not stats.is_contiguous():
         raise ValueError(f"stats must be a statistics tensor (new_stats) on GPU {dev}")
+    pa = _S._amax_ptr(amax)
+    if pa is not None and (amax.stats if isinstance(amax, _S.StatsAmax) else amax).get_device() != dev:
+        raise ValueError(f"amax must lie on GPU {dev}")
     if ws is None and (stats is not None or (amax is None and q.format != _S.MXFP4)):
         ws = torch.empty(sizer(rows, cols, q.format), dtype=torch.uint8, device=dev)
-    return q, stats, ws, (_operand(q, "q", dev), _S._amax_ptr(amax), _S._ptr(stats), *_scratch(ws, dev))
+    return q, stats, ws, (_operand(q, "q", dev), pa, _S._ptr(stats), *_scratch(ws, dev))
 
 
 def rmsnorm_fwd(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, res: Optional[torch.Tensor] = None,

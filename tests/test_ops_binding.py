@@ -175,3 +175,21 @@ def test_qgemv_weights_beyond_a_grid_are_refused(stand):
         return L.snipop_qgemv(at, k, 1, ctypes.byref(w), at, 0, n, None)
     assert gemv(1 << 31, 544) == -2 and "2^40" in L.snip_last_error().decode()
     assert gemv((1 << 15) + 1, 1 << 25) == -2
+
+
+class Elsewhere:
+    """What the binding asks of a device tensor, on device 3."""
+    is_cuda, dtype = True, F32
+    data_ptr, numel, get_device, is_contiguous = lambda s: 4096, lambda s: 1, lambda s: 3, lambda s: True
+
+
+def test_a_maximum_on_another_device_is_refused(stand):
+    x, gamma = torch.ones((4, 64), dtype=BF), torch.ones(64, dtype=BF)
+    record = S.StatsAmax.__new__(S.StatsAmax)
+    record.stats, record.i = Elsewhere(), 0
+    for amax in (Elsewhere(), record):
+        with pytest.raises(ValueError, match="amax"):
+            S.rmsnorm_fwd(x, gamma, out_fmt=S.FP8, amax=amax)
+        with pytest.raises(ValueError, match="amax"):
+            S.swiglu_fwd(x, x, out_fmt=S.NVFP4, amax=amax)
+    assert not stand.calls
