@@ -47,6 +47,11 @@ int check_mat(const char* who, const char* name, const void* p, int type, int64_
   return SNIP_OK;
 }
 
+// Shapes that the calls take.
+bool valid_shape(int64_t rows, int64_t cols, int64_t max_cols) {
+  return rows > 0 && rows <= kMaxDim && cols > 0 && cols <= max_cols;
+}
+
 int check_shape(const char* who, int64_t rows, int64_t cols, int64_t max_cols) {
   if (rows <= 0 || rows > kMaxDim || cols <= 0)
     return fail(SNIP_E_SHAPE, "%s: rows=%lld cols=%lld must be > 0", who, (long long)rows, (long long)cols);
@@ -114,17 +119,17 @@ LaunchTag op_tag(int kind, const snip_qtensor* out, int rounding, double work) {
 extern "C" {
 
 size_t snipop_rmsnorm_fwd_workspace(int64_t rows, int64_t cols, int format) {
-  if (rows <= 0 || cols <= 0 || cols > SNIPOP_NORM_MAX_COLS || !out_format(format) || cols % block_of(format)) return 0;
+  if (!valid_shape(rows, cols, SNIPOP_NORM_MAX_COLS) || !out_format(format) || cols % block_of(format)) return 0;
   return kOpsQuantWS;
 }
 
 size_t snipop_swiglu_fwd_workspace(int64_t rows, int64_t cols, int format) {
-  if (rows <= 0 || cols <= 0 || !out_format(format) || cols % block_of(format)) return 0;
+  if (!valid_shape(rows, cols, kMaxGateCols) || !out_format(format) || cols % block_of(format)) return 0;
   return kOpsQuantWS;
 }
 
 size_t snipop_rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
-  if (rows <= 0 || cols <= 0 || cols > SNIPOP_NORM_MAX_COLS) return 0;
+  if (!valid_shape(rows, cols, SNIPOP_NORM_MAX_COLS)) return 0;
   return align_up((size_t)norm_bwd_wg(rows, cols) * align_up((size_t)cols, 8) * sizeof(float), kAlign);
 }
 

@@ -193,3 +193,13 @@ def test_a_maximum_on_another_device_is_refused(stand):
         with pytest.raises(ValueError, match="amax"):
             S.swiglu_fwd(x, x, out_fmt=S.NVFP4, amax=amax)
     assert not stand.calls
+
+
+def test_no_workspace_for_shapes_that_the_calls_refuse(stand):
+    L = S.lib()
+    for rows in ((1 << 40) + 1, (1 << 63) - 1):
+        assert L.snipop_rmsnorm_bwd_workspace(rows, 64) == 0
+        assert L.snipop_rmsnorm_fwd_workspace(rows, 64, S.FP8) == 0
+        assert L.snipop_swiglu_fwd_workspace(rows, 64, S.FP8) == 0
+    assert L.snipop_swiglu_fwd_workspace(4, (1 << 31) + 16, S.FP8) == 0
+    assert L.snipop_swiglu_fwd_workspace(4, 1 << 31, S.FP8) > 0
