@@ -58,13 +58,16 @@ def _build_helper(src: str, out: str, verbose: bool, extra=()) -> str:
 
 ASAN_SRC = os.path.join(HELPERS, "abi_asan_check.cpp")
 ASAN_BIN = os.path.join(HELPERS, "abi_asan_check")
+ASAN_OPS_SRC = os.path.join(HELPERS, "abi_asan_ops_check.cpp")
+ASAN_OPS_BIN = os.path.join(HELPERS, "abi_asan_ops_check")
 
 
 def build_asan_check(verbose: bool = False) -> str:
-    """The library's sources and tests/helpers/abi_asan_check.cpp as one
-    executable whose host code is built with AddressSanitizer and
-    UndefinedBehaviorSanitizer (device code is not instrumented): the
-    validation and sizing paths of every entry point, checked on the CPU."""
+    """The library's sources with tests/helpers/abi_asan_check.cpp, and with
+    abi_asan_ops_check.cpp, as executables whose host code is built with
+    AddressSanitizer and UndefinedBehaviorSanitizer (device code is not
+    instrumented): the validation and sizing paths of every entry point of
+    snip.h and of snip_ops.h, checked on the CPU."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     san = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
            "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-fno-sanitize-recover=undefined"]
@@ -82,16 +85,17 @@ def build_asan_check(verbose: bool = False) -> str:
         return obj
 
     from concurrent.futures import ThreadPoolExecutor
-    srcs = [os.path.join(CSRC, s) for s in SOURCES] + [ASAN_SRC]
+    srcs = [os.path.join(CSRC, s) for s in SOURCES] + [ASAN_SRC, ASAN_OPS_SRC]
     with ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 1)) as ex:
-        objs = list(ex.map(one, srcs))
-    cmd = [hipcc_path(), "--offload-arch=gfx950", *san, "-o", ASAN_BIN + ".tmp", *objs]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stderr}")
-    os.replace(ASAN_BIN + ".tmp", ASAN_BIN)
+        *objs, snip, ops = ex.map(one, srcs)
+    for main, out in ((snip, ASAN_BIN), (ops, ASAN_OPS_BIN)):
+        cmd = [hipcc_path(), "--offload-arch=gfx950", *san, "-o", out + ".tmp", *objs, main]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"link failed:\n{res.stderr}")
+        os.replace(out + ".tmp", out)
     return ASAN_BIN
 
 
