@@ -14,7 +14,10 @@
  *               fp32; the pointer is 16-byte aligned. `cols` itself need not
  *               be a multiple of anything unless an output is quantized.
  *   Arithmetic  fp32 throughout (sums, statistics, exponentials); a value is
- *               rounded once, to nearest even, when it is stored as bf16.
+ *               rounded once, to nearest even, when it is stored as bf16. A
+ *               row whose sum of squares leaves fp32 (values about 1e19) has
+ *               r = 0. sigmoid is within 7 * 2^-24 of its value, and 0 where
+ *               exp(-gate) leaves fp32 (gate below -88).
  *   Overlap     An output may be the very matrix that an input is (same
  *               pointer, type and leading dimension) where the entry says
  *               so; any other overlap is undefined.
@@ -50,7 +53,9 @@ extern "C" {
  *   gamma      device [cols], gamma_type, 16-byte aligned.
  *   eps        >= 0, finite.
  *   h          device, h_type, ldh, or NULL (not stored). May be x or res
- *              itself: the residual stream updated in place.
+ *              itself: the residual stream updated in place. The backward
+ *              pass reads this h, so a training step keeps it as it is until
+ *              then: no later norm may update that buffer in place.
  *   y          device, y_type, ldy, or NULL.
  *   rstd       device fp32 [rows] (r, for the backward pass) or NULL.
  *   out        host descriptor or NULL: y quantized row-wise in out->format
@@ -101,9 +106,8 @@ int snipop_rmsnorm_bwd(const void* dy, int dy_type, int64_t lddy, const void* h,
  *   gate, up   device, one type, own leading dimensions (the two halves of
  *              one product's output, for instance).
  *   y, out, rounding, seed, tensor_id, amax_in, stats, ws  as
- *              snipop_rmsnorm_fwd; y may be gate or up itself unless the
- *              maximum is computed too (out in NVFP4 or FP8 without amax_in
- *              is fine: the pass for the maximum writes nothing).
+ *              snipop_rmsnorm_fwd. y may be gate or up itself, also where the
+ *              maximum is computed (the pass for it writes nothing).
  *   rows > 0, 0 < cols <= 2^31. One of y and out must be given.
  * Errors: NULL, SHAPE, ALIGN, FORMAT, WORKSPACE, HIP. */
 int snipop_swiglu_fwd(const void* gate, int64_t ldg, const void* up, int64_t ldu, int type,

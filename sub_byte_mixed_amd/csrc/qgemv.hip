@@ -11,8 +11,10 @@
 //  - MFMA: tiles of 16 rows x 16 tokens, the waves of a workgroup share K;
 //    scales are applied as the codes are decoded (64 VALU operations per KB of
 //    NVFP4, 16 of MXFP4, for all tokens).
-// NVFP4, one token, dot / MFMA: 2048 x 2048 2.7 / 3.9 us, 4096 x 11008 7.4 /
-// 9.0, 28672 x 8192 25.1 / 29.9 (5.3 TB/s; of 132 MB, a bare read takes 21.3).
+// NVFP4, one token, dot / MFMA: 2048 x 2048 2.9 / 4.1 us, 4096 x 11008 7.2 /
+// 8.5, 28672 x 8192 23.4 / 28.5 (5.6 TB/s; of 132 MB, a bare read takes 21.3).
+// Times here and below: launches of a captured graph, one after the other, over
+// weights that exceed the last-level cache.
 #include "row_common.h"
 
 namespace snip {
@@ -511,19 +513,19 @@ hipError_t gemv_row(const Gemv& a, hipStream_t s) {
 template <int FMT>
 hipError_t gemv_fmt(const Gemv& a, hipStream_t s) {
   // One token: a row a wave; beyond what is resident the waves stay and walk on,
-  // with the token in LDS (28672 x 8192 NVFP4 25.1 us, 30.3 as separate
-  // workgroups; 16384 x 4096 9.0 and 11.6; 11008 x 4096 7.1 and 8.3).
+  // with the token in LDS (28672 x 8192 NVFP4 23.4 us, 28.5 as separate
+  // workgroups; 16384 x 4096 8.9 and 11.3; 11008 x 4096 7.2 and 8.3).
   const bool more = a.N > kWalkWG * kRowWaves;
   // Many rows that fill no more than half of a wave's load go to the MFMA form
-  // (50000 x 1024: 13.1 us here and 10.4 there; 100000 x 512: 21.4 and 10.6, FP8
-  // 18.3 and 13.5), but for bf16 scales, which it pays twice (16384 x 1024: 5.9
-  // and 6.9).
+  // (50000 x 1024: 12.3 us here and 9.8 there; 100000 x 512: 20.5 and 10.3, FP8
+  // 17.0 and 13.0), but for bf16 scales, which it pays twice (16384 x 1024: 5.7
+  // and 7.1).
   const bool half = WFmt<FMT>::SC != 3 && 2 * a.K <= 64 * WFmt<FMT>::PER;
   if (a.M == 1 && !(more && half))
     return more && a.K <= kRowSlab ? gemv_row<FMT, 1, true>(a, s) : gemv_row<FMT, 1, false>(a, s);
   // Two tokens: the dot form while the time is mostly latency (NVFP4, dot and
-  // MFMA: 4096 x 4096 4.7 and 5.6 us, 11264 x 2048 7.0 and 6.2, 28672 x 8192
-  // 31.9 and 29.7). With three or four it is never ahead.
+  // MFMA: 4096 x 4096 4.7 and 5.3 us, 11264 x 2048 7.0 and 6.1, 28672 x 8192
+  // 32.7 and 28.8). With three or four it is never ahead.
   if (a.M == 2 && !more && a.N * a.K <= kPairMost) return gemv_row<FMT, 2, false>(a, s);
   constexpr int TPI = WFmt<FMT>::FP8 ? 4 : 2;          // tokens per load
   const int64_t tiles = ceil_div(a.N, 16), stages = ceil_div(a.K, WFmt<FMT>::FP8 ? 128 : 256);
@@ -531,22 +533,22 @@ hipError_t gemv_fmt(const Gemv& a, hipStream_t s) {
   // bytes as the codes of 64 rows at 16 tokens and next to nothing at 4; but
   // the 256 CUs want a workgroup each, and beyond that two workgroups a CU hide
   // more latency than one with twice the tiles, until the reads weigh more.
-  // NVFP4, 16 tokens, one, two, three and four tiles: 4096 x 4096 7.5, 9.1, -,
-  // 13.6 us; 7168 x 4096 10.6, 9.5, 11.5, 16.6; 11008 x 4096 14.9, 13.8, 12.4,
-  // 14.6; 16384 x 4096 16.8, 14.4, 22.0, 15.9; 28672 x 8192 52.9, 42.8, 51.7, 40.0.
+  // NVFP4, 16 tokens, one, two, three and four tiles: 4096 x 4096 8.4, 8.9, 10.8,
+  // 13.3 us; 7168 x 4096 10.6, 9.5, 11.2, 14.0; 11008 x 4096 14.6, 13.8, 12.1,
+  // 14.3; 16384 x 4096 18.7, 14.6, 21.1, 14.8; 28672 x 8192 49.7, 40.3, 48.0, 37.0.
   int rt = a.M <= 4 || tiles <= 256 ? 1 : tiles <= 512 ? 2 : tiles <= 768 ? 3 : tiles <= 1536 ? 2 : 4;
-  // Few tiles: more waves along K (2048 x 28672, 3 tokens: 16.3 us with 16
-  // waves, 18.6 with 8; 11008 x 4096: 12.3 and 9.6). Four where their loads are
-  // long enough: four tiles a wave (28672 x 8192, 16 tokens: 40.1 us with 4,
-  // 46.5 with 8), or many workgroups of up to 8 stages a wave (4 tokens, 16384 x
-  // 4096: 11.9 us with 4, 14.3 with 8; FP8 28672 x 8192, 16 stages: 45.7 and 41.8).
+  // Few tiles: more waves along K (2048 x 28672, 3 tokens: 15.3 us with 16
+  // waves, 17.1 with 8; 11008 x 4096: 12.2 and 9.4). Four where their loads are
+  // long enough: four tiles a wave (28672 x 8192, 16 tokens: 37.4 us with 4,
+  // 43.2 with 8), or many workgroups of up to 8 stages a wave (4 tokens, 16384 x
+  // 4096: 11.0 us with 4, 11.8 with 8; FP8 28672 x 8192, 16 stages: 41.2 and 39.6).
   const bool few = rt == 4 || (a.M <= 4 && tiles > 768 && stages <= 32);
   int waves = few ? 4 : tiles <= 256 ? 16 : 8;
   if (waves > stages) waves = (int)stages;
   const int xt = a.M <= TPI ? 1 : a.M <= 4 ? 2 : a.M <= 8 ? 8 / TPI : 16 / TPI;
   // The tiles' scales stay in LDS: for a long K fewer tiles, then fewer waves
-  // (bf16 scales of 16, 28672 x 28672, 16 tokens: 254 us, 1220 token by token;
-  // 24593 x 14400: 152 and 601), and where that does not do, token by token.
+  // (bf16 scales of 16, 28672 x 28672, 16 tokens: 260 us, 1219 token by token;
+  // 24593 x 14400: 152 and 604), and where that does not do, token by token.
   const auto over = [&] { return mfma_lds<FMT>(a.K, rt, xt, waves) > kMaxLds; };
   while (over() && rt > 1) --rt;
   while (over() && waves > 4) waves /= 2;

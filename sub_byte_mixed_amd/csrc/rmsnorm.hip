@@ -9,10 +9,12 @@
 // chunks of 8 elements (chunk t + v TPR, so that a wave's accesses are
 // contiguous): with 64 the reduction needs no LDS and a workgroup holds four
 // rows, with more it crosses the waves through LDS once per row.
-// Measured: forward 4096 x 2048, fp32 x, bf16 residual, to bf16 and FP8, 22.7 us
-// (4.1 TB/s); 4096 x 8192, bf16, to FP8, 44.5 us (5.3 TB/s, a large copy's
-// rate); backward 4096 x 2048, fp32 dy, 19.0 us (4.4 TB/s, with dgamma's
-// second launch).
+// Measured, calls back to back: forward 4096 x 2048, fp32 x, bf16 residual, to
+// bf16 and FP8 with statistics, 22.2 us (4.2 TB/s); 4096 x 8192, bf16, to FP8,
+// 43.8 us (5.4 TB/s, a large copy's rate); backward 4096 x 2048, fp32 dy, 18.4 us
+// (4.6 TB/s, with dgamma's second launch). Finding the maximum itself is one more
+// pass over the inputs: 4096 x 2048 24.0 -> 35.5 us in a graph, 4096 x 8192 48.6 ->
+// 75.6; NVFP4 and MX-FP4 outputs take 1 to 2 us less than FP8.
 #include "row_common.h"
 
 namespace snip {
@@ -214,8 +216,10 @@ __global__ __launch_bounds__(WG ? 1024 : 256) void rmsnorm_bwd_kernel(NormBwd A)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dg[v][i] = 0.0f;
 
-  // the next row's loads run while this one is worked on, where the registers
-  // suffice for both (two chunks a thread of 1024 spill)
+  // the next row's loads run while this one is worked on, but with two chunks a
+  // thread of 1024, whose 128 registers hardly hold one row: even so, of those
+  // forms the ones with bf16 dy and fp32 h or fp32 dres, and the all-fp32 one,
+  // spill 24 to 60 registers (36 to 52 bytes a lane)
   constexpr bool AHEAD = VPT == 1 || !WG;
   for (int it = 0; row < A.rows; ++it, row += step) {
     if (!AHEAD && it > 0) load(row);

@@ -9,8 +9,9 @@
 // row (the blocks of a quantized output need that); it advances by the grid's
 // stride in rows and chunks that the host has divided once, and the next
 // chunk's loads are issued before the present one is worked on. Measured:
-// forward 8192 x 11008, fp32 to FP8, 146 us (5.5 TB/s); backward 4096 x 5632,
-// fp32 in, bf16 out, 58.7 us (6.3 TB/s: mostly reads, part of them cached).
+// forward 8192 x 11008, fp32 to FP8, 142 us (5.7 TB/s), to NVFP4 149, to MX-FP4
+// 146, with its own maximum 243 to FP8; backward 4096 x 5632, fp32 in, bf16 out,
+// 58.8 us (6.3 TB/s: mostly reads, part of them cached).
 #include "row_common.h"
 
 namespace snip {
@@ -67,8 +68,10 @@ __device__ __forceinline__ void store_chunk(const Mat& m, const Offset<E>& o, bo
 // 1 / (1 + exp(-g)) within 7 half-ulps (2 each of the hardware's exp2 and
 // reciprocal, 3 of the products and the sum): -g log2(e) in two parts, the
 // second one's share as a factor. Beyond +-150 exp2 is 0 or infinite, and the
-// sigmoid 1 or 0. 9 operations (8192 x 11008 fp32 to FP8: 146 us, 157 with
-// the library's expf and division, 30 operations).
+// sigmoid 1 or 0. 9 operations; the library's expf and division, about half an
+// ulp each, take 30 (8192 x 11008 fp32 to FP8, one after the other: 146 and 157
+// us). An fp32 y can be an ulp further off for it; bf16 and quantized ones have
+// coarser roundings.
 __device__ __forceinline__ float sigmoid(float g) {
   const float t = __builtin_amdgcn_fmed3f(-g, -150.0f, 150.0f);
   const float hi = t * 1.44269502f;

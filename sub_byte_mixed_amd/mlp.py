@@ -38,7 +38,8 @@ class GatedMLP:
     def forward(self, x: torch.Tensor, res: torch.Tensor, seed: int = 0):
         """x: what joins the residual stream res, both [T, hidden], T a
         multiple of 128. Returns (output fp32, the new stream bf16, what
-        backward needs)."""
+        backward needs). backward reads the new stream again: until then it is
+        not updated in place (as by rmsnorm_fwd with h=)."""
         y, h, rstd, _, _ = S.rmsnorm_fwd(x, self.gamma, self.eps, res=res)
         gu, saved_gu, _ = S.linear_fwd_save(y, self.w_gate_up, self.fmt, seed, self.ids[0])
         a, _, _ = S.swiglu_fwd(gu[:, :self.ffn], gu[:, self.ffn:])

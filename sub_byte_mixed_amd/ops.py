@@ -176,7 +176,8 @@ def rmsnorm_fwd(x: torch.Tensor, gamma: torch.Tensor, eps: float = 1e-5, res: Op
 
     Returns (y, h, rstd, q, stats). h is the new residual stream (None where
     there is no res and no buffer for it; pass h=res or h=x to update in
-    place), rstd what rmsnorm_bwd needs, q the quantized y (out_fmt FP8, NVFP4
+    place, but not over an h that a rmsnorm_bwd has still to read), rstd what
+    rmsnorm_bwd needs, q the quantized y (out_fmt FP8, NVFP4
     or MXFP4, or a QuantizedTensor to write into; None otherwise). amax: a
     supplied max|y| for its tensor scale, as in linear_fwd_save (unused without
     q)."""
