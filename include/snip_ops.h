@@ -15,9 +15,9 @@
  *               be a multiple of anything unless an output is quantized.
  *   Arithmetic  fp32 throughout (sums, statistics, exponentials); a value is
  *               rounded once, to nearest even, when it is stored as bf16. A
- *               row whose sum of squares leaves fp32 (values of 1e17 and more) has
- *               r = 0. sigmoid is within 7 * 2^-24 of its value, and 0 where
- *               exp(-gate) leaves fp32 (gate below -88).
+ *               row whose sum of squares leaves fp32 (values of 1e17 and
+ *               more) has r = 0. sigmoid is within 7 * 2^-24 of its value, and
+ *               0 where exp(-gate) leaves fp32 (gate below -88).
  *   Overlap     An output may be the very matrix that an input is (same
  *               pointer, type and leading dimension) where the entry says
  *               so; any other overlap is undefined.

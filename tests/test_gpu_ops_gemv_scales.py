@@ -73,9 +73,9 @@ def test_both_ends_in_one_tile(fmt):
 
 
 @pytest.mark.parametrize("fmt", E8M0 + BF16)
-def test_scales_of_zero_stay_with_the_usual_product(fmt):
+def test_blocks_of_zeros(fmt):
     """Blocks of zeros (scale 0, or 2^-127 in E8M0) next to ordinary ones, as
-    the quantizer writes them: the same bits as without those blocks' rows."""
+    the quantizer writes them, and a row of nothing else."""
     wt = rand((64, 512), BF, 5, 0.02)
     wt[:, 128:192] = 0.0
     wt[7] = 0.0
