@@ -7,9 +7,10 @@ of sub_byte_mixed_amd. Head layouts are those of the workloads in synth/ (hidden
 heads of 64 over 4; hidden 4096: 32 heads of 128; hidden 8192 with K/V of 1024: 64 heads of 128 over 8),
 token counts theirs (4096, 8192) and ragged ones next to them.
 
-The cache, in pages of `page` tokens (a multiple of 16), E2M1 codes two to a byte, low nibble first:
-  k_codes  [pages][kv_heads][page][dim / 2]            k_scales  [pages][kv_heads][page][dim / block]
-  v_codes  [pages][kv_heads][page / 4][dim / 8][4 tokens][4 bytes]
+The cache, in pages of `page` tokens (a power of two from 16), E2M1 codes two to a byte, low nibble first:
+  k_codes  [pages][kv_heads][page / 16][dim / 2 / p][16 tokens][p bytes]        p = 16 (8 where dim is 64)
+  k_scales [pages][kv_heads][page / 16][dim / block / s][16 tokens][s]          s = 2 p / block, at least 1
+  v_codes  [pages][kv_heads][page / 4][dim / 2 / v][4 tokens][v bytes]          v = 4 (2 where dim is 64)
   v_scales [pages][kv_heads][page / 4][dim / block][4 tokens]
 block and scale: 16 and E4M3 under one power of two for all keys and one for all values (nvfp4), 32 and
 E8M0 (mxfp4). Sequence b has lens[b] tokens, the last of them new; token t lies in page table[b][t / page].
@@ -148,16 +149,24 @@ def _pack(codes):
     return codes[..., 0::2] | (codes[..., 1::2] << 4)
 
 
-def _fill(g, cache, fmt, texp, channels):
+def _pieces(case):
+    """Bytes of a piece of a key, of its scales, of a value."""
+    p = 8 if case["dim"] == 64 else 16
+    return p, max(1, 2 * p // FORMATS[case["fmt"]][1]), p // 4
+
+
+def _fill(g, cache, case, channels):
     """Keys and values of earlier tokens into every page, some pages at a time."""
-    pages, heads, page, half = cache["k_codes"].shape
-    step = max(1, (1 << 26) // (heads * page * half * 2))
+    fmt, page, dim, (p, s, v) = case["fmt"], case["page"], case["dim"], _pieces(case)
+    pages, heads = cache["k_codes"].shape[:2]
+    step = max(1, (1 << 26) // (heads * page * dim))
     for a in range(0, pages, step):
         n = min(step, pages - a)
-        codes, stored, _ = _quantize(_randn(g, n, heads, page, 2 * half) * channels, fmt, texp[0])
-        cache["k_codes"][a:a + n], cache["k_scales"][a:a + n] = _pack(codes), stored
-        codes, stored, _ = _quantize(0.5 * _randn(g, n, heads, page // 4, 4, 2 * half), fmt, texp[1])
-        cache["v_codes"][a:a + n] = _pack(codes).unflatten(-1, (-1, 4)).transpose(3, 4)
+        codes, stored, _ = _quantize(_randn(g, n, heads, page // 16, 16, dim) * channels[:, None], fmt, TEXP[0])
+        cache["k_codes"][a:a + n] = _pack(codes).unflatten(-1, (-1, p)).transpose(3, 4)
+        cache["k_scales"][a:a + n] = stored.unflatten(-1, (-1, s)).transpose(3, 4)
+        codes, stored, _ = _quantize(0.5 * _randn(g, n, heads, page // 4, 4, dim), fmt, TEXP[1])
+        cache["v_codes"][a:a + n] = _pack(codes).unflatten(-1, (-1, v)).transpose(3, 4)
         cache["v_scales"][a:a + n] = stored.transpose(3, 4)
 
 
@@ -182,14 +191,16 @@ def prepare(case, seed):
     def zeros(*shape):
         return torch.zeros(shape, dtype=torch.uint8, device="cuda")
 
-    cache = {"k_codes": zeros(pages, heads, page, dim // 2), "k_scales": zeros(pages, heads, page, dim // block),
-             "v_codes": zeros(pages, heads, page // 4, dim // 8, 4, 4), "v_scales": zeros(pages, heads, page // 4, dim // block, 4)}
+    p, each_s, v = _pieces(case)
+    cache = {"k_codes": zeros(pages, heads, page // 16, dim // 2 // p, 16, p),
+             "k_scales": zeros(pages, heads, page // 16, dim // block // each_s, 16, each_s),
+             "v_codes": zeros(pages, heads, page // 4, dim // 2 // v, 4, v), "v_scales": zeros(pages, heads, page // 4, dim // block, 4)}
     channels = _channels(g, heads, dim)
     s = {"case": case, "cache": cache, "table": table, "lens": torch.tensor(lens, dtype=torch.int32, device="cuda"),
          "cu": None if case["new"] == 1 else torch.tensor(cu, dtype=torch.int32, device="cuda"),
          "texp": torch.tensor(TEXP, dtype=torch.int32, device="cuda")}
     if case["op"] == "attn":
-        _fill(g, cache, fmt, TEXP, channels)
+        _fill(g, cache, case, channels)
         s["q"] = (1.3 * _randn(g, cu[-1], case["q_heads"] * dim)).to(torch.bfloat16)
         s["out"] = torch.empty_like(s["q"])
         return s
@@ -239,23 +250,26 @@ def _rotate(x, s, pos):
 
 def _plain_append(s):
     case, cache = s["case"], s["cache"]
-    fmt, page = case["fmt"], case["page"]
+    fmt, page, (p, each_s, each_v) = case["fmt"], case["page"], _pieces(case)
     seq, pos = _rows(s)
     at, row = s["table"][seq, pos // page].long(), pos % page
     out = {"q": _rotate(s["q"], s, pos).flatten(1).to(torch.bfloat16)}
     k, stored, scale = _quantize(_rotate(s["k"], s, pos), fmt, TEXP[0])
-    cache["k_codes"][at, :, row], cache["k_scales"][at, :, row] = _pack(k), stored
+    cache["k_codes"][at, :, row // 16, :, row % 16] = _pack(k).unflatten(-1, (-1, p))
+    cache["k_scales"][at, :, row // 16, :, row % 16] = stored.unflatten(-1, (-1, each_s))
     out["k"] = _values(k, scale, fmt, TEXP[0]).flatten(1).to(torch.bfloat16)
     v, stored, scale = _quantize(s["v"].float().unflatten(1, (-1, case["dim"])), fmt, TEXP[1])
-    cache["v_codes"][at, :, row // 4, :, row % 4] = _pack(v).unflatten(-1, (-1, 4))
+    cache["v_codes"][at, :, row // 4, :, row % 4] = _pack(v).unflatten(-1, (-1, each_v))
     cache["v_scales"][at, :, row // 4, :, row % 4] = stored
     out["v"] = _values(v, scale, fmt, TEXP[1]).flatten(1).to(torch.bfloat16)
     return out
 
 
 def _read(codes, scales, s, which):
-    """Cached values [sequence, kv head, token, dim] of the pages that the table names."""
+    """Cached values [sequence, kv head, token, dim], of what lies in [sequence, page, kv head, group of
+    tokens, piece, token, byte]."""
     fmt = s["case"]["fmt"]
+    codes, scales = (t.transpose(4, 5).flatten(5).flatten(3, 4) for t in (codes, scales))
     codes = torch.stack((codes & 15, codes >> 4), dim=-1).flatten(-2)
     scale = scales.view(torch.float8_e4m3fn).float() if fmt == "nvfp4" else torch.exp2(scales.float() - 127.0)
     return _values(codes, scale.unsqueeze(-1), fmt, TEXP[which]).transpose(1, 2).flatten(2, 3)
@@ -266,7 +280,7 @@ def _plain_attn(s):
     dim, heads, group = case["dim"], case["kv_heads"], case["q_heads"] // case["kv_heads"]
     table = s["table"].long().clamp(min=0)
     k = _read(cache["k_codes"][table], cache["k_scales"][table], s, 0)
-    v = _read(cache["v_codes"][table].transpose(4, 5).flatten(5).flatten(3, 4), cache["v_scales"][table].transpose(4, 5).flatten(3, 4), s, 1)
+    v = _read(cache["v_codes"][table], cache["v_scales"][table].unsqueeze(-1), s, 1)
     seq, pos = _rows(s)
     first = torch.zeros_like(s["lens"]) if s["cu"] is None else s["cu"][:-1]
     row = torch.zeros_like(seq) if s["cu"] is None else torch.arange(seq.numel(), device="cuda") - first[seq]
@@ -400,8 +414,8 @@ def exact(case, seed):
             else:
                 sc = torch.exp2(scales.to(torch.float64) - 127.0)
             return v * sc.repeat_interleave(block, dim=-1)
-        kc = c["k_codes"][use].permute(1, 0, 2, 3).reshape(hk, -1, dim // 2)[:, :n]
-        ks = c["k_scales"][use].permute(1, 0, 2, 3).reshape(hk, -1, dim // block)[:, :n]
+        kc = c["k_codes"][use].permute(1, 0, 2, 4, 3, 5).reshape(hk, -1, dim // 2)[:, :n]
+        ks = c["k_scales"][use].permute(1, 0, 2, 4, 3, 5).reshape(hk, -1, dim // block)[:, :n]
         vc = c["v_codes"][use].permute(1, 0, 2, 4, 3, 5).reshape(hk, -1, dim // 2)[:, :n]
         vs = c["v_scales"][use].permute(1, 0, 2, 4, 3).reshape(hk, -1, dim // block)[:, :n]
         k, v = decoded(kc, ks, TEXP[0]), decoded(vc, vs, TEXP[1])
