@@ -18,7 +18,9 @@ the C entry points (include/snip.h):
   timing_start(capacity), timing_read()    -> per-launch kernel times
 
 and those of include/snip_ops.h, the operators around the linear layers
-(ops.py): rmsnorm_fwd, rmsnorm_bwd, swiglu_fwd, swiglu_bwd, qgemv.
+(ops.py): rmsnorm_fwd, rmsnorm_bwd, swiglu_fwd, swiglu_bwd, qgemv; and those of
+include/snip_kv.h, attention over a key/value cache in 4 bits (kv.py): KVCache,
+KVBatch, kv_append, kv_attn, kv_gather.
 
 The library is built in-tree by `python -m sub_byte_mixed_amd.build`. If it is
 missing, importing works but every call raises: there is no CPU fallback.
@@ -80,7 +82,8 @@ class LaunchRecord(ctypes.Structure):
                 ("work", ctypes.c_double), ("ms", ctypes.c_double)]
 
 
-LAUNCH_KINDS = {0: "amax", 1: "quantize", 2: "gemm", 3: "splitk", 4: "finalize", 5: "norm", 6: "gate", 7: "gemv"}
+LAUNCH_KINDS = {0: "amax", 1: "quantize", 2: "gemm", 3: "splitk", 4: "finalize", 5: "norm", 6: "gate", 7: "gemv",
+                8: "kv_append", 9: "kv_attn", 10: "kv_join"}
 
 STATS_BYTES = 24     # sizeof(snip_stats)
 
@@ -146,7 +149,7 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m sub_byte_mixed_amd.build`")
         h = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in {**_SIGS, **ops.SIGS}.items():
+        for name, (res, args) in {**_SIGS, **ops.SIGS, **kv.SIGS}.items():
             f = getattr(h, name)
             f.restype = res
             f.argtypes = args
@@ -525,4 +528,6 @@ def timing_read() -> Tuple[List[dict], int]:
 
 
 from . import ops  # noqa: E402  (uses the definitions above)
+from . import kv  # noqa: E402
+from .kv import KVBatch, KVCache, kv_append, kv_attn, kv_gather  # noqa: E402,F401
 from .ops import qgemv, rmsnorm_bwd, rmsnorm_fwd, swiglu_bwd, swiglu_fwd  # noqa: E402,F401

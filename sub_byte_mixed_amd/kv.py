@@ -1,0 +1,242 @@
+"""Attention over a key/value cache held in 4 bits (include/snip_kv.h).
+Re-exported by the package:
+
+  KVCache(fmt, ...), KVCache.empty(...)    -> the pages of a cache
+  KVBatch(table, lens, cu)                 -> a call's sequences and their new tokens
+  kv_append(k, v, cache, batch, q, ...)    -> rotated queries; keys and values go into the cache
+  kv_attn(q, cache, batch, ...)            -> out, lse
+  kv_gather(cache, batch, tokens, ...)     -> cached keys and values in bfloat16
+
+As in the package, this module only marshals arguments: every step runs in the
+HIP kernels of libsnip. Queries, keys and values are 2-D GPU tensors with a row
+for each new token and heads * head_dim columns of unit stride; their row stride
+must keep rows 16-byte aligned. Outputs are allocated where no buffer is passed.
+Every call takes stream= (default: the current one of the tensors' device).
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional, Tuple
+
+import torch
+
+import sub_byte_mixed_amd as _S
+from . import ops as _ops
+from .ops import _ABSENT, _TYPES, _elsewhere, _mat, _scratch, _vec
+
+_c = ctypes
+_vp, _i, _l, _f, _sz = _c.c_void_p, _c.c_int, _c.c_int64, _c.c_float, _c.c_size_t
+
+
+class CacheDesc(_c.Structure):
+    """snipkv_cache."""
+    _fields_ = [("format", _c.c_int32), ("page_size", _c.c_int32), ("kv_heads", _c.c_int32), ("head_dim", _c.c_int32),
+                ("pages", _l), ("k_codes", _vp), ("k_scales", _vp), ("v_codes", _vp), ("v_scales", _vp), ("texp", _vp)]
+
+
+class BatchDesc(_c.Structure):
+    """snipkv_batch."""
+    _fields_ = [("table", _vp), ("table_ld", _l), ("max_pages", _l), ("lens", _vp), ("cu", _vp), ("seqs", _l)]
+
+
+_C, _B = _c.POINTER(CacheDesc), _c.POINTER(BatchDesc)
+SIGS = {
+    "snipkv_append": (_i, [_vp, _l, _l, _vp, _l, _vp, _l, _i, _l, _vp, _vp, _l, _l, _i, _vp, _C, _B, _vp, _l, _vp]),
+    "snipkv_gather": (_i, [_C, _B, _l, _vp, _l, _vp, _l, _vp]),
+    "snipkv_attn": (_i, [_vp, _l, _l, _l, _C, _B, _f, _l, _vp, _l, _vp, _vp, _sz, _vp]),
+    "snipkv_attn_workspace": (_sz, [_l, _l, _l, _l, _l]),
+}
+
+MAX_PAGE_SIZE = 4096           # SNIPKV_MAX_PAGE_SIZE
+HEAD_DIMS = (64, 128, 256)
+
+
+def cache_shapes(fmt: int, pages: int, page_size: int, kv_heads: int, head_dim: int) -> Tuple[tuple, ...]:
+    """Shapes of k_codes, k_scales, v_codes and v_scales."""
+    if fmt not in (_S.NVFP4, _S.MXFP4):
+        raise ValueError(f"a cache is in format NVFP4 or MXFP4, got {fmt}")
+    if head_dim not in HEAD_DIMS or page_size < 16 or page_size > MAX_PAGE_SIZE or page_size & (page_size - 1):
+        raise ValueError(f"head_dim must be one of {HEAD_DIMS} and page_size a power of two in 16 .. {MAX_PAGE_SIZE}, "
+                         f"got {head_dim} and {page_size}")
+    block = _S.FP4_LAYOUT[fmt][0]
+    p = 8 if head_dim == 64 else 16
+    v, s = p // 4, max(1, 2 * p // block)
+    return ((pages, kv_heads, page_size // 16, head_dim // 2 // p, 16, p),
+            (pages, kv_heads, page_size // 16, head_dim // block // s, 16, s),
+            (pages, kv_heads, page_size // 4, head_dim // 2 // v, 4, v),
+            (pages, kv_heads, page_size // 4, head_dim // block, 4))
+
+
+class KVCache:
+    """Caller-owned buffers of a paged cache, uint8 in the shapes of
+    cache_shapes(); texp (NVFP4): int32 [2], the powers of two that keys and
+    values are stored under (x = code * scale * 2^texp), chosen once by the
+    caller: the smallest e with max|x| <= 2688 * 2^e."""
+
+    def __init__(self, fmt: int, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                 v_scales: torch.Tensor, texp: Optional[torch.Tensor] = None):
+        if k_codes.dim() != 6:
+            raise ValueError("k_codes must have the six dimensions of cache_shapes()")
+        pages, heads, groups, pieces, _, p = k_codes.shape
+        self.format, self.pages, self.kv_heads = fmt, pages, heads
+        self.page_size, self.head_dim = 16 * groups, 2 * pieces * p
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.texp = k_codes, k_scales, v_codes, v_scales, texp
+        self.device = dev = k_codes.get_device()
+        for name, t, shape in zip(("k_codes", "k_scales", "v_codes", "v_scales"), (k_codes, k_scales, v_codes, v_scales),
+                                  cache_shapes(fmt, pages, self.page_size, heads, self.head_dim)):
+            if t.dtype != torch.uint8 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {shape} on {k_codes.device}, got "
+                                 f"{t.dtype}, {tuple(t.shape)} on {t.device}")
+        if fmt == _S.NVFP4 and texp is None:
+            raise ValueError("an NVFP4 cache needs texp")
+        self._desc = CacheDesc(fmt, self.page_size, heads, self.head_dim, pages, k_codes.data_ptr(), k_scales.data_ptr(),
+                               v_codes.data_ptr(), v_scales.data_ptr(), _vec(texp, "texp", 2, (torch.int32,), dev))
+        self.ref = ctypes.byref(self._desc)
+
+    @classmethod
+    def empty(cls, fmt: int, pages: int, page_size: int, kv_heads: int, head_dim: int, device,
+              texp: Tuple[int, int] = (0, 0)) -> "KVCache":
+        """A cache of new buffers, zeroed."""
+        bufs = [torch.zeros(s, dtype=torch.uint8, device=device) for s in cache_shapes(fmt, pages, page_size, kv_heads, head_dim)]
+        return cls(fmt, *bufs, torch.tensor(texp, dtype=torch.int32, device=device) if fmt == _S.NVFP4 else None)
+
+
+class KVBatch:
+    """The sequences of a call: table int32 [seqs, max_pages] (pages of each
+    sequence in order), lens int32 [seqs] (the call's new tokens included), cu
+    int32 [seqs + 1] (rows cu[b] .. cu[b + 1] are sequence b's new tokens, its
+    last; None: one each). A table entry outside 0 .. pages - 1 is a page that
+    is not mapped. The kernels read all three when they run: a captured call
+    follows what its buffers hold."""
+
+    def __init__(self, table: torch.Tensor, lens: torch.Tensor, cu: Optional[torch.Tensor] = None):
+        self.table, self.lens, self.cu = table, lens, cu
+        self.device = dev = table.get_device()
+        if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError(f"table must be a 2-D int32 tensor with unit column stride, got {table.dtype}, {tuple(table.shape)}")
+        self.seqs = n = table.shape[0]
+        i32 = (torch.int32,)
+        self._desc = BatchDesc(table.data_ptr(), table.stride(0) if n > 1 else table.shape[1], table.shape[1],
+                               _vec(lens, "lens", n, i32, dev), _vec(cu, "cu", n + 1, i32, dev), n)
+        self.ref = ctypes.byref(self._desc)
+
+
+def _place(cache: KVCache, batch: KVBatch, fn) -> int:
+    """The GPU that a call's cache and sequences lie on."""
+    dev = cache.device
+    if batch.device != dev:
+        raise ValueError(f"the cache and the batch of {fn.__name__} must lie on one GPU, got {dev} and {batch.device}")
+    return dev
+
+
+def _rows(t: torch.Tensor, name: str, dev: int, head_dim: int) -> Tuple[int, int]:
+    """(tokens, heads) of a matrix of heads."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.get_device() != dev or t.shape[1] % head_dim:
+        raise ValueError(f"{name} must be a 2-D tensor of heads of {head_dim} on GPU {dev}")
+    return t.shape[0], t.shape[1] // head_dim
+
+
+def kv_append(k: Optional[torch.Tensor], v: Optional[torch.Tensor], cache: KVCache, batch: KVBatch,
+              q: Optional[torch.Tensor] = None, cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None,
+              interleaved: bool = False, pos: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+              stream=None) -> Optional[torch.Tensor]:
+    """snipkv_append: rotates q and k by the angles of their tokens' positions
+    (cos, sin: float32 [positions, rot_dim / 2]; rot_dim a multiple of 64, the
+    rest of a head stays as it is; None: no rotation) and writes k and v into
+    the cache. q, k and v have one type, bfloat16 or float32 (the parts of one
+    product's columns, for instance). pos: int32 row of the angles for each
+    token, instead of its position. Returns q rotated, in bfloat16 (None
+    without q); q_out may be q itself."""
+    dev = _place(cache, batch, kv_append)
+    if stream is not None or dev != _ops._current_device():
+        return _elsewhere(kv_append, dev, stream, k, v, cache, batch, q, cos, sin, interleaved, pos, q_out)
+    first = k if k is not None else q
+    if first is None or (k is None) != (v is None):
+        raise ValueError("k and v are given together, or q alone")
+    hk, dim = cache.kv_heads * cache.head_dim, cache.head_dim
+    tokens, _ = _rows(first, "k" if k is not None else "q", dev, dim)
+    if any(t is not None and t.dtype != first.dtype for t in (q, v)) or first.dtype not in _TYPES:
+        raise ValueError("q, k and v must have the same type, bfloat16 or float32")
+    pk, _, lk = _mat(k, "k", tokens, hk, dev)
+    pv, _, lv = _mat(v, "v", tokens, hk, dev)
+    (pq, _, lq), (po, _, lo), heads = _ABSENT, _ABSENT, 0
+    if q is not None:
+        _, heads = _rows(q, "q", dev, dim)
+        pq, _, lq = _mat(q, "q", tokens, heads * dim, dev)
+        if q_out is None:
+            q_out = torch.empty((tokens, heads * dim), dtype=torch.bfloat16, device=dev)
+        elif q_out.dtype != torch.bfloat16:
+            raise ValueError("q_out must be bfloat16")
+        po, _, lo = _mat(q_out, "q_out", tokens, heads * dim, dev)
+    elif q_out is not None:
+        raise ValueError("q_out belongs to q")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin are given together")
+    angles, half, pc, ps = 0, 0, None, None
+    if cos is not None:
+        if cos.dim() != 2 or cos.shape != sin.shape or any(
+                t.dtype != torch.float32 or t.get_device() != dev or not t.is_contiguous() for t in (cos, sin)):
+            raise ValueError(f"cos and sin must be contiguous float32 tensors of one shape [positions, rot_dim / 2] on GPU {dev}")
+        (angles, half), pc, ps = cos.shape, cos.data_ptr(), sin.data_ptr()
+    pp = _vec(pos, "pos", tokens, (torch.int32,), dev)
+    _S._check(_S.lib().snipkv_append(pq, lq, heads, pk, lk, pv, lv, _TYPES[first.dtype], tokens, pc, ps, angles, 2 * half,
+                                     int(interleaved), pp, cache.ref, batch.ref, po, lo, _ops._current_stream(dev)))
+    return q_out
+
+
+def kv_gather(cache: KVCache, batch: KVBatch, tokens: Optional[int] = None, k: Optional[torch.Tensor] = None,
+              v: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """snipkv_gather: (keys, values) of the batch's tokens as they are cached,
+    [tokens, kv_heads * head_dim] in bfloat16; zeros where a position is not
+    mapped. tokens: rows of new outputs, cu[-1] at least (default: one a
+    sequence)."""
+    dev = _place(cache, batch, kv_gather)
+    if stream is not None or dev != _ops._current_device():
+        return _elsewhere(kv_gather, dev, stream, cache, batch, tokens, k, v)
+    cols = cache.kv_heads * cache.head_dim
+    if tokens is None:
+        tokens = k.shape[0] if k is not None else v.shape[0] if v is not None else batch.seqs
+    if k is None:
+        k = torch.empty((tokens, cols), dtype=torch.bfloat16, device=dev)
+    if v is None:
+        v = torch.empty((tokens, cols), dtype=torch.bfloat16, device=dev)
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
+        raise ValueError("k and v must be bfloat16")
+    pk, _, lk = _mat(k, "k", tokens, cols, dev)
+    pv, _, lv = _mat(v, "v", tokens, cols, dev)
+    _S._check(_S.lib().snipkv_gather(cache.ref, batch.ref, tokens, pk, lk, pv, lv, _ops._current_stream(dev)))
+    return k, v
+
+
+def kv_attn(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: Optional[float] = None, window: int = 0,
+            out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, with_lse: bool = False,
+            ws: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """snipkv_attn: attention of the new tokens over the cache, which holds
+    their keys and values already; causal, within the last `window` keys where
+    window > 0. q bfloat16 (kv_append's); scale: default 1 / sqrt(head_dim).
+    Returns (out bfloat16, lse): lse float32 [tokens, q_heads], the log of the
+    softmax's sum, where with_lse or a buffer asks for it. A row that sees no
+    key has out = 0 and lse = -inf."""
+    dev = _place(cache, batch, kv_attn)
+    if stream is not None or dev != _ops._current_device():
+        return _elsewhere(kv_attn, dev, stream, q, cache, batch, scale, window, out, lse, with_lse, ws)
+    dim, hk = cache.head_dim, cache.kv_heads
+    tokens, heads = _rows(q, "q", dev, dim)
+    if q.dtype != torch.bfloat16 or (out is not None and out.dtype != torch.bfloat16):
+        raise ValueError("q and out must be bfloat16")
+    pq, _, lq = _mat(q, "q", tokens, heads * dim, dev)
+    if out is None:
+        out = torch.empty((tokens, heads * dim), dtype=torch.bfloat16, device=dev)
+    po, _, lo = _mat(out, "out", tokens, heads * dim, dev)
+    if lse is None and with_lse:
+        lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (tokens, heads) or lse.get_device() != dev
+                            or not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous float32 tensor of shape ({tokens}, {heads}) on GPU {dev}")
+    L = _S.lib()
+    if ws is None:
+        ws = torch.empty(L.snipkv_attn_workspace(tokens, batch.seqs, heads, hk, dim), dtype=torch.uint8, device=dev)
+    _S._check(L.snipkv_attn(pq, lq, heads, tokens, cache.ref, batch.ref, 1.0 / math.sqrt(dim) if scale is None else scale,
+                            int(window), po, lo, _S._ptr(lse), *_scratch(ws, dev), _ops._current_stream(dev)))
+    return out, lse

@@ -1,0 +1,152 @@
+"""snipkv_attn against float64 attention over what the cache's bytes stand for.
+The cache holds NaN scales wherever no token lies; tolerances are counted in
+kv_common.Paged.attention."""
+import numpy as np
+import pytest
+import torch
+
+import sub_byte_mixed_amd as S
+from kv_common import Paged
+from ops_common import BF, F32, Guarded, f64, rand, say, strided
+
+pytestmark = pytest.mark.gpu
+FORMATS = [S.NVFP4, S.MXFP4]
+
+
+def run(P, group, window=0, scale=None, seed=0, qscale=0.5):
+    q = rand((P.rows, P.heads * group * P.dim), BF, seed, qscale)
+    out, lse = S.kv_attn(q.cuda(), P.cache, P.batch, window=window, scale=scale, with_lse=True)
+    P.check(q, out, lse, scale, window)
+    again, _ = S.kv_attn(q.cuda(), P.cache, P.batch, window=window, scale=scale)
+    assert torch.equal(again, out)
+    return q, out, lse
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 3, 8, 17])
+def test_single_tokens(fmt, dim, group):
+    """Lengths around 16, 32, a page and the waves' steps; zero tokens too."""
+    say("attn", fmt, dim, group)
+    lens = [1, 2, 15, 16, 17, 31, 32, 33, 64, 65, 127, 128, 129, 200, 0, 300]
+    run(Paged(fmt, dim, 2, 16, lens, [1] * len(lens), seed=group, one_each=True), group)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("page", [16, 32, 64, 256])
+def test_pages(fmt, page):
+    say("attn pages", fmt, page)
+    run(Paged(fmt, 128, 1, page, [page - 1, page, page + 1, 3 * page + 7], [1] * 4, seed=page, one_each=True), 4)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 4, 7])
+def test_prompts_and_tokens(fmt, dim, group):
+    """Whole prompts, chunks after others, drafted tokens, single tokens, no token, in one call."""
+    say("attn prompts", fmt, dim, group)
+    lens, new = [45, 100, 67, 300, 1, 50, 161], [45, 37, 1, 4, 1, 0, 130]
+    run(Paged(fmt, dim, 2, 32, lens, new, seed=dim + group), group)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("window", [1, 2, 16, 31, 32, 100, 2 ** 31 - 1, 2 ** 40])
+def test_windows(fmt, window):
+    say("attn window", fmt, window)
+    run(Paged(fmt, 64, 2, 16, [5, 200, 333], [5, 70, 1], seed=1), 2, window=window)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_pages_that_are_not_mapped(fmt):
+    """Their keys take no part; a row that has none left is zero with lse -inf."""
+    P = Paged(fmt, 128, 2, 16, [64, 40, 16, 90], [3, 40, 1, 1], seed=2, unmapped=[(0, 0), (0, 2), (1, 0), (2, 0), (3, 5), (3, 1)])
+    q, out, lse = run(P, 4)
+    r = slice(P.cu[1], P.cu[1] + 16)                   # the first page of sequence 1 is all that these see
+    assert not out[r].any() and bool((lse[r] == -float("inf")).all())
+    assert not out[P.cu[2]].any()
+    run(P, 4, window=20)
+
+
+def test_more_new_tokens_than_the_sequence_has():
+    """Rows at negative positions see nothing."""
+    P = Paged(S.NVFP4, 64, 1, 16, [5, -3, 0], [9, 2, 4], seed=4)
+    q, out, lse = run(P, 2)
+    assert not out[:4].any() and not out[9:].any() and bool((lse[9:] == -float("inf")).all())
+
+
+def test_rows_of_nobody_and_strides():
+    P = Paged(S.NVFP4, 128, 2, 16, [33, 80], [33, 2], seed=5)
+    q = rand((P.rows + 9, 2 * 2 * 128), BF, 1)
+    out = Guarded(P.rows + 9, 512, BF)
+    lse = torch.full((P.rows + 9, 4), 7.0, device="cuda")
+    S.kv_attn(strided(q, 24), P.cache, P.batch, out=out.t, lse=lse)
+    P.check(q[:P.rows], out.t, lse)
+    assert out.intact() and bool((out.t[P.rows:] == 7.0).all()) and bool((lse[P.rows:] == 7.0).all())
+
+
+def test_in_place():
+    P = Paged(S.MXFP4, 128, 2, 16, [333, 80], [5, 40], seed=6)
+    q = rand((P.rows, 512), BF, 1)
+    d = q.cuda()
+    S.kv_attn(d, P.cache, P.batch, out=d)
+    assert torch.equal(d, S.kv_attn(q.cuda(), P.cache, P.batch)[0])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("qscale,scale", [(0.0, None), (40.0, None), (1e-30, 1e29), (1e30, 1e-30), (0.5, 3.0)])
+def test_sizes_of_scores(fmt, qscale, scale):
+    """Queries of zero; peaked softmaxes; queries far from 1 under a scale that brings them back."""
+    say("attn sizes", fmt, qscale, scale)
+    run(Paged(fmt, 64, 1, 16, [100, 70], [1, 30], seed=7), 4, scale=scale, qscale=qscale)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_rising_scores(fmt):
+    """Keys whose scores grow along the sequence: the running maximum moves in every tile."""
+    P = Paged(fmt, 64, 1, 32, [700], [40], seed=8)
+    ramp = torch.arange(700) // 90
+    base = 0x20 if fmt == S.NVFP4 else 118
+    step = 8 if fmt == S.NVFP4 else 1                  # a power of two
+    t = P.cache.k_scales.transpose(3, 4)
+    for j in range(0, 700, 16):
+        n = min(16, 700 - j)
+        t[int(P.table[0, j // 32]), :, j % 32 // 16, :n] = (base + step * ramp[j:j + n, None, None]).to(torch.uint8).cuda()
+    run(P, 3)
+
+
+def test_a_key_of_nan_reaches_the_rows_that_see_it():
+    P = Paged(S.NVFP4, 64, 1, 16, [40], [40], seed=9)
+    P.cache.k_scales.transpose(3, 4)[int(P.table[0, 1]), 0, 0, 4] = 0x7F       # token 20
+    q = rand((40, 64), BF, 1)
+    out, lse = S.kv_attn(q.cuda(), P.cache, P.batch, with_lse=True)
+    assert bool(out[20:].isnan().all()) and bool(lse[20:].isnan().all())
+    assert not out[:20].isnan().any() and not lse[:20].isnan().any()
+
+
+def test_a_long_sequence():
+    """One token over 40000; and many waves' partial sums."""
+    P = Paged(S.NVFP4, 64, 1, 64, [40000], [1], seed=10, one_each=True)
+    run(P, 2)
+
+
+def test_offsets_past_32_bits():
+    """Pages past 4 GiB of codes."""
+    fmt, page, heads, dim = S.MXFP4, 256, 8, 256
+    per = page * heads * dim // 2
+    pages = (5 << 30) // per + 1
+    shapes = S.kv.cache_shapes(fmt, pages, page, heads, dim)
+    bufs = [torch.zeros(s, dtype=torch.uint8, device="cuda") for s in shapes]
+    cache = S.KVCache(fmt, *bufs)
+    n, use = 2 * page - 9, [pages - 1, pages - 2]
+    table = torch.tensor([use], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    k, v, q = (rand((n, heads * dim), BF, i).cuda() for i in range(3))
+    S.kv_append(k, v, cache, S.KVBatch(table, lens, cu))
+    small = S.KVCache(fmt, *[b[-2:].clone() for b in bufs])
+    assert bool(small.k_codes.any()) and bool(small.v_scales.any())
+    low = S.KVBatch(torch.tensor([[1, 0]], dtype=torch.int32, device="cuda"), lens, cu)
+    want, _ = S.kv_attn(q, small, low)
+    got, _ = S.kv_attn(q, cache, S.KVBatch(table, lens, cu))
+    assert torch.equal(got, want) and bool(want.any())
+    assert all(torch.equal(a, b) for a, b in zip(S.kv_gather(cache, S.KVBatch(table, lens, cu), n), S.kv_gather(small, low, n)))
