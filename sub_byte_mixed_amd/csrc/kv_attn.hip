@@ -323,37 +323,64 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attn_kernel(KvAttn A) {
   const int last = limit(U.pos0 + (U.r0 + U.rows - 1) / A.group);
   const int first = from(U.pos0 + U.r0 / A.group);
 
-  for (int key = (first & ~31) + 32 * wave; key <= last; key += 32 * kWaves) {
-    Tile<FMT, D> T;
-    bool mapped[2];
+  // keys that every row of the unit sees, between two tests of single keys
+  const int every_first = from(U.pos0 + (U.r0 + U.rows - 1) / A.group), every_last = limit(U.pos0 + U.r0 / A.group);
+  constexpr int kStep = 32 * kWaves;
+  struct Pages {
+    int p[2];
+  };
+  auto pages = [&](int key) {
+    Pages g;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k0 = key + 16 * h;
-      const int page = k0 <= last ? kv_page(A.c, A.b, U.seq, k0) : -1;
-      mapped[h] = page >= 0;
-      load_half<FMT, D>(A.c, kv_slot(A.c, page < 0 ? 0 : page, U.head, k0 & ((1 << A.c.shift) - 1)), h, T);
-    }
+    for (int h = 0; h < 2; ++h) g.p[h] = key + 16 * h <= last ? kv_page(A.c, A.b, U.seq, key + 16 * h) : -1;
+    return g;
+  };
+  auto load = [&](int key, const Pages& g, Tile<FMT, D>& T) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      load_half<FMT, D>(A.c, kv_slot(A.c, g.p[h] < 0 ? 0 : g.p[h], U.head, (key + 16 * h) & ((1 << A.c.shift) - 1)), h, T);
+  };
+  auto use = [&](int key, const Pages& g, Tile<FMT, D>& T) {
     f4_t s[2];
     scores<FMT, D>(T, R, s);
+    const bool whole = g.p[0] >= 0 && g.p[1] >= 0 && key >= every_first && key + 31 <= every_last;
     float top = kLowest;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = key + 16 * h + 4 * c + j;
-        s[h][j] = mapped[h] && k >= R.first && k <= R.last ? s[h][j] * R.factor : -__builtin_inff();
-        top = fmaxf(top, s[h][j]);
-      }
-    top = fmaxf(row_max(top), R.m);
-    const float f = __builtin_amdgcn_exp2f(R.m - top);
-    R.m = top;
-    R.l *= f;
+      for (int j = 0; j < 4; ++j) s[h][j] *= R.factor;
+    if (!whole) {
 #pragma unroll
-    for (int i = 0; i < G::DT; ++i) R.o[i] *= f;
+      for (int h = 0; h < 2; ++h) {
+        uint32_t keep = 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = key + 16 * h + 4 * c + j;
+          s[h][j] = g.p[h] >= 0 && k >= R.first && k <= R.last ? s[h][j] : -__builtin_inff();
+          keep |= g.p[h] >= 0 && k >= first && k <= last ? 0xFFu << (8 * j) : 0u;
+        }
+        // values of places that no row sees may be anything: their scales are replaced
+#pragma unroll
+        for (int l = 0; l < G::VL; ++l) T.vs[h][l] &= keep;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = fmaxf(top, s[h][j]);
+    // the maximum may lag by 2^8: terms of up to 256 are as exact, and most tiles leave the output as it is
+    if (__any(top > R.m + 8.0f)) {
+      top = fmaxf(row_max(top), R.m);
+      const float f = __builtin_amdgcn_exp2f(R.m - top);
+      R.m = top;
+      R.l *= f;
+#pragma unroll
+      for (int i = 0; i < G::DT; ++i) R.o[i] *= f;
+    }
     float p[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      p[i] = __builtin_amdgcn_exp2f(s[i / 4][i % 4] - top);
+      p[i] = __builtin_amdgcn_exp2f(s[i / 4][i % 4] - R.m);
       R.l += p[i];
     }
     u32x4_t ph, pl;                                    // fp16, or the two parts in bf16
@@ -365,18 +392,6 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attn_kernel(KvAttn A) {
         ph[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
         pl[i] = pack_bf16(p[2 * i] - bf16_lo(ph[i]), p[2 * i + 1] - bf16_hi(ph[i]));
       }
-    }
-    // values of places that no row sees may be anything: their scales are replaced
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t keep = 0u;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = key + 16 * h + 4 * c + j;
-        keep |= mapped[h] && k >= first && k <= last ? 0xFFu << (8 * j) : 0u;
-      }
-#pragma unroll
-      for (int l = 0; l < G::VL; ++l) T.vs[h][l] = (T.vs[h][l] & keep);
     }
 #pragma unroll
     for (int l = 0; l < G::VL; ++l) {
@@ -391,6 +406,23 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attn_kernel(KvAttn A) {
         if constexpr (!G::NV) o = mfma<FMT>(a, pl, o);
       }
     }
+  };
+  int key = (first & ~31) + 32 * wave;
+  Tile<FMT, D> T0, T1;
+  Pages g0 = pages(key), g1 = pages(key + kStep);
+  if (key <= last) load(key, g0, T0);
+  while (key <= last) {
+    if (key + kStep <= last) load(key + kStep, g1, T1);
+    const Pages g2 = pages(key + 2 * kStep);
+    use(key, g0, T0);
+    key += kStep;
+    if (key > last) break;
+    if (key + kStep <= last) load(key + kStep, g2, T0);
+    const Pages g3 = pages(key + 2 * kStep);
+    use(key, g1, T1);
+    key += kStep;
+    g0 = g2;
+    g1 = g3;
   }
 
   // the waves' shares of the rows, joined
