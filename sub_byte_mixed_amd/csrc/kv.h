@@ -41,12 +41,16 @@ struct KvGather {
   int64_t ldk, ldv, tokens;
 };
 
+struct Left;                   // what the attention leaves for its second launch
+
 struct KvAttn {
   KvCache c;
   KvBatch b;
   const uint16_t* q;
   uint16_t* out;
   float* lse;                  // or null
+  float* part;                 // workspace of kv_attn_slots() bytes
+  Left* left;                  // within it
   int64_t ldq, ldo, tokens;
   int32_t q_heads, group;      // query heads of a kv head
   int32_t window;              // 0: none
@@ -63,8 +67,10 @@ constexpr int kv_scale_piece(int dim, int block) {
 // Row tiles of an attention call, of every kv head.
 int64_t kv_attn_tiles(int64_t tokens, int64_t seqs, int64_t group, bool cu);
 
+size_t kv_attn_slots(int dim);
+
 hipError_t launch_kv_append(int format, int dim, const KvAppend& a, hipStream_t s);
 hipError_t launch_kv_gather(int format, int dim, const KvGather& a, hipStream_t s);
-hipError_t launch_kv_attn(int format, int dim, const KvAttn& a, hipStream_t s);
+hipError_t launch_kv_attn(int format, int dim, KvAttn a, hipStream_t s);
 
 }  // namespace snip

@@ -170,7 +170,7 @@ size_t snipkv_attn_workspace(int64_t tokens, int64_t seqs, int64_t q_heads, int6
       q_heads < 1 || q_heads > kMaxHeads || q_heads % kv_heads || !head_dim_ok(head_dim))
     return 0;
   if (kv_attn_tiles(tokens, seqs, q_heads / kv_heads, true) > kMaxTiles) return 0;
-  return kAlign;
+  return align_up(kv_attn_slots((int)head_dim), kAlign);
 }
 
 int snipkv_attn(const void* q, int64_t ldq, int64_t q_heads, int64_t tokens, const snipkv_cache* cache,
@@ -198,6 +198,7 @@ int snipkv_attn(const void* q, int64_t ldq, int64_t q_heads, int64_t tokens, con
   a.q = static_cast<const uint16_t*>(q);
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
+  a.part = static_cast<float*>(ws);
   a.ldq = ldq;
   a.ldo = ldo;
   a.tokens = tokens;

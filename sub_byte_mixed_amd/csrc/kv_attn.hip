@@ -257,88 +257,183 @@ __device__ __forceinline__ void scores(const Tile<FMT, D>& T, const Rows<FMT, D>
   }
 }
 
-// The workgroup's unit: 16 rows of one kv head of one sequence.
-struct Unit {
-  int seq, head;
-  int64_t row0;                // first row of the sequence in the call's matrices
-  int rows;                    // of the unit
-  int r0;                      // its first (token, query head) of the sequence
-  int64_t pos0;                // position of the sequence's first row
+// Work is counted in steps: the workgroup's waves take 32 keys each. A unit --
+// 16 rows of one kv head of one sequence -- has the steps of the sequence's
+// keys, units follow each other by sequence, head and rows, and the steps of the
+// call are shared evenly among the workgroups, whatever the lengths. A workgroup
+// finds its share from lens and cu alone, so a captured launch follows them.
+constexpr int kStep = 32 * kWaves;
+
+struct Span {                  // of one sequence
+  int64_t row0, pos0;          // first row in the call's matrices, its position
+  int rows;                    // (token, query head) pairs of a kv head
+  int tiles, steps;            // units a head, steps a unit
 };
 
-// Tile u of the call's row tiles; those of sequence b begin at
-// floor(cu[b] group / 16) + b, which leaves room for every sequence's last.
-__device__ __forceinline__ Unit find_unit(const KvAttn& A, int64_t u, int head) {
-  Unit x;
-  x.head = head;
-  x.rows = 0;
-  if (!A.b.cu) {
-    const int per = (A.group + kRows - 1) / kRows;
-    x.seq = (int)(u / per);
-    x.row0 = x.seq;
-    x.r0 = (int)(u % per) * kRows;
-    if (x.seq < A.b.seqs) {
-      x.rows = A.group - x.r0 < kRows ? A.group - x.r0 : kRows;
-      x.pos0 = (int64_t)A.b.lens[x.seq] - 1;
-    }
-    return x;
+__device__ __forceinline__ int limit(const KvAttn& A, int64_t p) {
+  return (int)(p < 0 ? -1 : p >= A.b.max_len ? A.b.max_len - 1 : p);
+}
+// First key that a row at position p sees.
+__device__ __forceinline__ int first_key(const KvAttn& A, int64_t p) {
+  return A.window && p >= A.window ? limit(A, p - A.window + 1) : 0;
+}
+
+__device__ __forceinline__ Span span_of(const KvAttn& A, int b) {
+  Span x = {};
+  if (b >= A.b.seqs) return x;
+  int64_t a = b, e = b + 1;
+  if (A.b.cu) {
+    a = A.b.cu[b];
+    e = A.b.cu[b + 1];
   }
-  auto start = [&](int i) { return (int64_t)A.b.cu[i] * A.group / kRows + i; };
-  x.seq = kv_find(A.b.seqs, u, start);
-  if (x.seq < 0 || x.seq >= A.b.seqs) return x;
-  const int64_t a = A.b.cu[x.seq], b = A.b.cu[x.seq + 1] < A.tokens ? A.b.cu[x.seq + 1] : A.tokens;
-  const int64_t r0 = (u - start(x.seq)) * kRows, n = (b - a) * A.group;
-  if (a < 0 || r0 < 0 || r0 >= n) return x;
-  x.rows = n - r0 < kRows ? (int)(n - r0) : kRows;
+  const int64_t len = A.b.lens[b];
   x.row0 = a;
-  x.r0 = (int)r0;
-  x.pos0 = (int64_t)A.b.lens[x.seq] - (A.b.cu[x.seq + 1] - a);
+  x.pos0 = len - (e - a);
+  if (e > A.tokens) e = A.tokens;
+  if (a < 0 || e <= a) return x;
+  x.rows = (int)(e - a) * A.group;
+  x.tiles = (x.rows + kRows - 1) / kRows;
+  const int n = limit(A, len - 1) + 1 - (first_key(A, x.pos0) & ~31);
+  x.steps = n > kStep ? (n + kStep - 1) / kStep : 1;   // a unit without keys writes its zeros
   return x;
 }
 
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+}
+
+// The sequences 64 at a time: the steps up to and with each of them, in the
+// wave's own LDS (a register each would cost the kernel a wave of occupancy).
+struct Cursor {
+  int64_t* upto;               // [64]
+  int seq0;
+  int64_t before, end;         // steps before the 64, and with them
+
+  __device__ __forceinline__ void load(const KvAttn& A, int s0, int64_t b) {
+    const int lane = threadIdx.x & 63;
+    const Span x = span_of(A, s0 + lane);
+    int64_t n = (int64_t)x.tiles * x.steps * A.c.heads;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int64_t v = __shfl_up(n, o, 64);
+      if (lane >= o) n += v;
+    }
+    seq0 = s0;
+    before = b;
+    end = uniform(b + __shfl(n, 63, 64));
+    upto[lane] = b + n;
+    __builtin_amdgcn_wave_barrier();
+  }
+  // Steps of all sequences; leaves the cursor at the first ones.
+  __device__ __forceinline__ int64_t total(const KvAttn& A) {
+    load(A, 0, 0);
+    if (A.b.seqs <= 64) return end;
+    for (int s = 64; s < A.b.seqs; s += 64) load(A, s, end);
+    const int64_t n = end;
+    load(A, 0, 0);
+    return n;
+  }
+  // The sequence that step `at` is in, and the steps before it.
+  __device__ __forceinline__ int seek(const KvAttn& A, int64_t at, int64_t* from) {
+    while (at >= end) load(A, seq0 + 64, end);
+    const int i = __ffsll((unsigned long long)__ballot(upto[threadIdx.x & 63] > at)) - 1;
+    *from = i ? uniform(upto[i - 1]) : before;
+    return seq0 + i;
+  }
+};
+
+// The steps of n workgroups: q each, one more for the first r.
+struct Shares {
+  int64_t q, r;
+  __device__ __forceinline__ Shares(int64_t total, int n) {
+    if (total >> 31) {
+      q = total / n;
+    } else {
+      q = (uint32_t)total / (uint32_t)n;
+    }
+    r = total - q * n;
+  }
+  __device__ __forceinline__ int64_t first(int w) const { return w * q + (w < r ? w : r); }
+  __device__ __forceinline__ int owner(int64_t at) const {   // of a step
+    const int64_t many = r * (q + 1);
+    if (at < many) return at >> 31 ? (int)(at / (q + 1)) : (int)((uint32_t)at / (uint32_t)(q + 1));
+    const int64_t rest = at - many;
+    return (int)r + (rest >> 31 ? (int)(rest / q) : (int)((uint32_t)rest / (uint32_t)q));
+  }
+};
+
+}  // namespace
+
+// What a workgroup leaves for the joining launch: two slots, of the unit that
+// its share begins within and of the one that it ends within (16 maxima, 16
+// sums, 16 rows of output each), and where the latter's output belongs.
+struct Left {
+  int64_t row0;                // first row of the sequence
+  int rows, r0, head;          // rows of the unit (0: none is left), its first, its kv head
+  int last;                    // the workgroup that has the unit's last step
+};
+
+namespace {
+
+constexpr int slot_floats(int dim) { return kRows * (dim + 2); }
+
 template <int FMT, int D>
-__global__ __launch_bounds__(64 * kWaves) void kv_attn_kernel(KvAttn A) {
+__global__ __launch_bounds__(64 * kWaves, 3) void kv_attn_kernel(KvAttn A) {
   using G = Geo<FMT, D>;
   constexpr int LD = D + 4;                            // a row in LDS: the lanes' rows meet different banks
   __shared__ float stats[2][kWaves][kRows];
   __shared__ float part[kWaves][kRows * LD];
   const int lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Unit U = find_unit(A, blockIdx.x, blockIdx.y);
-  if (U.rows == 0) return;
   int ek = 0, ev = 0;
   if constexpr (G::NV) {
     ek = A.c.texp[0];
     ev = A.c.texp[1];
   }
+  __shared__ int64_t upto[kWaves][64];
+  Cursor cur;
+  cur.upto = upto[wave];
+  const int64_t total = cur.total(A);
+  const Shares shares(total, gridDim.x);
+  int64_t at = shares.first(blockIdx.x);
+  const int64_t stop = shares.first(blockIdx.x + 1);
+  Left left = {0, 0, 0, 0, 0};
+  while (at < stop) {
+  int64_t from;
+  const int seq = cur.seek(A, at, &from);
+  const Span U = span_of(A, seq);
+  const int64_t rel = at - from;
+  const int unit = rel >> 31 ? (int)(rel / U.steps) : (int)((uint32_t)rel / (uint32_t)U.steps);
+  const int s0 = (int)(rel - (int64_t)unit * U.steps);
+  const int s1 = stop - at < U.steps - s0 ? s0 + (int)(stop - at) : U.steps;
+  at += s1 - s0;
+  const int head = unit / U.tiles, r0 = unit % U.tiles * kRows;
+  const int rows = U.rows - r0 < kRows ? U.rows - r0 : kRows;
   Rows<FMT, D> R;
-  const int r = U.r0 + n, tok = r / A.group;
-  const bool mine = n < U.rows;
-  R.start(mine ? A.q + (U.row0 + tok) * A.ldq + (int64_t)(U.head * A.group + r % A.group) * D : nullptr, A.scale, ek);
-  // keys of this lane's row, and of the unit
-  auto limit = [&](int64_t p) { return (int)(p < 0 ? -1 : p >= A.b.max_len ? A.b.max_len - 1 : p); };
-  auto from = [&](int64_t p) { return A.window && p >= A.window ? limit(p - A.window + 1) : 0; };
-  R.last = mine ? limit(U.pos0 + tok) : -1;
-  R.first = from(U.pos0 + tok);
-  const int last = limit(U.pos0 + (U.r0 + U.rows - 1) / A.group);
-  const int first = from(U.pos0 + U.r0 / A.group);
-
-  // keys that every row of the unit sees, between two tests of single keys
-  const int every_first = from(U.pos0 + (U.r0 + U.rows - 1) / A.group), every_last = limit(U.pos0 + U.r0 / A.group);
-  constexpr int kStep = 32 * kWaves;
+  const int r = r0 + n, tok = r / A.group;
+  const bool mine = n < rows;
+  R.start(mine ? A.q + (U.row0 + tok) * A.ldq + (int64_t)(head * A.group + r % A.group) * D : nullptr, A.scale, ek);
+  // keys of this lane's row, of any row of the unit and of all
+  const int64_t p0 = U.pos0 + r0 / A.group, p1 = U.pos0 + (r0 + rows - 1) / A.group;
+  R.last = mine ? limit(A, U.pos0 + tok) : -1;
+  R.first = first_key(A, U.pos0 + tok);
+  const int first = first_key(A, p0), every_first = first_key(A, p1), every_last = limit(A, p0);
+  const int begin = (first_key(A, U.pos0) & ~31) + s0 * kStep;
+  const int last = s1 == U.steps ? limit(A, p1) : (begin + (s1 - s0) * kStep - 1 < limit(A, p1) ? begin + (s1 - s0) * kStep - 1 : limit(A, p1));
   struct Pages {
     int p[2];
   };
   auto pages = [&](int key) {
     Pages g;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) g.p[h] = key + 16 * h <= last ? kv_page(A.c, A.b, U.seq, key + 16 * h) : -1;
+    for (int h = 0; h < 2; ++h) g.p[h] = key + 16 * h <= last ? kv_page(A.c, A.b, seq, key + 16 * h) : -1;
     return g;
   };
   auto load = [&](int key, const Pages& g, Tile<FMT, D>& T) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      load_half<FMT, D>(A.c, kv_slot(A.c, g.p[h] < 0 ? 0 : g.p[h], U.head, (key + 16 * h) & ((1 << A.c.shift) - 1)), h, T);
+      load_half<FMT, D>(A.c, kv_slot(A.c, g.p[h] < 0 ? 0 : g.p[h], head, (key + 16 * h) & ((1 << A.c.shift) - 1)), h, T);
   };
   auto use = [&](int key, const Pages& g, Tile<FMT, D>& T) {
     f4_t s[2];
@@ -407,7 +502,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attn_kernel(KvAttn A) {
       }
     }
   };
-  int key = (first & ~31) + 32 * wave;
+  int key = begin + 32 * wave;
   Tile<FMT, D> T0, T1;
   Pages g0 = pages(key), g1 = pages(key + kStep);
   if (key <= last) load(key, g0, T0);
@@ -446,37 +541,119 @@ __global__ __launch_bounds__(64 * kWaves) void kv_attn_kernel(KvAttn A) {
     w[i] = __builtin_amdgcn_exp2f(stats[0][i][row] - M);
     L += stats[1][i][row] * w[i];
   }
+  if (row < rows) {
+    const bool all = s1 - s0 == U.steps;               // the unit's: the output; else a slot, the first of a share
+    const int rr = r0 + row;                           // where it goes on with a unit, the second where it leaves one
+    const int64_t t = U.row0 + rr / A.group;
+    const int qh = head * A.group + rr % A.group;
+    float* slot = A.part + (2 * (int64_t)blockIdx.x + (s0 == 0)) * slot_floats(D);
+    const float inv = !all ? 1.0f : L == 0.0f ? 0.0f : ldexpf(1.0f / L, ev);
+#pragma unroll
+    for (int d = 0; d < D / 16; d += 4) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) x[e] += part[i][row * LD + d0 + d + e] * w[i];
+        x[e] *= inv;
+      }
+      if (all)
+        store_whole(A.out, false, t * A.ldo + (int64_t)qh * D + d0 + d, x);
+      else
+        store_whole(slot, true, 2 * kRows + row * D + d0 + d, x);
+    }
+    if (d0 == 0) {
+      if (!all) {
+        slot[row] = M;
+        slot[kRows + row] = L;
+      } else if (A.lse) {
+        A.lse[t * A.q_heads + qh] = L == 0.0f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(L)) * 0.693147180559945309f;
+      }
+    }
+  }
+  if (s0 == 0 && s1 < U.steps) left = Left{U.row0, rows, r0, head, shares.owner(at - s1 + U.steps - 1)};
+  if (at < stop) __syncthreads();
+  }
+  if (threadIdx.x == 0) A.left[blockIdx.x] = left;
+}
+
+// A unit that several workgroups had a share of, joined: blockIdx.x is the one
+// that has its first step, blockIdx.y the row. The parts are taken by several
+// groups of lanes and added in a fixed order.
+template <int D>
+__global__ __launch_bounds__(256) void kv_join_kernel(KvAttn A, bool nv) {
+  constexpr int LR = D / 4, SUBS = 256 / LR;           // lanes of a row, parts taken at once
+  __shared__ float sm[SUBS], sl[SUBS];
+  __shared__ f4_t so[SUBS][LR];
+  const int w0 = blockIdx.x, row = blockIdx.y;
+  const Left U = A.left[w0];
   if (row >= U.rows) return;
+  const int w1 = U.last;
+  auto slot = [&](int w) { return A.part + (2 * (int64_t)w + (w == w0)) * slot_floats(D); };
+  const int sub = threadIdx.x / LR, d = threadIdx.x % LR * 4;
+  float M = kLowest, L = 0.0f;
+  f4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int w = w0 + sub; w <= w1; w += SUBS) M = fmaxf(M, slot(w)[row]);
+#pragma unroll 4
+  for (int w = w0 + sub; w <= w1; w += SUBS) {
+    const float* p = slot(w);
+    const float f = __builtin_amdgcn_exp2f(p[row] - M);
+    L += p[kRows + row] * f;
+    x += *reinterpret_cast<const f4_t*>(p + 2 * kRows + row * D + d) * f;
+  }
+  so[sub][threadIdx.x % LR] = x;
+  if (d == 0) {
+    sm[sub] = M;
+    sl[sub] = L;
+  }
+  __syncthreads();
+  if (sub) return;
+  M = kLowest;
+  L = 0.0f;
+  x = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < SUBS; ++i) M = fmaxf(M, sm[i]);
+#pragma unroll
+  for (int i = 0; i < SUBS; ++i) {
+    const float f = __builtin_amdgcn_exp2f(sm[i] - M);
+    L += sl[i] * f;
+    x += so[i][threadIdx.x] * f;
+  }
   const int rr = U.r0 + row;
   const int64_t t = U.row0 + rr / A.group;
   const int qh = U.head * A.group + rr % A.group;
-  const float inv = L == 0.0f ? 0.0f : ldexpf(1.0f / L, ev);
-#pragma unroll
-  for (int d = 0; d < D / 16; d += 4) {
-    float x[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[e] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) x[e] += part[i][row * LD + d0 + d + e] * w[i];
-      x[e] *= inv;
-    }
-    store_whole(A.out, false, t * A.ldo + (int64_t)qh * D + d0 + d, x);
-  }
-  if (A.lse && d0 == 0)
+  const float inv = L == 0.0f ? 0.0f : ldexpf(1.0f / L, nv ? A.c.texp[1] : 0);
+  const float y[4] = {x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv};
+  store_whole(A.out, false, t * A.ldo + (int64_t)qh * D + d, y);
+  if (A.lse && d == 0)
     A.lse[t * A.q_heads + qh] = L == 0.0f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(L)) * 0.693147180559945309f;
 }
 
 }  // namespace
 
+// Workgroups of the split kernel: as many as are resident.
+constexpr int workers_of(int dim) { return dim == 64 ? 1024 : dim == 128 ? 768 : 256; }
+
 int64_t kv_attn_tiles(int64_t tokens, int64_t seqs, int64_t group, bool cu) {
   return cu ? tokens * group / kRows + seqs : tokens * ((group + kRows - 1) / kRows);
 }
 
-hipError_t launch_kv_attn(int format, int dim, const KvAttn& a, hipStream_t s) {
-  const dim3 grid((unsigned)kv_attn_tiles(a.tokens, a.b.seqs, a.group, a.b.cu), (unsigned)a.c.heads);
+size_t kv_attn_slots(int dim) {
+  return (size_t)workers_of(dim) * (2 * slot_floats(dim) * sizeof(float) + sizeof(Left));
+}
+
+
+hipError_t launch_kv_attn(int format, int dim, KvAttn a, hipStream_t s) {
+  a.left = reinterpret_cast<Left*>(a.part + (size_t)workers_of(dim) * 2 * slot_floats(dim));
   auto go = [&](auto f, auto d) {
-    kv_attn_kernel<decltype(f)::value, decltype(d)::value><<<grid, 64 * kWaves, 0, s>>>(a);
+    constexpr int D = decltype(d)::value;
+    kv_attn_kernel<decltype(f)::value, D><<<workers_of(D), 64 * kWaves, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t rows = a.b.cu ? kRows : a.group;     // a unit has no more
+    kv_join_kernel<D><<<dim3(workers_of(D) - 1, rows < kRows ? rows : kRows), 256, 0, s>>>(a, format == SNIP_NVFP4);
     return hipGetLastError();
   };
   auto of = [&](auto f) {
