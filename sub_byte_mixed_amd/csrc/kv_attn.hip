@@ -421,25 +421,31 @@ __global__ __launch_bounds__(64 * kWaves, 3) void kv_attn_kernel(KvAttn A) {
   const int first = first_key(A, p0), every_first = first_key(A, p1), every_last = limit(A, p0);
   const int begin = (first_key(A, U.pos0) & ~31) + s0 * kStep;
   const int last = s1 == U.steps ? limit(A, p1) : (begin + (s1 - s0) * kStep - 1 < limit(A, p1) ? begin + (s1 - s0) * kStep - 1 : limit(A, p1));
+  // The table's entries are asked for two steps ahead, as scalars of the constant
+  // address space: a vector load would be waited for in order with the keys'.
   struct Pages {
     int p[2];
   };
+  typedef const __attribute__((address_space(4))) int32_t* Entries;
+  const Entries entries = (Entries)(uintptr_t)(A.b.table + (int64_t)seq * A.b.table_ld);
   auto pages = [&](int key) {
     Pages g;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) g.p[h] = key + 16 * h <= last ? kv_page(A.c, A.b, seq, key + 16 * h) : -1;
+    for (int h = 0; h < 2; ++h) g.p[h] = entries[(key + 16 * h < last ? key + 16 * h : last) >> A.c.shift];
     return g;
   };
+  auto mapped = [&](const Pages& g, int h) { return (uint32_t)g.p[h] < (uint32_t)A.c.pages; };
+  // Loads are never skipped, since the wait for a tile counts those of the next
+  // one: beyond the last key, and where a page is not mapped, they read others.
   auto load = [&](int key, const Pages& g, Tile<FMT, D>& T) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      load_half<FMT, D>(A.c, kv_slot(A.c, g.p[h] < 0 ? 0 : g.p[h], head, (key + 16 * h) & ((1 << A.c.shift) - 1)), h, T);
+      load_half<FMT, D>(A.c, kv_slot(A.c, mapped(g, h) ? g.p[h] : 0, head, (key + 16 * h) & ((1 << A.c.shift) - 1)), h, T);
   };
   auto use = [&](int key, const Pages& g, Tile<FMT, D>& T) {
     f4_t s[2];
     scores<FMT, D>(T, R, s);
-    const bool whole = g.p[0] >= 0 && g.p[1] >= 0 && key >= every_first && key + 31 <= every_last;
-    float top = kLowest;
+    const bool whole = mapped(g, 0) & mapped(g, 1) & (key >= every_first) & (key + 31 <= every_last);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -447,18 +453,19 @@ __global__ __launch_bounds__(64 * kWaves, 3) void kv_attn_kernel(KvAttn A) {
     if (!whole) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        const int k0 = key + 16 * h + 4 * c, end = mapped(g, h) ? last : -1, mine_end = R.last < end ? R.last : end;
         uint32_t keep = 0u;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int k = key + 16 * h + 4 * c + j;
-          s[h][j] = g.p[h] >= 0 && k >= R.first && k <= R.last ? s[h][j] : -__builtin_inff();
-          keep |= g.p[h] >= 0 && k >= first && k <= last ? 0xFFu << (8 * j) : 0u;
+          s[h][j] = (k0 + j >= R.first) & (k0 + j <= mine_end) ? s[h][j] : -__builtin_inff();
+          keep |= (k0 + j >= first) & (k0 + j <= end) ? 0xFFu << (8 * j) : 0u;
         }
         // values of places that no row sees may be anything: their scales are replaced
 #pragma unroll
         for (int l = 0; l < G::VL; ++l) T.vs[h][l] &= keep;
       }
     }
+    float top = kLowest;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -504,20 +511,23 @@ __global__ __launch_bounds__(64 * kWaves, 3) void kv_attn_kernel(KvAttn A) {
   };
   int key = begin + 32 * wave;
   Tile<FMT, D> T0, T1;
-  Pages g0 = pages(key), g1 = pages(key + kStep);
-  if (key <= last) load(key, g0, T0);
-  while (key <= last) {
-    if (key + kStep <= last) load(key + kStep, g1, T1);
-    const Pages g2 = pages(key + 2 * kStep);
-    use(key, g0, T0);
-    key += kStep;
-    if (key > last) break;
-    if (key + kStep <= last) load(key + kStep, g2, T0);
-    const Pages g3 = pages(key + 2 * kStep);
-    use(key, g1, T1);
-    key += kStep;
-    g0 = g2;
-    g1 = g3;
+  if (key <= last) {
+    Pages g0 = pages(key), g1 = pages(key + kStep);
+    load(key, g0, T0);
+    while (true) {
+      load(key + kStep, g1, T1);
+      const Pages g2 = pages(key + 2 * kStep);
+      use(key, g0, T0);
+      key += kStep;
+      if (key > last) break;
+      load(key + kStep, g2, T0);
+      const Pages g3 = pages(key + 2 * kStep);
+      use(key, g1, T1);
+      key += kStep;
+      if (key > last) break;
+      g0 = g2;
+      g1 = g3;
+    }
   }
 
   // the waves' shares of the rows, joined
