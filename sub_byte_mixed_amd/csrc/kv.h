@@ -54,6 +54,7 @@ struct KvAttn {
   int64_t ldq, ldo, tokens;
   int32_t q_heads, group;      // query heads of a kv head
   int32_t window;              // 0: none
+  int32_t step;                // keys of a step of work, a multiple of a workgroup's
   float scale;                 // times log2 e
 };
 
@@ -65,7 +66,7 @@ constexpr int kv_scale_piece(int dim, int block) {
 }
 
 // Row tiles of an attention call, of every kv head.
-int64_t kv_attn_tiles(int64_t tokens, int64_t seqs, int64_t group, bool cu);
+int64_t kv_attn_tiles(int64_t tokens, int64_t seqs, int64_t group);
 
 size_t kv_attn_slots(int dim);
 

@@ -68,7 +68,7 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
 template <int FMT, int D>
 __device__ __forceinline__ void load_half(const KvCache& C, int64_t slot, int h, Tile<FMT, D>& T) {
   using G = Geo<FMT, D>;
-  const int lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4;
+  const uint32_t lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4;   // unsigned: added to scalar bases by the loads
   const uint8_t* kc = C.kc + slot * (D / 2);
   const uint8_t* ks = C.ks + slot * (D / G::BLK);
   const uint8_t* vc = C.vc + slot * (D / 2);
@@ -204,19 +204,20 @@ struct Rows {
 #pragma unroll
     for (int l_ = 0; l_ < G::KL; ++l_)
 #pragma unroll
-      for (int w = 0; w < G::KD; ++w) {
+      for (int w = 0; w < G::KD; ++w)
         q[l_][w] = qp ? *reinterpret_cast<const u32x4_t*>(qp + (c + 4 * l_) * 2 * G::PB + 8 * w) : u32x4_t{0u, 0u, 0u, 0u};
-        if constexpr (G::NV) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) big = fmaxf(big, fmaxf(fabsf(bf16_lo(q[l_][w][i])), fabsf(bf16_hi(q[l_][w][i]))));
-        }
-      }
     factor = scale;
     if constexpr (G::NV) {
+#pragma unroll
+      for (int l_ = 0; l_ < G::KL; ++l_)
+#pragma unroll
+        for (int w = 0; w < G::KD; ++w)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) big = fmaxf(big, fmaxf(fabsf(bf16_lo(q[l_][w][i])), fabsf(bf16_hi(q[l_][w][i]))));
+      big = row_max(big);
       int e;
-      frexpf(row_max(big), &e);
-      const bool finite = row_max(big) < __builtin_inff();
-      e = finite ? e : 0;
+      frexpf(big, &e);
+      e = big < __builtin_inff() ? e : 0;
 #pragma unroll
       for (int l_ = 0; l_ < G::KL; ++l_)
 #pragma unroll
@@ -233,37 +234,16 @@ struct Rows {
   }
 };
 
-// Scores of 32 keys for 16 rows: s[half][j] is key 16 half + 4 c + j.
-template <int FMT, int D>
-__device__ __forceinline__ void scores(const Tile<FMT, D>& T, const Rows<FMT, D>& R, f4_t (&s)[2]) {
-  using G = Geo<FMT, D>;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    s[h] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int l = 0; l < G::KL; ++l) {
-      h2_t sc = {};
-      float e = 0.0f;
-      if constexpr (G::NV)
-        sc = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(T.ks[h][l], 1.0f, false);
-      else
-        e = e8m0_val(T.ks[h][l]);
-#pragma unroll
-      for (int w = 0; w < G::KD; ++w) {
-        const int b = G::SB == 2 ? w / 2 : 0;          // block of the piece
-        s[h] = mfma<FMT>(decode_key<FMT>(T.k[h][l][w], h2_t{sc[b], sc[b]}, e), R.q[l][w], s[h]);
-      }
-    }
-  }
-}
+// Loads whose address is the same in the wave's lanes, of what the launch does
+// not write: scalar, and not waited for in order with the vector loads.
+typedef const __attribute__((address_space(4))) int32_t* Entries;
+__device__ __forceinline__ Entries entries(const int32_t* p) { return (Entries)(uintptr_t)p; }
 
-// Work is counted in steps: the workgroup's waves take 32 keys each. A unit --
-// 16 rows of one kv head of one sequence -- has the steps of the sequence's
-// keys, units follow each other by sequence, head and rows, and the steps of the
-// call are shared evenly among the workgroups, whatever the lengths. A workgroup
-// finds its share from lens and cu alone, so a captured launch follows them.
-constexpr int kStep = 32 * kWaves;
-
+// Work is counted in steps of a number of keys. A unit -- 16 R rows of one kv
+// head of one sequence -- has the steps of the sequence's keys, units follow each
+// other by sequence, head and rows, and the steps of the call are shared evenly
+// among the workgroups, whatever the lengths. A workgroup finds its share from
+// lens and cu alone, so a captured launch follows them.
 struct Span {                  // of one sequence
   int64_t row0, pos0;          // first row in the call's matrices, its position
   int rows;                    // (token, query head) pairs of a kv head
@@ -278,96 +258,88 @@ __device__ __forceinline__ int first_key(const KvAttn& A, int64_t p) {
   return A.window && p >= A.window ? limit(A, p - A.window + 1) : 0;
 }
 
-__device__ __forceinline__ Span span_of(const KvAttn& A, int b) {
+__device__ __forceinline__ Span span_of(const KvAttn& A, int b, int unit_rows) {
   Span x = {};
   if (b >= A.b.seqs) return x;
   int64_t a = b, e = b + 1;
   if (A.b.cu) {
-    a = A.b.cu[b];
-    e = A.b.cu[b + 1];
+    a = entries(A.b.cu)[b];
+    e = entries(A.b.cu)[b + 1];
   }
-  const int64_t len = A.b.lens[b];
+  const int64_t len = entries(A.b.lens)[b];
   x.row0 = a;
   x.pos0 = len - (e - a);
   if (e > A.tokens) e = A.tokens;
   if (a < 0 || e <= a) return x;
   x.rows = (int)(e - a) * A.group;
-  x.tiles = (x.rows + kRows - 1) / kRows;
+  x.tiles = (x.rows + unit_rows - 1) / unit_rows;
   const int n = limit(A, len - 1) + 1 - (first_key(A, x.pos0) & ~31);
-  x.steps = n > kStep ? (n + kStep - 1) / kStep : 1;   // a unit without keys writes its zeros
+  x.steps = n > A.step ? (n + A.step - 1) / A.step : 1;   // a unit without keys writes its zeros
   return x;
 }
 
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
-                   (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+// Sum over the lanes up to and with each.
+__device__ __forceinline__ int wave_prefix(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // the rows before: row_bcast 15, 31
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
 }
 
 // The sequences 64 at a time: the steps up to and with each of them, in the
 // wave's own LDS (a register each would cost the kernel a wave of occupancy).
 struct Cursor {
-  int64_t* upto;               // [64]
-  int seq0;
-  int64_t before, end;         // steps before the 64, and with them
+  int* upto;                   // [64]
+  int unit_rows, seq0;
+  int before, end;             // steps before the 64, and with them
 
-  __device__ __forceinline__ void load(const KvAttn& A, int s0, int64_t b) {
+  __device__ __forceinline__ void load(const KvAttn& A, int s0, int b) {
     const int lane = threadIdx.x & 63;
-    const Span x = span_of(A, s0 + lane);
-    int64_t n = (int64_t)x.tiles * x.steps * A.c.heads;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t v = __shfl_up(n, o, 64);
-      if (lane >= o) n += v;
-    }
+    const Span x = span_of(A, s0 + lane, unit_rows);
+    const int n = b + wave_prefix(x.tiles * x.steps * A.c.heads);
     seq0 = s0;
     before = b;
-    end = uniform(b + __shfl(n, 63, 64));
-    upto[lane] = b + n;
+    end = __builtin_amdgcn_readlane(n, 63);
+    upto[lane] = n;
     __builtin_amdgcn_wave_barrier();
   }
   // Steps of all sequences; leaves the cursor at the first ones.
-  __device__ __forceinline__ int64_t total(const KvAttn& A) {
+  __device__ __forceinline__ int total(const KvAttn& A) {
     load(A, 0, 0);
     if (A.b.seqs <= 64) return end;
     for (int s = 64; s < A.b.seqs; s += 64) load(A, s, end);
-    const int64_t n = end;
+    const int n = end;
     load(A, 0, 0);
     return n;
   }
   // The sequence that step `at` is in, and the steps before it.
-  __device__ __forceinline__ int seek(const KvAttn& A, int64_t at, int64_t* from) {
+  __device__ __forceinline__ int seek(const KvAttn& A, int at, int* from) {
     while (at >= end) load(A, seq0 + 64, end);
     const int i = __ffsll((unsigned long long)__ballot(upto[threadIdx.x & 63] > at)) - 1;
-    *from = i ? uniform(upto[i - 1]) : before;
+    *from = i ? __builtin_amdgcn_readfirstlane(upto[i - 1]) : before;
     return seq0 + i;
   }
 };
 
 // The steps of n workgroups: q each, one more for the first r.
 struct Shares {
-  int64_t q, r;
-  __device__ __forceinline__ Shares(int64_t total, int n) {
-    if (total >> 31) {
-      q = total / n;
-    } else {
-      q = (uint32_t)total / (uint32_t)n;
-    }
-    r = total - q * n;
-  }
-  __device__ __forceinline__ int64_t first(int w) const { return w * q + (w < r ? w : r); }
-  __device__ __forceinline__ int owner(int64_t at) const {   // of a step
-    const int64_t many = r * (q + 1);
-    if (at < many) return at >> 31 ? (int)(at / (q + 1)) : (int)((uint32_t)at / (uint32_t)(q + 1));
-    const int64_t rest = at - many;
-    return (int)r + (rest >> 31 ? (int)(rest / q) : (int)((uint32_t)rest / (uint32_t)q));
+  uint32_t q, r;
+  __device__ __forceinline__ Shares(uint32_t total, uint32_t n) : q(total / n), r(total % n) {}
+  __device__ __forceinline__ int first(uint32_t w) const { return (int)(w * q + (w < r ? w : r)); }
+  __device__ __forceinline__ int owner(uint32_t at) const {   // of a step
+    const uint32_t many = r * (q + 1);
+    return (int)(at < many ? at / (q + 1) : r + (at - many) / q);
   }
 };
 
 }  // namespace
 
 // What a workgroup leaves for the joining launch: two slots, of the unit that
-// its share begins within and of the one that it ends within (16 maxima, 16
-// sums, 16 rows of output each), and where the latter's output belongs.
+// its share begins within and of the one that it ends within (maxima, sums and
+// rows of output), and where the latter's output belongs.
 struct Left {
   int64_t row0;                // first row of the sequence
   int rows, r0, head;          // rows of the unit (0: none is left), its first, its kv head
@@ -376,214 +348,269 @@ struct Left {
 
 namespace {
 
-constexpr int slot_floats(int dim) { return kRows * (dim + 2); }
+constexpr int slot_floats(int dim, int rows) { return rows * (dim + 2); }
 
-template <int FMT, int D>
-__global__ __launch_bounds__(64 * kWaves, 3) void kv_attn_kernel(KvAttn A) {
+// Row tiles of a unit, waves of a SIMD that the registers are held to, and
+// workgroups: as many as are resident.
+constexpr int most_tiles(int dim) { return dim == 256 ? 1 : 2; }
+constexpr int waves_of(int dim, int tiles) { return dim == 256 ? 2 : (dim == 128 ? 3 : 4) - (tiles == 2); }
+constexpr int workers_of(int dim, int tiles) { return 256 * waves_of(dim, tiles); }
+
+__device__ __forceinline__ void store_lse(const KvAttn& A, int64_t t, int qh, float M, float L) {
+  A.lse[t * A.q_heads + qh] = L == 0.0f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(L)) * 0.693147180559945309f;
+}
+
+template <int FMT, int D, int NR>
+__global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(KvAttn A) {
   using G = Geo<FMT, D>;
   constexpr int LD = D + 4;                            // a row in LDS: the lanes' rows meet different banks
+  constexpr int kKeys = 32 * kWaves;                   // of a round of the waves
+  constexpr int kUnit = kRows * NR;
   __shared__ float stats[2][kWaves][kRows];
   __shared__ float part[kWaves][kRows * LD];
+  __shared__ int upto[kWaves][64];
   const int lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int ek = 0, ev = 0;
-  if constexpr (G::NV) {
-    ek = A.c.texp[0];
-    ev = A.c.texp[1];
-  }
-  __shared__ int64_t upto[kWaves][64];
+  const int ek = G::NV ? entries(A.c.texp)[0] : 0, ev = G::NV ? entries(A.c.texp)[1] : 0;
   Cursor cur;
   cur.upto = upto[wave];
-  const int64_t total = cur.total(A);
-  const Shares shares(total, gridDim.x);
-  int64_t at = shares.first(blockIdx.x);
-  const int64_t stop = shares.first(blockIdx.x + 1);
+  cur.unit_rows = kUnit;
+  const Shares shares(cur.total(A), gridDim.x);
+  int at = shares.first(blockIdx.x);
+  const int stop = shares.first(blockIdx.x + 1);
   Left left = {0, 0, 0, 0, 0};
   while (at < stop) {
-  int64_t from;
-  const int seq = cur.seek(A, at, &from);
-  const Span U = span_of(A, seq);
-  const int64_t rel = at - from;
-  const int unit = rel >> 31 ? (int)(rel / U.steps) : (int)((uint32_t)rel / (uint32_t)U.steps);
-  const int s0 = (int)(rel - (int64_t)unit * U.steps);
-  const int s1 = stop - at < U.steps - s0 ? s0 + (int)(stop - at) : U.steps;
-  at += s1 - s0;
-  const int head = unit / U.tiles, r0 = unit % U.tiles * kRows;
-  const int rows = U.rows - r0 < kRows ? U.rows - r0 : kRows;
-  Rows<FMT, D> R;
-  const int r = r0 + n, tok = r / A.group;
-  const bool mine = n < rows;
-  R.start(mine ? A.q + (U.row0 + tok) * A.ldq + (int64_t)(head * A.group + r % A.group) * D : nullptr, A.scale, ek);
-  // keys of this lane's row, of any row of the unit and of all
-  const int64_t p0 = U.pos0 + r0 / A.group, p1 = U.pos0 + (r0 + rows - 1) / A.group;
-  R.last = mine ? limit(A, U.pos0 + tok) : -1;
-  R.first = first_key(A, U.pos0 + tok);
-  const int first = first_key(A, p0), every_first = first_key(A, p1), every_last = limit(A, p0);
-  const int begin = (first_key(A, U.pos0) & ~31) + s0 * kStep;
-  const int last = s1 == U.steps ? limit(A, p1) : (begin + (s1 - s0) * kStep - 1 < limit(A, p1) ? begin + (s1 - s0) * kStep - 1 : limit(A, p1));
-  // The table's entries are asked for two steps ahead, as scalars of the constant
-  // address space: a vector load would be waited for in order with the keys'.
-  struct Pages {
-    int p[2];
-  };
-  typedef const __attribute__((address_space(4))) int32_t* Entries;
-  const Entries entries = (Entries)(uintptr_t)(A.b.table + (int64_t)seq * A.b.table_ld);
-  auto pages = [&](int key) {
-    Pages g;
+    int from;
+    const int seq = cur.seek(A, at, &from);
+    const Span U = span_of(A, seq, kUnit);
+    const int unit = (at - from) / U.steps, s0 = (at - from) % U.steps;
+    const int s1 = stop - at < U.steps - s0 ? s0 + (stop - at) : U.steps;
+    at += s1 - s0;
+    const int head = unit / U.tiles, r0 = unit % U.tiles * kUnit;
+    const int rows = U.rows - r0 < kUnit ? U.rows - r0 : kUnit;
+    Rows<FMT, D> R[NR];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) g.p[h] = entries[(key + 16 * h < last ? key + 16 * h : last) >> A.c.shift];
-    return g;
-  };
-  auto mapped = [&](const Pages& g, int h) { return (uint32_t)g.p[h] < (uint32_t)A.c.pages; };
-  // Loads are never skipped, since the wait for a tile counts those of the next
-  // one: beyond the last key, and where a page is not mapped, they read others.
-  auto load = [&](int key, const Pages& g, Tile<FMT, D>& T) {
+    for (int i = 0; i < NR; ++i) {
+      const int r = r0 + kRows * i + n, tok = r / A.group;
+      const bool mine = kRows * i + n < rows;
+      R[i].start(mine ? A.q + (U.row0 + tok) * A.ldq + (int64_t)(head * A.group + r % A.group) * D : nullptr, A.scale, ek);
+      R[i].last = mine ? limit(A, U.pos0 + tok) : -1;
+      R[i].first = first_key(A, U.pos0 + tok);
+    }
+    // keys of any row of the unit, and of all
+    const int64_t p0 = U.pos0 + r0 / A.group, p1 = U.pos0 + (r0 + rows - 1) / A.group;
+    const int first = first_key(A, p0), every_first = first_key(A, p1), every_last = limit(A, p0);
+    const int64_t begin64 = (int64_t)(first_key(A, U.pos0) & ~31) + (int64_t)s0 * A.step;
+    const int begin = (int)begin64;
+    const int64_t end64 = begin64 + (int64_t)(s1 - s0) * A.step - 1;
+    const int last = end64 < limit(A, p1) ? (int)end64 : limit(A, p1);
+
+    // The table's entries are asked for two rounds ahead.
+    struct Pages {
+      int p[2];
+    };
+    const Entries table = entries(A.b.table + (int64_t)seq * A.b.table_ld);
+    auto pages = [&](int key) {
+      Pages g;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      load_half<FMT, D>(A.c, kv_slot(A.c, mapped(g, h) ? g.p[h] : 0, head, (key + 16 * h) & ((1 << A.c.shift) - 1)), h, T);
-  };
-  auto use = [&](int key, const Pages& g, Tile<FMT, D>& T) {
-    f4_t s[2];
-    scores<FMT, D>(T, R, s);
-    const bool whole = mapped(g, 0) & mapped(g, 1) & (key >= every_first) & (key + 31 <= every_last);
+      for (int h = 0; h < 2; ++h) g.p[h] = table[(key + 16 * h < last ? key + 16 * h : last) >> A.c.shift];
+      return g;
+    };
+    auto mapped = [&](const Pages& g, int h) { return (uint32_t)g.p[h] < (uint32_t)A.c.pages; };
+    // Loads are never skipped, since the wait for a tile counts those of the next
+    // one: beyond the last key, and where a page is not mapped, they read others.
+    auto load = [&](int key, const Pages& g, Tile<FMT, D>& T) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s[h][j] *= R.factor;
-    if (!whole) {
+      for (int h = 0; h < 2; ++h)
+        load_half<FMT, D>(A.c, kv_slot(A.c, mapped(g, h) ? g.p[h] : 0, head, (key + 16 * h) & ((1 << A.c.shift) - 1)), h, T);
+    };
+    auto use = [&](int key, const Pages& g, Tile<FMT, D>& T) {
+      // scores: s[i][h][j] is key 16 h + 4 c + j for row n of tile i
+      f4_t s[NR][2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int k0 = key + 16 * h + 4 * c, end = mapped(g, h) ? last : -1, mine_end = R.last < end ? R.last : end;
-        uint32_t keep = 0u;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) s[i][h] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int l = 0; l < G::KL; ++l) {
+          h2_t sc = {};
+          float e = 0.0f;
+          if constexpr (G::NV)
+            sc = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(T.ks[h][l], 1.0f, false);
+          else
+            e = e8m0_val(T.ks[h][l]);
+#pragma unroll
+          for (int w = 0; w < G::KD; ++w) {
+            const int b = G::SB == 2 ? w / 2 : 0;      // block of the piece
+            const u32x4_t k = decode_key<FMT>(T.k[h][l][w], h2_t{sc[b], sc[b]}, e);
+#pragma unroll
+            for (int i = 0; i < NR; ++i) s[i][h] = mfma<FMT>(k, R[i].q[l][w], s[i][h]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[i][h][j] *= R[i].factor;
+      const bool whole = mapped(g, 0) & mapped(g, 1) & (key >= every_first) & (key + 31 <= every_last);
+      if (!whole) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k0 = key + 16 * h + 4 * c, end = mapped(g, h) ? last : -1;
+          uint32_t keep = 0u;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+              s[i][h][j] = ((k0 + j >= R[i].first) & (k0 + j <= R[i].last) & (k0 + j <= end)) ? s[i][h][j] : -__builtin_inff();
+            keep |= ((k0 + j >= first) & (k0 + j <= end)) ? 0xFFu << (8 * j) : 0u;
+          }
+          // values of places that no row sees may be anything: their scales are replaced
+#pragma unroll
+          for (int l = 0; l < G::VL; ++l) T.vs[h][l] &= keep;
+        }
+      }
+      // The maximum may lag by 2^8: terms of up to 256 are as exact, and most tiles leave the output as it is.
+      float top[NR];
+      bool above = false;
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        top[i] = kLowest;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top[i] = fmaxf(top[i], s[i][h][j]);
+        above |= top[i] > R[i].m + 8.0f;
+      }
+      if (__any(above)) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const float m = fmaxf(row_max(top[i]), R[i].m), f = __builtin_amdgcn_exp2f(R[i].m - m);
+          R[i].m = m;
+          R[i].l *= f;
+#pragma unroll
+          for (int d = 0; d < G::DT; ++d) R[i].o[d] *= f;
+        }
+      }
+      u32x4_t ph[NR], pl[NR];                          // fp16, or the two parts in bf16
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        float p[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          p[j] = __builtin_amdgcn_exp2f(s[i][j / 4][j % 4] - R[i].m);
+          R[i].l += p[j];
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s[h][j] = (k0 + j >= R.first) & (k0 + j <= mine_end) ? s[h][j] : -__builtin_inff();
-          keep |= (k0 + j >= first) & (k0 + j <= end) ? 0xFFu << (8 * j) : 0u;
+          if constexpr (G::NV) {
+            ph[i][j] = bits(h2_t{(_Float16)p[2 * j], (_Float16)p[2 * j + 1]});
+          } else {
+            ph[i][j] = pack_bf16(p[2 * j], p[2 * j + 1]);
+            pl[i][j] = pack_bf16(p[2 * j] - bf16_lo(ph[i][j]), p[2 * j + 1] - bf16_hi(ph[i][j]));
+          }
         }
-        // values of places that no row sees may be anything: their scales are replaced
-#pragma unroll
-        for (int l = 0; l < G::VL; ++l) T.vs[h][l] &= keep;
       }
-    }
-    float top = kLowest;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int l = 0; l < G::VL; ++l) {
+        uint32_t v0[2 * G::VB][2], v1[2 * G::VB][2];
+        decode_values<FMT, D>(T.v[0][l], T.vs[0][l], v0);
+        decode_values<FMT, D>(T.v[1][l], T.vs[1][l], v1);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) top = fmaxf(top, s[h][j]);
-    // the maximum may lag by 2^8: terms of up to 256 are as exact, and most tiles leave the output as it is
-    if (__any(top > R.m + 8.0f)) {
-      top = fmaxf(row_max(top), R.m);
-      const float f = __builtin_amdgcn_exp2f(R.m - top);
-      R.m = top;
-      R.l *= f;
+        for (int d = 0; d < 2 * G::VB; ++d) {
+          const u32x4_t a = {v0[d][0], v0[d][1], v1[d][0], v1[d][1]};
 #pragma unroll
-      for (int i = 0; i < G::DT; ++i) R.o[i] *= f;
-    }
-    float p[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      p[i] = __builtin_amdgcn_exp2f(s[i / 4][i % 4] - R.m);
-      R.l += p[i];
-    }
-    u32x4_t ph, pl;                                    // fp16, or the two parts in bf16
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (G::NV) {
-        ph[i] = bits(h2_t{(_Float16)p[2 * i], (_Float16)p[2 * i + 1]});
-      } else {
-        ph[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
-        pl[i] = pack_bf16(p[2 * i] - bf16_lo(ph[i]), p[2 * i + 1] - bf16_hi(ph[i]));
+          for (int i = 0; i < NR; ++i) {
+            f4_t& o = R[i].o[l * 2 * G::VB + d];
+            o = mfma<FMT>(a, ph[i], o);
+            if constexpr (!G::NV) o = mfma<FMT>(a, pl[i], o);
+          }
+        }
       }
-    }
-#pragma unroll
-    for (int l = 0; l < G::VL; ++l) {
-      uint32_t v0[2 * G::VB][2], v1[2 * G::VB][2];
-      decode_values<FMT, D>(T.v[0][l], T.vs[0][l], v0);
-      decode_values<FMT, D>(T.v[1][l], T.vs[1][l], v1);
-#pragma unroll
-      for (int i = 0; i < 2 * G::VB; ++i) {
-        const u32x4_t a = {v0[i][0], v0[i][1], v1[i][0], v1[i][1]};
-        f4_t& o = R.o[l * 2 * G::VB + i];
-        o = mfma<FMT>(a, ph, o);
-        if constexpr (!G::NV) o = mfma<FMT>(a, pl, o);
-      }
-    }
-  };
-  int key = begin + 32 * wave;
-  Tile<FMT, D> T0, T1;
-  if (key <= last) {
-    Pages g0 = pages(key), g1 = pages(key + kStep);
-    load(key, g0, T0);
-    while (true) {
-      load(key + kStep, g1, T1);
-      const Pages g2 = pages(key + 2 * kStep);
-      use(key, g0, T0);
-      key += kStep;
-      if (key > last) break;
-      load(key + kStep, g2, T0);
-      const Pages g3 = pages(key + 2 * kStep);
-      use(key, g1, T1);
-      key += kStep;
-      if (key > last) break;
-      g0 = g2;
-      g1 = g3;
-    }
-  }
+    };
 
-  // the waves' shares of the rows, joined
-  const float l = row_sum(R.l);
-  if (c == 0) {
-    stats[0][wave][n] = R.m;
-    stats[1][wave][n] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < G::DT; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)                        // dimension of O^T's row 4 c + j in tile i
-      part[wave][n * LD + (i / (2 * G::VB)) * 32 * G::VB + (4 * c + j) * 2 * G::VB + i % (2 * G::VB)] = R.o[i][j];
-  __syncthreads();
-  const int row = threadIdx.x / 16, d0 = threadIdx.x % 16 * (D / 16);
-  float M = kLowest, L = 0.0f, w[kWaves];
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) M = fmaxf(M, stats[0][i][row]);
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    w[i] = __builtin_amdgcn_exp2f(stats[0][i][row] - M);
-    L += stats[1][i][row] * w[i];
-  }
-  if (row < rows) {
-    const bool all = s1 - s0 == U.steps;               // the unit's: the output; else a slot, the first of a share
-    const int rr = r0 + row;                           // where it goes on with a unit, the second where it leaves one
-    const int64_t t = U.row0 + rr / A.group;
-    const int qh = head * A.group + rr % A.group;
-    float* slot = A.part + (2 * (int64_t)blockIdx.x + (s0 == 0)) * slot_floats(D);
-    const float inv = !all ? 1.0f : L == 0.0f ? 0.0f : ldexpf(1.0f / L, ev);
-#pragma unroll
-    for (int d = 0; d < D / 16; d += 4) {
-      float x[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kWaves; ++i) x[e] += part[i][row * LD + d0 + d + e] * w[i];
-        x[e] *= inv;
-      }
-      if (all)
-        store_whole(A.out, false, t * A.ldo + (int64_t)qh * D + d0 + d, x);
-      else
-        store_whole(slot, true, 2 * kRows + row * D + d0 + d, x);
-    }
-    if (d0 == 0) {
-      if (!all) {
-        slot[row] = M;
-        slot[kRows + row] = L;
-      } else if (A.lse) {
-        A.lse[t * A.q_heads + qh] = L == 0.0f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(L)) * 0.693147180559945309f;
+    int key = begin + 32 * wave;
+    if (key <= last) {
+      Tile<FMT, D> T0, T1;
+      Pages g0 = pages(key), g1 = pages(key + kKeys);
+      load(key, g0, T0);
+      while (true) {
+        load(key + kKeys, g1, T1);
+        const Pages g2 = pages(key + 2 * kKeys);
+        use(key, g0, T0);
+        key += kKeys;
+        if (key > last) break;
+        load(key + kKeys, g2, T0);
+        const Pages g3 = pages(key + 2 * kKeys);
+        use(key, g1, T1);
+        key += kKeys;
+        if (key > last) break;
+        g0 = g2;
+        g1 = g3;
       }
     }
-  }
-  if (s0 == 0 && s1 < U.steps) left = Left{U.row0, rows, r0, head, shares.owner(at - s1 + U.steps - 1)};
-  if (at < stop) __syncthreads();
+
+    // the waves' shares of the rows, joined, a tile at a time
+    const bool all = s1 - s0 == U.steps;               // the unit's: the output; else a slot, the first where a share
+    float* slot = A.part + (2 * (int64_t)blockIdx.x + (s0 == 0)) * slot_floats(D, kUnit);   // goes on with a unit
+    if (s0 == 0 && !all) left = Left{U.row0, rows, r0, head, shares.owner(at - s1 + U.steps - 1)};
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      if (kRows * i >= rows) break;
+      const float l = row_sum(R[i].l);
+      if (c == 0) {
+        stats[0][wave][n] = R[i].m;
+        stats[1][wave][n] = l;
+      }
+#pragma unroll
+      for (int d = 0; d < G::DT; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)                    // dimension of O^T's row 4 c + j in tile d
+          part[wave][n * LD + (d / (2 * G::VB)) * 32 * G::VB + (4 * c + j) * 2 * G::VB + d % (2 * G::VB)] = R[i].o[d][j];
+      __syncthreads();
+      const int row = threadIdx.x / 16, d0 = threadIdx.x % 16 * (D / 16);
+      float M = kLowest, L = 0.0f, w[kWaves];
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) M = fmaxf(M, stats[0][k][row]);
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) {
+        w[k] = __builtin_amdgcn_exp2f(stats[0][k][row] - M);
+        L += stats[1][k][row] * w[k];
+      }
+      const int ur = kRows * i + row;
+      if (ur < rows) {
+        const int rr = r0 + ur;
+        const int64_t t = U.row0 + rr / A.group;
+        const int qh = head * A.group + rr % A.group;
+        const float inv = !all ? 1.0f : L == 0.0f ? 0.0f : ldexpf(1.0f / L, ev);
+#pragma unroll
+        for (int d = 0; d < D / 16; d += 4) {
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kWaves; ++k) x[e] += part[k][row * LD + d0 + d + e] * w[k];
+            x[e] *= inv;
+          }
+          if (all)
+            store_whole(A.out, false, t * A.ldo + (int64_t)qh * D + d0 + d, x);
+          else
+            store_whole(slot, true, 2 * kUnit + ur * D + d0 + d, x);
+        }
+        if (d0 == 0) {
+          if (!all) {
+            slot[ur] = M;
+            slot[kUnit + ur] = L;
+          } else if (A.lse) {
+            store_lse(A, t, qh, M, L);
+          }
+        }
+      }
+      if (i + 1 < NR || at < stop) __syncthreads();
+    }
   }
   if (threadIdx.x == 0) A.left[blockIdx.x] = left;
 }
@@ -591,16 +618,17 @@ __global__ __launch_bounds__(64 * kWaves, 3) void kv_attn_kernel(KvAttn A) {
 // A unit that several workgroups had a share of, joined: blockIdx.x is the one
 // that has its first step, blockIdx.y the row. The parts are taken by several
 // groups of lanes and added in a fixed order.
-template <int D>
+template <int D, int NR>
 __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn A, bool nv) {
   constexpr int LR = D / 4, SUBS = 256 / LR;           // lanes of a row, parts taken at once
+  constexpr int kUnit = kRows * NR;
   __shared__ float sm[SUBS], sl[SUBS];
   __shared__ f4_t so[SUBS][LR];
   const int w0 = blockIdx.x, row = blockIdx.y;
   const Left U = A.left[w0];
   if (row >= U.rows) return;
   const int w1 = U.last;
-  auto slot = [&](int w) { return A.part + (2 * (int64_t)w + (w == w0)) * slot_floats(D); };
+  auto slot = [&](int w) { return A.part + (2 * (int64_t)w + (w == w0)) * slot_floats(D, kUnit); };
   const int sub = threadIdx.x / LR, d = threadIdx.x % LR * 4;
   float M = kLowest, L = 0.0f;
   f4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -610,8 +638,8 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn A, bool nv) {
   for (int w = w0 + sub; w <= w1; w += SUBS) {
     const float* p = slot(w);
     const float f = __builtin_amdgcn_exp2f(p[row] - M);
-    L += p[kRows + row] * f;
-    x += *reinterpret_cast<const f4_t*>(p + 2 * kRows + row * D + d) * f;
+    L += p[kUnit + row] * f;
+    x += *reinterpret_cast<const f4_t*>(p + 2 * kUnit + row * D + d) * f;
   }
   so[sub][threadIdx.x % LR] = x;
   if (d == 0) {
@@ -637,42 +665,49 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn A, bool nv) {
   const float inv = L == 0.0f ? 0.0f : ldexpf(1.0f / L, nv ? A.c.texp[1] : 0);
   const float y[4] = {x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv};
   store_whole(A.out, false, t * A.ldo + (int64_t)qh * D + d, y);
-  if (A.lse && d == 0)
-    A.lse[t * A.q_heads + qh] = L == 0.0f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(L)) * 0.693147180559945309f;
+  if (A.lse && d == 0) store_lse(A, t, qh, M, L);
 }
 
 }  // namespace
 
-// Workgroups of the split kernel: as many as are resident.
-constexpr int workers_of(int dim) { return dim == 64 ? 1024 : dim == 128 ? 768 : 256; }
-
-int64_t kv_attn_tiles(int64_t tokens, int64_t seqs, int64_t group, bool cu) {
-  return cu ? tokens * group / kRows + seqs : tokens * ((group + kRows - 1) / kRows);
-}
+int64_t kv_attn_tiles(int64_t tokens, int64_t seqs, int64_t group) { return tokens * group / kRows + seqs; }
 
 size_t kv_attn_slots(int dim) {
-  return (size_t)workers_of(dim) * (2 * slot_floats(dim) * sizeof(float) + sizeof(Left));
+  size_t most = 0;
+  for (int t = 1; t <= most_tiles(dim); ++t) {
+    const size_t n = (size_t)workers_of(dim, t) * (2 * slot_floats(dim, kRows * t) * sizeof(float) + sizeof(Left));
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
-
 hipError_t launch_kv_attn(int format, int dim, KvAttn a, hipStream_t s) {
-  a.left = reinterpret_cast<Left*>(a.part + (size_t)workers_of(dim) * 2 * slot_floats(dim));
-  auto go = [&](auto f, auto d) {
-    constexpr int D = decltype(d)::value;
-    kv_attn_kernel<decltype(f)::value, D><<<workers_of(D), 64 * kWaves, 0, s>>>(a);
+  // steps are counted in 31 bits, whatever the lengths that the tables allow
+  const double tiles = (double)kv_attn_tiles(a.tokens, a.b.seqs, a.group) * a.c.heads;
+  a.step = 32 * kWaves;
+  while (a.step < a.b.max_len && tiles * ((double)a.b.max_len / a.step + 1.0) >= 2147483647.0) a.step *= 2;
+  const bool two = dim != 256 && a.tokens * a.group > kRows * (int64_t)a.b.seqs;   // rows of a sequence, on average
+  auto go = [&](auto f, auto d, auto t) {
+    constexpr int D = decltype(d)::value, NR = decltype(t)::value, W = workers_of(D, NR);
+    a.left = reinterpret_cast<Left*>(a.part + (size_t)W * 2 * slot_floats(D, kRows * NR));
+    kv_attn_kernel<decltype(f)::value, D, NR><<<W, 64 * kWaves, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t rows = a.b.cu ? kRows : a.group;     // a unit has no more
-    kv_join_kernel<D><<<dim3(workers_of(D) - 1, rows < kRows ? rows : kRows), 256, 0, s>>>(a, format == SNIP_NVFP4);
+    const int rows = !a.b.cu && a.group < kRows * NR ? a.group : kRows * NR;   // a unit has no more
+    kv_join_kernel<D, NR><<<dim3(W - 1, rows), 256, 0, s>>>(a, format == SNIP_NVFP4);
     return hipGetLastError();
   };
-  auto of = [&](auto f) {
-    return dim == 64    ? go(f, std::integral_constant<int, 64>{})
-           : dim == 128 ? go(f, std::integral_constant<int, 128>{})
-                        : go(f, std::integral_constant<int, 256>{});
+  auto of = [&](auto f, auto d) {
+    if constexpr (most_tiles(decltype(d)::value) > 1)
+      if (two) return go(f, d, std::integral_constant<int, 2>{});
+    return go(f, d, std::integral_constant<int, 1>{});
   };
-  return format == SNIP_NVFP4 ? of(std::integral_constant<int, SNIP_NVFP4>{})
-                              : of(std::integral_constant<int, SNIP_MXFP4>{});
+  auto at = [&](auto f) {
+    return dim == 64    ? of(f, std::integral_constant<int, 64>{})
+           : dim == 128 ? of(f, std::integral_constant<int, 128>{})
+                        : of(f, std::integral_constant<int, 256>{});
+  };
+  return format == SNIP_NVFP4 ? at(std::integral_constant<int, SNIP_NVFP4>{}) : at(std::integral_constant<int, SNIP_MXFP4>{});
 }
 
 }  // namespace snip
