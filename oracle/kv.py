@@ -52,8 +52,8 @@ def attention(q, k, v, pos, mapped, scale, window):
     pos [rows], mapped [tokens]. Returns out and lse (-inf and 0 for a row without
     keys) and, for bounds on rounding, sum p |v|, the largest sum |q| |k| * scale
     of a key that a row sees, and the number of keys."""
-    x = np.einsum("rhd,td->rht", q, k) * scale
-    size = np.einsum("rhd,td->rht", np.abs(q), np.abs(k)) * scale
+    x = np.matmul(q, k.T) * scale
+    size = np.matmul(np.abs(q), np.abs(k).T) * scale
     t = np.arange(k.shape[0])
     seen = (t[None] <= pos[:, None]) & mapped[None]
     if window:
@@ -68,5 +68,5 @@ def attention(q, k, v, pos, mapped, scale, window):
         lse = np.where(some, m + np.log(total), -np.inf)
     p = p / np.where(some, total, 1.0)[..., None]
     v = np.where(mapped[:, None], v, 0.0)
-    return (np.einsum("rht,td->rhd", p, v), lse, np.einsum("rht,td->rhd", p, np.abs(v)),
+    return (np.matmul(p, v), lse, np.matmul(p, np.abs(v)),
             np.where(seen, size, 0.0).max(axis=2, initial=0.0), seen.sum(axis=2))

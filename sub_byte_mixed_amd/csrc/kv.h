@@ -54,6 +54,7 @@ struct KvAttn {
   int64_t ldq, ldo, tokens;
   int32_t q_heads, group;      // query heads of a kv head
   int32_t window;              // 0: none
+  int32_t few, split;          // split: sequences of more rows than `few` have a launch of their own
   int32_t step;                // keys of a step of work, a multiple of a workgroup's
   float scale;                 // times log2 e
 };

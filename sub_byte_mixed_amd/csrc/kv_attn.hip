@@ -64,9 +64,11 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
   }
 }
 
-// 16 tokens from `slot` (wave-uniform) into half `h` of a tile.
+// 16 tokens from `slot` (wave-uniform): a lane's share.
 template <int FMT, int D>
-__device__ __forceinline__ void load_half(const KvCache& C, int64_t slot, int h, Tile<FMT, D>& T) {
+__device__ __forceinline__ void load_half(const KvCache& C, int64_t slot, uint32_t (&k)[Geo<FMT, D>::KL][Geo<FMT, D>::KD],
+                                          uint32_t (&ksc)[Geo<FMT, D>::KL], uint32_t (&v)[Geo<FMT, D>::VL][Geo<FMT, D>::VB],
+                                          uint32_t (&vsc)[Geo<FMT, D>::VL]) {
   using G = Geo<FMT, D>;
   const uint32_t lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4;   // unsigned: added to scalar bases by the loads
   const uint8_t* kc = C.kc + slot * (D / 2);
@@ -75,18 +77,18 @@ __device__ __forceinline__ void load_half(const KvCache& C, int64_t slot, int h,
   const uint8_t* vs = C.vs + slot * (D / G::BLK);
 #pragma unroll
   for (int l = 0; l < G::KL; ++l) {
-    load_words<G::KD>(kc + (64 * l + lane) * G::PB, T.k[h][l]);
+    load_words<G::KD>(kc + (64 * l + lane) * G::PB, k[l]);
     if constexpr (G::SB == 2)
-      T.ks[h][l] = *reinterpret_cast<const uint16_t*>(ks + (64 * l + lane) * 2);
+      ksc[l] = *reinterpret_cast<const uint16_t*>(ks + (64 * l + lane) * 2);
     else if constexpr (2 * G::PB < G::BLK)             // two pieces to a block
-      T.ks[h][l] = ks[c / 2 * 16 + n];
+      ksc[l] = ks[c / 2 * 16 + n];
     else
-      T.ks[h][l] = ks[64 * l + lane];
+      ksc[l] = ks[64 * l + lane];
   }
 #pragma unroll
   for (int l = 0; l < G::VL; ++l) {
-    load_words<G::VB>(vc + c * 2 * D + (16 * l + n) * 4 * G::VB, T.v[h][l]);
-    T.vs[h][l] = *reinterpret_cast<const uint32_t*>(vs + c * 4 * (D / G::BLK) + (16 * l + n) * 2 * G::VB / G::BLK * 4);
+    load_words<G::VB>(vc + c * 2 * D + (16 * l + n) * 4 * G::VB, v[l]);
+    vsc[l] = *reinterpret_cast<const uint32_t*>(vs + c * 4 * (D / G::BLK) + (16 * l + n) * 2 * G::VB / G::BLK * 4);
   }
 }
 
@@ -299,7 +301,7 @@ struct Cursor {
   __device__ __forceinline__ void load(const KvAttn& A, int s0, int b) {
     const int lane = threadIdx.x & 63;
     const Span x = span_of(A, s0 + lane, unit_rows);
-    const int n = b + wave_prefix(x.tiles * x.steps * A.c.heads);
+    const int n = b + wave_prefix(x.rows > A.few && A.split ? 0 : x.tiles * x.steps * A.c.heads);
     seq0 = s0;
     before = b;
     end = __builtin_amdgcn_readlane(n, 63);
@@ -422,7 +424,8 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
     auto load = [&](int key, const Pages& g, Tile<FMT, D>& T) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        load_half<FMT, D>(A.c, kv_slot(A.c, mapped(g, h) ? g.p[h] : 0, head, (key + 16 * h) & ((1 << A.c.shift) - 1)), h, T);
+        load_half<FMT, D>(A.c, kv_slot(A.c, mapped(g, h) ? g.p[h] : 0, head, (key + 16 * h) & ((1 << A.c.shift) - 1)), T.k[h],
+                          T.ks[h], T.v[h], T.vs[h]);
     };
     auto use = [&](int key, const Pages& g, Tile<FMT, D>& T) {
       // scores: s[i][h][j] is key 16 h + 4 c + j for row n of tile i
@@ -668,6 +671,222 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn A, bool nv) {
   if (A.lse && d == 0) store_lse(A, t, qh, M, L);
 }
 
+// Many rows a sequence: a workgroup has a unit of 64 NR rows, a wave 16 NR of
+// them, and all keys of the unit. The waves decode 16 of 64 keys each into LDS, in
+// the order of the products' operands, for all of them: a quarter of the decoding
+// a wave, and one barrier for 64 keys, with two buffers.
+template <int FMT, int D>
+struct Half {                  // what a lane holds of 16 tokens
+  using G = Geo<FMT, D>;
+  uint32_t k[G::KL][G::KD], ks[G::KL];
+  uint32_t v[G::VL][G::VB], vs[G::VL];
+};
+
+constexpr int prompt_tiles(int dim) { return dim == 64 ? 4 : dim == 128 ? 2 : 1; }   // NR
+
+template <int FMT, int D, int NR>
+__global__ __launch_bounds__(64 * kWaves, 2) void kv_prompt_kernel(KvAttn A) {
+  using G = Geo<FMT, D>;
+  constexpr int kUnit = kRows * NR * kWaves, kKeys = 16 * kWaves, KC = G::KL * G::KD;
+  __shared__ u32x4_t keys[2][kWaves][KC][64];          // [half of 16 keys][32 dimensions][lane]
+  __shared__ u32x2_t vals[2][kWaves / 2][G::DT][64][2];   // [32 keys][tile of 16 dimensions][lane][half]
+  const int lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // heads first: a head's units meet in one XCD's cache; of a sequence's units those with the most keys first
+  const int head = blockIdx.x % A.c.heads, place = blockIdx.x / A.c.heads;
+  auto start = [&](int i) { return (int64_t)A.b.cu[i] * A.group / kUnit + i; };
+  const int seq = A.b.cu ? kv_find(A.b.seqs, place, start) : place / ((A.group + kUnit - 1) / kUnit);
+  if (seq < 0 || seq >= A.b.seqs) return;
+  const Span U = span_of(A, seq, kUnit);
+  const int64_t base = A.b.cu ? (int64_t)entries(A.b.cu)[seq] * A.group / kUnit + seq : (int64_t)seq * U.tiles;
+  const int64_t tile = U.tiles - 1 - (place - base);
+  if (tile < 0 || tile >= U.tiles || U.rows <= A.few) return;
+  const int ek = G::NV ? entries(A.c.texp)[0] : 0, ev = G::NV ? entries(A.c.texp)[1] : 0;
+  const int r0 = (int)tile * kUnit, w0 = r0 + wave * kRows * NR;
+  const int rows = U.rows - r0 < kUnit ? U.rows - r0 : kUnit, wrows = U.rows - w0;
+  Rows<FMT, D> R[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int r = w0 + kRows * i + n, tok = r / A.group;
+    const bool mine = kRows * i + n < wrows;
+    R[i].start(mine ? A.q + (U.row0 + tok) * A.ldq + (int64_t)(head * A.group + r % A.group) * D : nullptr, A.scale, ek);
+    R[i].factor = fmaxf(R[i].factor, 1.0e-37f);        // times -inf is -inf
+    R[i].last = mine ? limit(A, U.pos0 + tok) : -1;
+    R[i].first = first_key(A, U.pos0 + tok);
+  }
+  // keys of any row of the unit; of any and of all rows of the wave
+  const int first = first_key(A, U.pos0 + r0 / A.group), last = limit(A, U.pos0 + (r0 + rows - 1) / A.group);
+  const int wlast = wrows > 0 ? limit(A, U.pos0 + (w0 + (wrows < kRows * NR ? wrows : kRows * NR) - 1) / A.group) : -1;
+  const int wfirst = first_key(A, U.pos0 + w0 / A.group);
+  const int every_first = first_key(A, U.pos0 + (w0 + kRows * NR - 1) / A.group), every_last = limit(A, U.pos0 + w0 / A.group);
+  const Entries table = entries(A.b.table + (int64_t)seq * A.b.table_ld);
+
+  struct Pages {
+    int p[kWaves];
+  };
+  auto pages = [&](int key) {
+    Pages g;
+#pragma unroll
+    for (int h = 0; h < kWaves; ++h) g.p[h] = table[(key + 16 * h < last ? key + 16 * h : last) >> A.c.shift];
+    return g;
+  };
+  auto mapped = [&](int p) { return (uint32_t)p < (uint32_t)A.c.pages; };
+  auto load = [&](int key, Half<FMT, D>& T) {          // the wave's 16 of the 64 keys
+    const int k = key + 16 * wave;
+    const int p = table[(k < last ? k : last) >> A.c.shift];
+    load_half<FMT, D>(A.c, kv_slot(A.c, mapped(p) ? p : 0, head, k & ((1 << A.c.shift) - 1)), T.k, T.ks, T.v, T.vs);
+  };
+  auto decode = [&](int key, int buf, Half<FMT, D>& T) {
+    const int k0 = key + 16 * wave;
+    if (k0 < first || k0 + 15 > last || !mapped(table[(k0 < last ? k0 : last) >> A.c.shift])) {
+      // values of places that no row sees may be anything: their scales are replaced
+      const int end = mapped(table[(k0 < last ? k0 : last) >> A.c.shift]) ? last : -1;
+      uint32_t keep = 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) keep |= ((k0 + 4 * c + j >= first) & (k0 + 4 * c + j <= end)) ? 0xFFu << (8 * j) : 0u;
+#pragma unroll
+      for (int l = 0; l < G::VL; ++l) T.vs[l] &= keep;
+    }
+#pragma unroll
+    for (int l = 0; l < G::KL; ++l) {
+      h2_t sc = {};
+      float e = 0.0f;
+      if constexpr (G::NV)
+        sc = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(T.ks[l], 1.0f, false);
+      else
+        e = e8m0_val(T.ks[l]);
+#pragma unroll
+      for (int w = 0; w < G::KD; ++w) {
+        const int b = G::SB == 2 ? w / 2 : 0;
+        keys[buf][wave][l * G::KD + w][lane] = decode_key<FMT>(T.k[l][w], h2_t{sc[b], sc[b]}, e);
+      }
+    }
+#pragma unroll
+    for (int l = 0; l < G::VL; ++l) {
+      uint32_t v[2 * G::VB][2];
+      decode_values<FMT, D>(T.v[l], T.vs[l], v);
+#pragma unroll
+      for (int d = 0; d < 2 * G::VB; ++d) vals[buf][wave / 2][l * 2 * G::VB + d][lane][wave % 2] = u32x2_t{v[d][0], v[d][1]};
+    }
+  };
+  auto use = [&](int key, int buf, const Pages& g) {
+    f4_t s[NR][kWaves];
+#pragma unroll
+    for (int h = 0; h < kWaves; ++h) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i) s[i][h] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < KC; ++w) {
+        const u32x4_t k = keys[buf][h][w][lane];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) s[i][h] = mfma<FMT>(k, R[i].q[w / G::KD][w % G::KD], s[i][h]);
+      }
+    }
+    const bool whole = mapped(g.p[0]) & mapped(g.p[1]) & mapped(g.p[2]) & mapped(g.p[3]) & (key >= every_first) &
+                       (key + kKeys - 1 <= every_last);
+    if (!whole) {
+#pragma unroll
+      for (int h = 0; h < kWaves; ++h) {
+        const int k0 = key + 16 * h + 4 * c, end = mapped(g.p[h]) ? last : -1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < NR; ++i)
+            s[i][h][j] = ((k0 + j >= R[i].first) & (k0 + j <= R[i].last) & (k0 + j <= end)) ? s[i][h][j] : -__builtin_inff();
+      }
+    }
+    float top[NR];
+    bool above = false;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      top[i] = kLowest;
+#pragma unroll
+      for (int h = 0; h < kWaves; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top[i] = fmaxf(top[i], s[i][h][j]);
+      top[i] *= R[i].factor;
+      above |= top[i] > R[i].m + 8.0f;
+    }
+    if (__any(above)) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        const float m = fmaxf(row_max(top[i]), R[i].m), f = __builtin_amdgcn_exp2f(R[i].m - m);
+        R[i].m = m;
+        R[i].l *= f;
+#pragma unroll
+        for (int d = 0; d < G::DT; ++d) R[i].o[d] *= f;
+      }
+    }
+#pragma unroll
+    for (int pr = 0; pr < kWaves / 2; ++pr) {
+      u32x4_t ph[NR], pl[NR];                          // fp16, or the two parts in bf16
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        float p[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][2 * pr + j / 4][j % 4], R[i].factor, -R[i].m));
+          R[i].l += p[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (G::NV) {
+            ph[i][j] = bits(h2_t{(_Float16)p[2 * j], (_Float16)p[2 * j + 1]});
+          } else {
+            ph[i][j] = pack_bf16(p[2 * j], p[2 * j + 1]);
+            pl[i][j] = pack_bf16(p[2 * j] - bf16_lo(ph[i][j]), p[2 * j + 1] - bf16_hi(ph[i][j]));
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < G::DT; ++d) {
+        const u32x4_t a = *reinterpret_cast<const u32x4_t*>(vals[buf][pr][d][lane]);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          R[i].o[d] = mfma<FMT>(a, ph[i], R[i].o[d]);
+          if constexpr (!G::NV) R[i].o[d] = mfma<FMT>(a, pl[i], R[i].o[d]);
+        }
+      }
+    }
+  };
+
+  int key = first & ~15;
+  if (key <= last) {
+    Half<FMT, D> T;
+    load(key, T);
+    decode(key, 0, T);
+    load(key + kKeys, T);
+    __syncthreads();
+    for (int buf = 0; key <= last; key += kKeys, buf ^= 1) {
+      const Pages g = pages(key);
+      if (key + kKeys <= last) {
+        decode(key + kKeys, buf ^ 1, T);
+        load(key + 2 * kKeys, T);
+      }
+      if (key <= wlast && key + kKeys > wfirst) use(key, buf, g);
+      __syncthreads();
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const float L = row_sum(R[i].l), inv = L == 0.0f ? 0.0f : ldexpf(1.0f / L, ev);
+    if (kRows * i + n >= wrows) continue;
+    const int r = w0 + kRows * i + n;
+    const int64_t t = U.row0 + r / A.group;
+    const int qh = head * A.group + r % A.group;
+#pragma unroll
+    for (int l = 0; l < G::VL; ++l)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float x[2 * G::VB];
+#pragma unroll
+        for (int d = 0; d < 2 * G::VB; ++d) x[d] = R[i].o[l * 2 * G::VB + d][j] * inv;
+        store_whole(A.out, false, t * A.ldo + (int64_t)qh * D + l * 32 * G::VB + (4 * c + j) * 2 * G::VB, x);
+      }
+    if (A.lse && c == 0) store_lse(A, t, qh, R[i].m, L);
+  }
+}
+
 }  // namespace
 
 int64_t kv_attn_tiles(int64_t tokens, int64_t seqs, int64_t group) { return tokens * group / kRows + seqs; }
@@ -686,9 +905,20 @@ hipError_t launch_kv_attn(int format, int dim, KvAttn a, hipStream_t s) {
   const double tiles = (double)kv_attn_tiles(a.tokens, a.b.seqs, a.group) * a.c.heads;
   a.step = 32 * kWaves;
   while (a.step < a.b.max_len && tiles * ((double)a.b.max_len / a.step + 1.0) >= 2147483647.0) a.step *= 2;
-  const bool two = dim != 256 && a.tokens * a.group > kRows * (int64_t)a.b.seqs;   // rows of a sequence, on average
+  const int64_t rows = a.tokens * a.group / a.b.seqs;    // of a sequence, on average
+  const bool two = dim != 256 && rows > kRows;
+  const int unit = kRows * kWaves * prompt_tiles(dim);
+  const int64_t places = a.b.cu ? a.tokens * a.group / unit + a.b.seqs : (int64_t)a.b.seqs * ((a.group + unit - 1) / unit);
+  const bool prompt = rows >= 64 && a.tokens * a.group / unit * a.c.heads >= 256 && places * a.c.heads < (1 << 24);
+  a.split = prompt && a.b.seqs > 1;
+  a.few = a.split ? 64 : 0;
   auto go = [&](auto f, auto d, auto t) {
     constexpr int D = decltype(d)::value, NR = decltype(t)::value, W = workers_of(D, NR);
+    if (prompt) {
+      kv_prompt_kernel<decltype(f)::value, D, prompt_tiles(D)><<<(unsigned)(places * a.c.heads), 64 * kWaves, 0, s>>>(a);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess || !a.split) return e;
+    }
     a.left = reinterpret_cast<Left*>(a.part + (size_t)W * 2 * slot_floats(D, kRows * NR));
     kv_attn_kernel<decltype(f)::value, D, NR><<<W, 64 * kWaves, 0, s>>>(a);
     const hipError_t e = hipGetLastError();

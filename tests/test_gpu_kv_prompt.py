@@ -1,0 +1,76 @@
+"""snipkv_attn with as many rows as its launch for prompts takes (64 row tiles
+or more a kv head's sequences), against float64 as in test_gpu_kv_attn.py."""
+import pytest
+import torch
+
+import sub_byte_mixed_amd as S
+from kv_common import Paged
+from ops_common import BF, Guarded, rand, say, strided
+
+pytestmark = pytest.mark.gpu
+FORMATS = [S.NVFP4, S.MXFP4]
+UNIT = {64: 256, 128: 128, 256: 64}                    # rows of a workgroup
+
+
+def heads_for(dim, rows):
+    """kv heads that give the call the 256 units that the launch is for."""
+    return -(-256 // (rows // UNIT[dim]))
+
+
+def run(P, group, window=0, seed=0):
+    q = rand((P.rows, P.heads * group * P.dim), BF, seed, 0.5)
+    out, lse = S.kv_attn(q.cuda(), P.cache, P.batch, window=window, with_lse=True)
+    P.check(q, out, lse, None, window)
+    again, _ = S.kv_attn(q.cuda(), P.cache, P.batch, window=window)
+    assert torch.equal(again, out)
+    return q, out, lse
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 5, 8])
+def test_one_prompt(fmt, dim, group):
+    new = {1: 2100, 5: 333, 8: 257}[group]
+    heads = heads_for(dim, new * group)
+    say("prompt", fmt, dim, group, heads)
+    run(Paged(fmt, dim, heads, 16, [new + 37], [new], seed=dim + group), group)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("window", [0, 1, 63, 64, 200])
+def test_several_sequences(fmt, window):
+    """Prompts, chunks after others, drafted and single tokens, none: the launch for prompts and that for few rows."""
+    lens, new = [700, 40, 250, 333, 9, 1, 90, 1000], [400, 40, 250, 4, 0, 1, 65, 33]
+    heads = heads_for(64, sum(new) * 4)
+    say("prompts", fmt, window, heads)
+    run(Paged(fmt, 64, heads, 32, lens, new, seed=window), 4, window=window)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_pages_that_are_not_mapped(fmt, dim):
+    new = 600
+    P = Paged(fmt, dim, heads_for(dim, new * 2), 16, [650], [new], seed=dim, unmapped=[(0, 0), (0, 5), (0, 6), (0, 20), (0, 40)])
+    say("prompt, unmapped", fmt, dim)
+    run(P, 2)
+    run(P, 2, window=30)
+
+
+def test_rows_of_nobody_and_negative_positions():
+    P = Paged(S.NVFP4, 128, heads_for(128, 700 * 2), 16, [500, 100], [600, 100], seed=1)
+    q = rand((P.rows + 70, P.heads * 2 * 128), BF, 1)
+    out = Guarded(P.rows + 70, P.heads * 256, BF)
+    lse = torch.full((P.rows + 70, P.heads * 2), 7.0, device="cuda")
+    S.kv_attn(strided(q, 8), P.cache, P.batch, out=out.t, lse=lse)
+    P.check(q[:P.rows], out.t, lse)
+    assert out.intact() and bool((out.t[P.rows:] == 7.0).all()) and bool((lse[P.rows:] == 7.0).all())
+    assert not out.t[:100].any() and bool((lse[:100] == -float("inf")).all())
+    d = q.cuda()
+    S.kv_attn(d, P.cache, P.batch, out=d)              # in place
+    assert torch.equal(d[:P.rows], out.t[:P.rows]) and torch.equal(d[P.rows:].cpu(), q[P.rows:])
+
+
+def test_many_query_heads_of_one_token():
+    """More heads to a kv head than a workgroup has rows, without cu."""
+    P = Paged(S.NVFP4, 64, 1, 16, [100 + b for b in range(300)], [1] * 300, one_each=True)
+    run(P, 300)
