@@ -682,18 +682,27 @@ struct Half {                  // what a lane holds of 16 tokens
   uint32_t v[G::VL][G::VB], vs[G::VL];
 };
 
-constexpr int prompt_tiles(int dim) { return dim == 64 ? 4 : dim == 128 ? 2 : 1; }   // NR
+#ifndef PT64
+#define PT64 2
+#define PT256 1
+#endif
+constexpr int prompt_tiles(int dim) { return dim == 64 ? PT64 : dim == 128 ? 2 : PT256; }   // NR
+constexpr int prompt_halves(int dim) { return dim == 256 ? 2 : 4; }
 
 template <int FMT, int D, int NR>
-__global__ __launch_bounds__(64 * kWaves, 2) void kv_prompt_kernel(KvAttn A) {
+__global__ __launch_bounds__(64 * kWaves, D == 256 && NR == 2 ? 1 : 2) void kv_prompt_kernel(KvAttn A) {
   using G = Geo<FMT, D>;
-  constexpr int kUnit = kRows * NR * kWaves, kKeys = 16 * kWaves, KC = G::KL * G::KD;
-  __shared__ u32x4_t keys[2][kWaves][KC][64];          // [half of 16 keys][32 dimensions][lane]
-  __shared__ u32x2_t vals[2][kWaves / 2][G::DT][64][2];   // [32 keys][tile of 16 dimensions][lane][half]
+  constexpr int KH = prompt_halves(D);                 // halves of 16 keys at a time: a wave's both, or keys or values
+  constexpr int kUnit = kRows * NR * kWaves, kKeys = 16 * KH, KC = G::KL * G::KD;
+  __shared__ u32x4_t keys[2][KH][KC][64];              // [half of 16 keys][32 dimensions][lane]
+  __shared__ u32x2_t vals[2][KH / 2][G::DT][64][2];    // [32 keys][tile of 16 dimensions][lane][half]
   const int lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // heads first: a head's units meet in one XCD's cache; of a sequence's units those with the most keys first
-  const int head = blockIdx.x % A.c.heads, place = blockIdx.x / A.c.heads;
+  // heads first: a head's units meet in one XCD's cache; of a sequence's units those with the most keys
+  // first; every other round of the CUs goes the other way, so that a CU gets long and short ones
+  const int head = blockIdx.x % A.c.heads, round = A.c.heads < 256 ? 256 / A.c.heads : 1;
+  int place = blockIdx.x / A.c.heads;
+  if (place / round % 2 == 1 && (place / round + 1) * round * A.c.heads <= (int)gridDim.x) place = (place / round * 2 + 1) * round - 1 - place;
   auto start = [&](int i) { return (int64_t)A.b.cu[i] * A.group / kUnit + i; };
   const int seq = A.b.cu ? kv_find(A.b.seqs, place, start) : place / ((A.group + kUnit - 1) / kUnit);
   if (seq < 0 || seq >= A.b.seqs) return;
@@ -722,22 +731,24 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_prompt_kernel(KvAttn A) {
   const Entries table = entries(A.b.table + (int64_t)seq * A.b.table_ld);
 
   struct Pages {
-    int p[kWaves];
+    int p[KH];
   };
   auto pages = [&](int key) {
     Pages g;
 #pragma unroll
-    for (int h = 0; h < kWaves; ++h) g.p[h] = table[(key + 16 * h < last ? key + 16 * h : last) >> A.c.shift];
+    for (int h = 0; h < KH; ++h) g.p[h] = table[(key + 16 * h < last ? key + 16 * h : last) >> A.c.shift];
     return g;
   };
   auto mapped = [&](int p) { return (uint32_t)p < (uint32_t)A.c.pages; };
-  auto load = [&](int key, Half<FMT, D>& T) {          // the wave's 16 of the 64 keys
-    const int k = key + 16 * wave;
+  const int half = wave % KH;                          // what the wave decodes
+  const bool do_keys = KH == kWaves || wave < KH, do_values = KH == kWaves || wave >= KH;
+  auto load = [&](int key, Half<FMT, D>& T) {
+    const int k = key + 16 * half;
     const int p = table[(k < last ? k : last) >> A.c.shift];
     load_half<FMT, D>(A.c, kv_slot(A.c, mapped(p) ? p : 0, head, k & ((1 << A.c.shift) - 1)), T.k, T.ks, T.v, T.vs);
   };
   auto decode = [&](int key, int buf, Half<FMT, D>& T) {
-    const int k0 = key + 16 * wave;
+    const int k0 = key + 16 * half;
     if (k0 < first || k0 + 15 > last || !mapped(table[(k0 < last ? k0 : last) >> A.c.shift])) {
       // values of places that no row sees may be anything: their scales are replaced
       const int end = mapped(table[(k0 < last ? k0 : last) >> A.c.shift]) ? last : -1;
@@ -747,6 +758,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_prompt_kernel(KvAttn A) {
 #pragma unroll
       for (int l = 0; l < G::VL; ++l) T.vs[l] &= keep;
     }
+    if (do_keys) {
 #pragma unroll
     for (int l = 0; l < G::KL; ++l) {
       h2_t sc = {};
@@ -758,21 +770,24 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_prompt_kernel(KvAttn A) {
 #pragma unroll
       for (int w = 0; w < G::KD; ++w) {
         const int b = G::SB == 2 ? w / 2 : 0;
-        keys[buf][wave][l * G::KD + w][lane] = decode_key<FMT>(T.k[l][w], h2_t{sc[b], sc[b]}, e);
+        keys[buf][half][l * G::KD + w][lane] = decode_key<FMT>(T.k[l][w], h2_t{sc[b], sc[b]}, e);
       }
     }
+    }
+    if (do_values) {
 #pragma unroll
     for (int l = 0; l < G::VL; ++l) {
       uint32_t v[2 * G::VB][2];
       decode_values<FMT, D>(T.v[l], T.vs[l], v);
 #pragma unroll
-      for (int d = 0; d < 2 * G::VB; ++d) vals[buf][wave / 2][l * 2 * G::VB + d][lane][wave % 2] = u32x2_t{v[d][0], v[d][1]};
+      for (int d = 0; d < 2 * G::VB; ++d) vals[buf][half / 2][l * 2 * G::VB + d][lane][half % 2] = u32x2_t{v[d][0], v[d][1]};
+    }
     }
   };
   auto use = [&](int key, int buf, const Pages& g) {
-    f4_t s[NR][kWaves];
+    f4_t s[NR][KH];
 #pragma unroll
-    for (int h = 0; h < kWaves; ++h) {
+    for (int h = 0; h < KH; ++h) {
 #pragma unroll
       for (int i = 0; i < NR; ++i) s[i][h] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -782,11 +797,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_prompt_kernel(KvAttn A) {
         for (int i = 0; i < NR; ++i) s[i][h] = mfma<FMT>(k, R[i].q[w / G::KD][w % G::KD], s[i][h]);
       }
     }
-    const bool whole = mapped(g.p[0]) & mapped(g.p[1]) & mapped(g.p[2]) & mapped(g.p[3]) & (key >= every_first) &
-                       (key + kKeys - 1 <= every_last);
+    bool whole = (key >= every_first) & (key + kKeys - 1 <= every_last);
+#pragma unroll
+    for (int h = 0; h < KH; ++h) whole &= mapped(g.p[h]);
     if (!whole) {
 #pragma unroll
-      for (int h = 0; h < kWaves; ++h) {
+      for (int h = 0; h < KH; ++h) {
         const int k0 = key + 16 * h + 4 * c, end = mapped(g.p[h]) ? last : -1;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -801,7 +817,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_prompt_kernel(KvAttn A) {
     for (int i = 0; i < NR; ++i) {
       top[i] = kLowest;
 #pragma unroll
-      for (int h = 0; h < kWaves; ++h)
+      for (int h = 0; h < KH; ++h)
 #pragma unroll
         for (int j = 0; j < 4; ++j) top[i] = fmaxf(top[i], s[i][h][j]);
       top[i] *= R[i].factor;
@@ -818,7 +834,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void kv_prompt_kernel(KvAttn A) {
       }
     }
 #pragma unroll
-    for (int pr = 0; pr < kWaves / 2; ++pr) {
+    for (int pr = 0; pr < KH / 2; ++pr) {
       u32x4_t ph[NR], pl[NR];                          // fp16, or the two parts in bf16
 #pragma unroll
       for (int i = 0; i < NR; ++i) {
