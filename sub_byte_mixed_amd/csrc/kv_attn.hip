@@ -682,15 +682,11 @@ struct Half {                  // what a lane holds of 16 tokens
   uint32_t v[G::VL][G::VB], vs[G::VL];
 };
 
-#ifndef PT64
-#define PT64 2
-#define PT256 1
-#endif
-constexpr int prompt_tiles(int dim) { return dim == 64 ? PT64 : dim == 128 ? 2 : PT256; }   // NR
+constexpr int prompt_tiles(int dim) { return dim == 256 ? 1 : 2; }      // NR
 constexpr int prompt_halves(int dim) { return dim == 256 ? 2 : 4; }
 
 template <int FMT, int D, int NR>
-__global__ __launch_bounds__(64 * kWaves, D == 256 && NR == 2 ? 1 : 2) void kv_prompt_kernel(KvAttn A) {
+__global__ __launch_bounds__(64 * kWaves, D == 64 ? 3 : 2) void kv_prompt_kernel(KvAttn A) {
   using G = Geo<FMT, D>;
   constexpr int KH = prompt_halves(D);                 // halves of 16 keys at a time: a wave's both, or keys or values
   constexpr int kUnit = kRows * NR * kWaves, kKeys = 16 * KH, KC = G::KL * G::KD;
@@ -742,17 +738,15 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 && NR == 2 ? 1 : 2) void kv_p
   auto mapped = [&](int p) { return (uint32_t)p < (uint32_t)A.c.pages; };
   const int half = wave % KH;                          // what the wave decodes
   const bool do_keys = KH == kWaves || wave < KH, do_values = KH == kWaves || wave >= KH;
-  auto load = [&](int key, Half<FMT, D>& T) {
-    const int k = key + 16 * half;
-    const int p = table[(k < last ? k : last) >> A.c.shift];
-    load_half<FMT, D>(A.c, kv_slot(A.c, mapped(p) ? p : 0, head, k & ((1 << A.c.shift) - 1)), T.k, T.ks, T.v, T.vs);
+  auto entry = [&](int key) { return table[(key + 16 * half < last ? key + 16 * half : last) >> A.c.shift]; };
+  auto load = [&](int key, int p, Half<FMT, D>& T) {
+    load_half<FMT, D>(A.c, kv_slot(A.c, mapped(p) ? p : 0, head, (key + 16 * half) & ((1 << A.c.shift) - 1)), T.k, T.ks, T.v, T.vs);
   };
-  auto decode = [&](int key, int buf, Half<FMT, D>& T) {
-    const int k0 = key + 16 * half;
-    if (k0 < first || k0 + 15 > last || !mapped(table[(k0 < last ? k0 : last) >> A.c.shift])) {
+  auto decode = [&](int key, int buf, int p, Half<FMT, D>& T) {
+    const int k0 = key + 16 * half, end = mapped(p) ? last : -1;
+    if (k0 < first || k0 + 15 > end) {
       // values of places that no row sees may be anything: their scales are replaced
-      const int end = mapped(table[(k0 < last ? k0 : last) >> A.c.shift]) ? last : -1;
-      uint32_t keep = 0u;
+    uint32_t keep = 0u;
 #pragma unroll
       for (int j = 0; j < 4; ++j) keep |= ((k0 + 4 * c + j >= first) & (k0 + 4 * c + j <= end)) ? 0xFFu << (8 * j) : 0u;
 #pragma unroll
@@ -866,21 +860,35 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 && NR == 2 ? 1 : 2) void kv_p
     }
   };
 
+  // Codes are loaded two tiles ahead of their decoding, and decoded one ahead of
+  // their use, whether or not there are keys left (see kv_attn_kernel). The
+  // table's entries are asked for before a barrier, which waits for them.
   int key = first & ~15;
   if (key <= last) {
-    Half<FMT, D> T;
-    load(key, T);
-    decode(key, 0, T);
-    load(key + kKeys, T);
+    Half<FMT, D> T0, T1;
+    int e0 = entry(key), e1 = entry(key + kKeys), e2 = entry(key + 2 * kKeys), e3 = entry(key + 3 * kKeys);
+    Pages g = pages(key);
+    load(key, e0, T0);
+    load(key + kKeys, e1, T1);
+    decode(key, 0, e0, T0);
+    load(key + 2 * kKeys, e2, T0);
     __syncthreads();
-    for (int buf = 0; key <= last; key += kKeys, buf ^= 1) {
-      const Pages g = pages(key);
-      if (key + kKeys <= last) {
-        decode(key + kKeys, buf ^ 1, T);
-        load(key + 2 * kKeys, T);
-      }
+    auto tile = [&](int buf, Half<FMT, D>& T) {
+      decode(key + kKeys, buf ^ 1, e1, T);
+      load(key + 3 * kKeys, e3, T);
       if (key <= wlast && key + kKeys > wfirst) use(key, buf, g);
+      key += kKeys;
+      e1 = e2;
+      e2 = e3;
+      e3 = entry(key + 3 * kKeys);
+      g = pages(key);
       __syncthreads();
+    };
+    while (true) {
+      tile(0, T1);
+      if (key > last) break;
+      tile(1, T0);
+      if (key > last) break;
     }
   }
 #pragma unroll
