@@ -16,6 +16,7 @@ Every call takes stream= (default: the current one of the tensors' device).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional, Tuple
 
@@ -23,7 +24,7 @@ import torch
 
 import sub_byte_mixed_amd as _S
 from . import ops as _ops
-from .ops import _ABSENT, _TYPES, _elsewhere, _mat, _scratch, _vec
+from .ops import _TYPES, _elsewhere, _scratch, _vec
 
 _c = ctypes
 _vp, _i, _l, _f, _sz = _c.c_void_p, _c.c_int, _c.c_int64, _c.c_float, _c.c_size_t
@@ -52,6 +53,10 @@ MAX_PAGE_SIZE = 4096           # SNIPKV_MAX_PAGE_SIZE
 HEAD_DIMS = (64, 128, 256)
 
 
+_U8, _I32, _BF, _F32 = torch.uint8, torch.int32, torch.bfloat16, torch.float32
+
+
+@functools.lru_cache(maxsize=256)
 def cache_shapes(fmt: int, pages: int, page_size: int, kv_heads: int, head_dim: int) -> Tuple[tuple, ...]:
     """Shapes of k_codes, k_scales, v_codes and v_scales."""
     if fmt not in (_S.NVFP4, _S.MXFP4):
@@ -68,6 +73,12 @@ def cache_shapes(fmt: int, pages: int, page_size: int, kv_heads: int, head_dim: 
             (pages, kv_heads, page_size // 4, head_dim // block, 4))
 
 
+def _buffer(t: torch.Tensor, name: str, shape: tuple, dev: int) -> None:
+    if t.dtype is not _U8 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {shape} on GPU {dev}, got {t.dtype}, "
+                         f"{tuple(t.shape)} on {t.device}")
+
+
 class KVCache:
     """Caller-owned buffers of a paged cache, uint8 in the shapes of
     cache_shapes(); texp (NVFP4): int32 [2], the powers of two that keys and
@@ -79,19 +90,18 @@ class KVCache:
         if k_codes.dim() != 6:
             raise ValueError("k_codes must have the six dimensions of cache_shapes()")
         pages, heads, groups, pieces, _, p = k_codes.shape
-        self.format, self.pages, self.kv_heads = fmt, pages, heads
-        self.page_size, self.head_dim = 16 * groups, 2 * pieces * p
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.texp = k_codes, k_scales, v_codes, v_scales, texp
-        self.device = dev = k_codes.get_device()
-        for name, t, shape in zip(("k_codes", "k_scales", "v_codes", "v_scales"), (k_codes, k_scales, v_codes, v_scales),
-                                  cache_shapes(fmt, pages, self.page_size, heads, self.head_dim)):
-            if t.dtype != torch.uint8 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {shape} on {k_codes.device}, got "
-                                 f"{t.dtype}, {tuple(t.shape)} on {t.device}")
-        if fmt == _S.NVFP4 and texp is None:
+        page, dim, dev = 16 * groups, 2 * pieces * p, k_codes.get_device()
+        sk, ssk, sv, ssv = cache_shapes(fmt, pages, page, heads, dim)
+        _buffer(k_codes, "k_codes", sk, dev)
+        _buffer(k_scales, "k_scales", ssk, dev)
+        _buffer(v_codes, "v_codes", sv, dev)
+        _buffer(v_scales, "v_scales", ssv, dev)
+        if texp is None and fmt == _S.NVFP4:
             raise ValueError("an NVFP4 cache needs texp")
-        self._desc = CacheDesc(fmt, self.page_size, heads, self.head_dim, pages, k_codes.data_ptr(), k_scales.data_ptr(),
-                               v_codes.data_ptr(), v_scales.data_ptr(), _vec(texp, "texp", 2, (torch.int32,), dev))
+        self.format, self.pages, self.kv_heads, self.page_size, self.head_dim, self.device = fmt, pages, heads, page, dim, dev
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.texp = k_codes, k_scales, v_codes, v_scales, texp
+        self._desc = CacheDesc(fmt, page, heads, dim, pages, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                               v_scales.data_ptr(), _vec(texp, "texp", 2, (_I32,), dev))
         self.ref = ctypes.byref(self._desc)
 
     @classmethod
@@ -111,14 +121,15 @@ class KVBatch:
     follows what its buffers hold."""
 
     def __init__(self, table: torch.Tensor, lens: torch.Tensor, cu: Optional[torch.Tensor] = None):
-        self.table, self.lens, self.cu = table, lens, cu
-        self.device = dev = table.get_device()
-        if table.dtype != torch.int32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
-            raise ValueError(f"table must be a 2-D int32 tensor with unit column stride, got {table.dtype}, {tuple(table.shape)}")
-        self.seqs = n = table.shape[0]
-        i32 = (torch.int32,)
-        self._desc = BatchDesc(table.data_ptr(), table.stride(0) if n > 1 else table.shape[1], table.shape[1],
-                               _vec(lens, "lens", n, i32, dev), _vec(cu, "cu", n + 1, i32, dev), n)
+        dev = table.get_device()
+        if table.dtype is not _I32 or table.dim() != 2:
+            raise ValueError(f"table must be a 2-D int32 tensor, got {table.dtype}, {tuple(table.shape)}")
+        (n, wide), (ld, unit) = table.shape, table.stride()
+        if unit != 1 and wide > 1:
+            raise ValueError("table must have unit column stride")
+        self.table, self.lens, self.cu, self.seqs, self.device = table, lens, cu, n, dev
+        self._desc = BatchDesc(table.data_ptr(), ld if n > 1 else wide, wide, _vec(lens, "lens", n, (_I32,), dev),
+                               _vec(cu, "cu", n + 1, (_I32,), dev), n)
         self.ref = ctypes.byref(self._desc)
 
 
@@ -130,11 +141,23 @@ def _place(cache: KVCache, batch: KVBatch, fn) -> int:
     return dev
 
 
-def _rows(t: torch.Tensor, name: str, dev: int, head_dim: int) -> Tuple[int, int]:
-    """(tokens, heads) of a matrix of heads."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.get_device() != dev or t.shape[1] % head_dim:
-        raise ValueError(f"{name} must be a 2-D tensor of heads of {head_dim} on GPU {dev}")
-    return t.shape[0], t.shape[1] // head_dim
+def _heads(t: torch.Tensor, name: str, dev: int, dim: int, dtype) -> Tuple[int, int, int, int]:
+    """(address, leading dimension, tokens, heads) of a matrix of heads."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be a 2-D {dtype} tensor on GPU {dev}, got "
+                         f"{(t.dtype, tuple(t.shape), t.device) if isinstance(t, torch.Tensor) else type(t)}")
+    (rows, cols), (ld, unit) = t.shape, t.stride()
+    if cols % dim or cols == 0:
+        raise ValueError(f"{name} must have columns of heads of {dim}, got {cols}")
+    if unit != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr(), ld if rows > 1 else cols, rows, cols // dim      # one row: its stride says nothing
+
+
+def _same(got: Tuple[int, int, int, int], name: str, tokens: int, heads: int) -> Tuple[int, int]:
+    if got[2] != tokens or got[3] != heads:
+        raise ValueError(f"{name} must have {tokens} rows of {heads} heads, got {got[2]} of {got[3]}")
+    return got[:2]
 
 
 def kv_append(k: Optional[torch.Tensor], v: Optional[torch.Tensor], cache: KVCache, batch: KVBatch,
@@ -145,43 +168,48 @@ def kv_append(k: Optional[torch.Tensor], v: Optional[torch.Tensor], cache: KVCac
     (cos, sin: float32 [positions, rot_dim / 2]; rot_dim a multiple of 64, the
     rest of a head stays as it is; None: no rotation) and writes k and v into
     the cache. q, k and v have one type, bfloat16 or float32 (the parts of one
-    product's columns, for instance). pos: int32 row of the angles for each
-    token, instead of its position. Returns q rotated, in bfloat16 (None
-    without q); q_out may be q itself."""
+    product's columns, for instance); k and v may be None: queries alone. pos:
+    int32 row of the angles for each token, instead of its position. Returns q
+    rotated, in bfloat16 (None without q); q_out may be q itself."""
     dev = _place(cache, batch, kv_append)
     if stream is not None or dev != _ops._current_device():
         return _elsewhere(kv_append, dev, stream, k, v, cache, batch, q, cos, sin, interleaved, pos, q_out)
-    first = k if k is not None else q
+    dim, hk = cache.head_dim, cache.kv_heads
+    first = q if k is None else k
     if first is None or (k is None) != (v is None):
         raise ValueError("k and v are given together, or q alone")
-    hk, dim = cache.kv_heads * cache.head_dim, cache.head_dim
-    tokens, _ = _rows(first, "k" if k is not None else "q", dev, dim)
-    if any(t is not None and t.dtype != first.dtype for t in (q, v)) or first.dtype not in _TYPES:
-        raise ValueError("q, k and v must have the same type, bfloat16 or float32")
-    pk, _, lk = _mat(k, "k", tokens, hk, dev)
-    pv, _, lv = _mat(v, "v", tokens, hk, dev)
-    (pq, _, lq), (po, _, lo), heads = _ABSENT, _ABSENT, 0
+    dtype = first.dtype
+    ty = _TYPES.get(dtype)
+    if ty is None:
+        raise ValueError(f"q, k and v must be bfloat16 or float32, got {dtype}")
+    pk = lk = pv = lv = pq = lq = po = lo = pc = ps = pp = None
+    angles = half = heads = 0
+    if k is not None:
+        got = _heads(k, "k", dev, dim, dtype)
+        tokens = got[2]
+        pk, lk = _same(got, "k", tokens, hk)
+        pv, lv = _same(_heads(v, "v", dev, dim, dtype), "v", tokens, hk)
     if q is not None:
-        _, heads = _rows(q, "q", dev, dim)
-        pq, _, lq = _mat(q, "q", tokens, heads * dim, dev)
+        pq, lq, rows, heads = _heads(q, "q", dev, dim, dtype)
+        if k is None:
+            tokens = rows
+        elif rows != tokens:
+            raise ValueError(f"q must have {tokens} rows, got {rows}")
         if q_out is None:
-            q_out = torch.empty((tokens, heads * dim), dtype=torch.bfloat16, device=dev)
-        elif q_out.dtype != torch.bfloat16:
-            raise ValueError("q_out must be bfloat16")
-        po, _, lo = _mat(q_out, "q_out", tokens, heads * dim, dev)
+            q_out = q.new_empty((tokens, heads * dim), dtype=_BF)
+        po, lo = _same(_heads(q_out, "q_out", dev, dim, _BF), "q_out", tokens, heads)
     elif q_out is not None:
         raise ValueError("q_out belongs to q")
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin are given together")
-    angles, half, pc, ps = 0, 0, None, None
-    if cos is not None:
-        if cos.dim() != 2 or cos.shape != sin.shape or any(
-                t.dtype != torch.float32 or t.get_device() != dev or not t.is_contiguous() for t in (cos, sin)):
+    if cos is not None or sin is not None:
+        if (cos is None or sin is None or cos.dim() != 2 or cos.shape != sin.shape or cos.dtype is not _F32
+                or sin.dtype is not _F32 or cos.get_device() != dev or sin.get_device() != dev or not cos.is_contiguous()
+                or not sin.is_contiguous()):
             raise ValueError(f"cos and sin must be contiguous float32 tensors of one shape [positions, rot_dim / 2] on GPU {dev}")
         (angles, half), pc, ps = cos.shape, cos.data_ptr(), sin.data_ptr()
-    pp = _vec(pos, "pos", tokens, (torch.int32,), dev)
-    _S._check(_S.lib().snipkv_append(pq, lq, heads, pk, lk, pv, lv, _TYPES[first.dtype], tokens, pc, ps, angles, 2 * half,
-                                     int(interleaved), pp, cache.ref, batch.ref, po, lo, _ops._current_stream(dev)))
+    if pos is not None:
+        pp = _vec(pos, "pos", tokens, (_I32,), dev)
+    _S._check(_S.lib().snipkv_append(pq, lq or 0, heads, pk, lk or 0, pv, lv or 0, ty, tokens, pc, ps, angles, 2 * half,
+                                     interleaved, pp, cache.ref, batch.ref, po, lo or 0, _ops._current_stream(dev)))
     return q_out
 
 
@@ -194,19 +222,22 @@ def kv_gather(cache: KVCache, batch: KVBatch, tokens: Optional[int] = None, k: O
     dev = _place(cache, batch, kv_gather)
     if stream is not None or dev != _ops._current_device():
         return _elsewhere(kv_gather, dev, stream, cache, batch, tokens, k, v)
-    cols = cache.kv_heads * cache.head_dim
+    dim, hk = cache.head_dim, cache.kv_heads
     if tokens is None:
         tokens = k.shape[0] if k is not None else v.shape[0] if v is not None else batch.seqs
     if k is None:
-        k = torch.empty((tokens, cols), dtype=torch.bfloat16, device=dev)
+        k = cache.k_codes.new_empty((tokens, hk * dim), dtype=_BF)
     if v is None:
-        v = torch.empty((tokens, cols), dtype=torch.bfloat16, device=dev)
-    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
-        raise ValueError("k and v must be bfloat16")
-    pk, _, lk = _mat(k, "k", tokens, cols, dev)
-    pv, _, lv = _mat(v, "v", tokens, cols, dev)
+        v = cache.k_codes.new_empty((tokens, hk * dim), dtype=_BF)
+    pk, lk = _same(_heads(k, "k", dev, dim, _BF), "k", tokens, hk)
+    pv, lv = _same(_heads(v, "v", dev, dim, _BF), "v", tokens, hk)
     _S._check(_S.lib().snipkv_gather(cache.ref, batch.ref, tokens, pk, lk, pv, lv, _ops._current_stream(dev)))
     return k, v
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace(tokens: int, seqs: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return _S.lib().snipkv_attn_workspace(tokens, seqs, q_heads, kv_heads, head_dim)
 
 
 def kv_attn(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: Optional[float] = None, window: int = 0,
@@ -222,21 +253,20 @@ def kv_attn(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: Optional[flo
     if stream is not None or dev != _ops._current_device():
         return _elsewhere(kv_attn, dev, stream, q, cache, batch, scale, window, out, lse, with_lse, ws)
     dim, hk = cache.head_dim, cache.kv_heads
-    tokens, heads = _rows(q, "q", dev, dim)
-    if q.dtype != torch.bfloat16 or (out is not None and out.dtype != torch.bfloat16):
-        raise ValueError("q and out must be bfloat16")
-    pq, _, lq = _mat(q, "q", tokens, heads * dim, dev)
+    pq, lq, tokens, heads = _heads(q, "q", dev, dim, _BF)
     if out is None:
-        out = torch.empty((tokens, heads * dim), dtype=torch.bfloat16, device=dev)
-    po, _, lo = _mat(out, "out", tokens, heads * dim, dev)
+        out = q.new_empty((tokens, heads * dim))
+    po, lo = _same(_heads(out, "out", dev, dim, _BF), "out", tokens, heads)
+    pl = None
     if lse is None and with_lse:
-        lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (tokens, heads) or lse.get_device() != dev
-                            or not lse.is_contiguous()):
-        raise ValueError(f"lse must be a contiguous float32 tensor of shape ({tokens}, {heads}) on GPU {dev}")
-    L = _S.lib()
+        lse = q.new_empty((tokens, heads), dtype=_F32)
+    if lse is not None:
+        if lse.dtype is not _F32 or lse.shape != (tokens, heads) or lse.get_device() != dev or not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous float32 tensor of shape ({tokens}, {heads}) on GPU {dev}")
+        pl = lse.data_ptr()
     if ws is None:
-        ws = torch.empty(L.snipkv_attn_workspace(tokens, batch.seqs, heads, hk, dim), dtype=torch.uint8, device=dev)
-    _S._check(L.snipkv_attn(pq, lq, heads, tokens, cache.ref, batch.ref, 1.0 / math.sqrt(dim) if scale is None else scale,
-                            int(window), po, lo, _S._ptr(lse), *_scratch(ws, dev), _ops._current_stream(dev)))
+        ws = q.new_empty(_workspace(tokens, batch.seqs, heads, hk, dim), dtype=_U8)
+    pw, nw = _scratch(ws, dev)
+    _S._check(_S.lib().snipkv_attn(pq, lq, heads, tokens, cache.ref, batch.ref, 1.0 / math.sqrt(dim) if scale is None else scale,
+                                   window, po, lo, pl, pw, nw, _ops._current_stream(dev)))
     return out, lse
