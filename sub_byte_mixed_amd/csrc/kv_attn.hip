@@ -199,17 +199,20 @@ struct Rows {
   float m, l;                  // l: of this lane's keys
   f4_t o[G::DT];
 
-  // qp: the row's head (or null: no row).
-  __device__ __forceinline__ void start(const uint16_t* qp, float scale, int ek) {
+  // The row's head (qp null: no row) is asked for here, and made the products'
+  // operand in start().
+  __device__ __forceinline__ void load(const uint16_t* qp) {
     const int c = (threadIdx.x & 63) >> 4;
-    float big = 0.0f;
 #pragma unroll
     for (int l_ = 0; l_ < G::KL; ++l_)
 #pragma unroll
       for (int w = 0; w < G::KD; ++w)
         q[l_][w] = qp ? *reinterpret_cast<const u32x4_t*>(qp + (c + 4 * l_) * 2 * G::PB + 8 * w) : u32x4_t{0u, 0u, 0u, 0u};
+  }
+  __device__ __forceinline__ void start(float scale, int ek) {
     factor = scale;
     if constexpr (G::NV) {
+      float big = 0.0f;
 #pragma unroll
       for (int l_ = 0; l_ < G::KL; ++l_)
 #pragma unroll
@@ -291,38 +294,56 @@ __device__ __forceinline__ int wave_prefix(int v) {
   return v;
 }
 
-// The sequences 64 at a time: the steps up to and with each of them, in the
-// wave's own LDS (a register each would cost the kernel a wave of occupancy).
+// Finds the sequence of a step. The sequences are taken in 64 groups of
+// neighbours, a group a lane, so that all loads of lens are in flight at once;
+// the steps up to and with each group, and with each of 64 sequences of the group
+// that was looked into last, lie in the wave's own LDS (registers would cost the
+// kernel a wave of occupancy).
 struct Cursor {
-  int* upto;                   // [64]
-  int unit_rows, seq0;
-  int before, end;             // steps before the 64, and with them
+  int* coarse;                 // [64]
+  int* fine;                   // [64]
+  int unit_rows, each;         // sequences of a group
+  int seq0, before, end;       // the 64 looked into last: the first, the steps before and with them
 
-  __device__ __forceinline__ void load(const KvAttn& A, int s0, int b) {
-    const int lane = threadIdx.x & 63;
-    const Span x = span_of(A, s0 + lane, unit_rows);
-    const int n = b + wave_prefix(x.rows > A.few && A.split ? 0 : x.tiles * x.steps * A.c.heads);
-    seq0 = s0;
-    before = b;
-    end = __builtin_amdgcn_readlane(n, 63);
-    upto[lane] = n;
-    __builtin_amdgcn_wave_barrier();
+  __device__ __forceinline__ int cost(const KvAttn& A, int b) const {
+    const Span x = span_of(A, b, unit_rows);
+    return A.split && x.rows > A.few ? 0 : x.tiles * x.steps * A.c.heads;
   }
-  // Steps of all sequences; leaves the cursor at the first ones.
+  // Steps of all sequences.
   __device__ __forceinline__ int total(const KvAttn& A) {
-    load(A, 0, 0);
-    if (A.b.seqs <= 64) return end;
-    for (int s = 64; s < A.b.seqs; s += 64) load(A, s, end);
-    const int n = end;
-    load(A, 0, 0);
-    return n;
+    const int lane = threadIdx.x & 63;
+    each = (A.b.seqs + 63) >> 6;
+    int n = 0;
+#pragma unroll 4
+    for (int j = 0; j < each; ++j) n += cost(A, lane * each + j);
+    n = wave_prefix(n);
+    coarse[lane] = n;
+    before = end = 0;
+    __builtin_amdgcn_wave_barrier();
+    return __builtin_amdgcn_readlane(n, 63);
   }
   // The sequence that step `at` is in, and the steps before it.
   __device__ __forceinline__ int seek(const KvAttn& A, int at, int* from) {
-    while (at >= end) load(A, seq0 + 64, end);
-    const int i = __ffsll((unsigned long long)__ballot(upto[threadIdx.x & 63] > at)) - 1;
-    *from = i ? __builtin_amdgcn_readfirstlane(upto[i - 1]) : before;
-    return seq0 + i;
+    const int lane = threadIdx.x & 63;
+    if (each > 1 && (at < before || at >= end)) {
+      const int g = __ffsll((unsigned long long)__ballot(coarse[lane] > at)) - 1;
+      before = g ? __builtin_amdgcn_readfirstlane(coarse[g - 1]) : 0;
+      for (int o = 0;; o += 64) {
+        seq0 = g * each + o;
+        const int n = before + wave_prefix(o + lane < each ? cost(A, seq0 + lane) : 0);
+        end = __builtin_amdgcn_readlane(n, 63);
+        if (at < end || o + 64 >= each) {
+          fine[lane] = n;
+          break;
+        }
+        before = end;
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    const int* upto = each > 1 ? fine : coarse;
+    const int i = __ffsll((unsigned long long)__ballot(upto[lane] > at)) - 1;
+    *from = i ? __builtin_amdgcn_readfirstlane(upto[i - 1]) : each > 1 ? before : 0;
+    return (each > 1 ? seq0 : 0) + i;
   }
 };
 
@@ -370,63 +391,107 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
   constexpr int kUnit = kRows * NR;
   __shared__ float stats[2][kWaves][kRows];
   __shared__ float part[kWaves][kRows * LD];
-  __shared__ int upto[kWaves][64];
+  __shared__ int upto[kWaves][2][64];
   const int lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ek = G::NV ? entries(A.c.texp)[0] : 0, ev = G::NV ? entries(A.c.texp)[1] : 0;
   Cursor cur;
-  cur.upto = upto[wave];
+  cur.coarse = upto[wave][0];
+  cur.fine = upto[wave][1];
   cur.unit_rows = kUnit;
   const Shares shares(cur.total(A), gridDim.x);
   int at = shares.first(blockIdx.x);
   const int stop = shares.first(blockIdx.x + 1);
-  Left left = {0, 0, 0, 0, 0};
-  while (at < stop) {
+  if (at >= stop) {
+    if (threadIdx.x == 0) A.left[blockIdx.x] = Left{0, 0, 0, 0, 0};
+    return;
+  }
+
+  // A share's part of a unit. Its queries and first keys are asked for before the
+  // one before it is joined.
+  struct Part {
+    int64_t row0, pos0;
+    int seq, head, r0, rows;
+    int begin, last;           // keys
+    bool all, goes_on;         // the whole unit; a unit that an earlier workgroup began
+    int owner;                 // of the unit's last step
+  };
+  Rows<FMT, D> R[NR];
+  Tile<FMT, D> T0, T1;
+  struct Pages {
+    int p[2];
+  };
+  Pages g0, g1;
+  auto setup = [&](Part& P) {
     int from;
-    const int seq = cur.seek(A, at, &from);
-    const Span U = span_of(A, seq, kUnit);
+    P.seq = cur.seek(A, at, &from);
+    const Span U = span_of(A, P.seq, kUnit);
     const int unit = (at - from) / U.steps, s0 = (at - from) % U.steps;
     const int s1 = stop - at < U.steps - s0 ? s0 + (stop - at) : U.steps;
     at += s1 - s0;
-    const int head = unit / U.tiles, r0 = unit % U.tiles * kUnit;
-    const int rows = U.rows - r0 < kUnit ? U.rows - r0 : kUnit;
-    Rows<FMT, D> R[NR];
+    P.row0 = U.row0;
+    P.pos0 = U.pos0;
+    P.head = unit / U.tiles;
+    P.r0 = unit % U.tiles * kUnit;
+    P.rows = U.rows - P.r0 < kUnit ? U.rows - P.r0 : kUnit;
+    const int64_t begin = (int64_t)(first_key(A, U.pos0) & ~31) + (int64_t)s0 * A.step, end = begin + (int64_t)(s1 - s0) * A.step - 1;
+    const int unit_last = limit(A, U.pos0 + (P.r0 + P.rows - 1) / A.group);
+    P.begin = (int)begin;
+    P.last = end < unit_last ? (int)end : unit_last;
+    P.all = s1 - s0 == U.steps;
+    P.goes_on = s0 > 0;
+    P.owner = P.all ? 0 : shares.owner(at - s1 + U.steps - 1);
+  };
+  // The table's entries are asked for two rounds ahead.
+  auto pages = [&](const Part& P, int key) {
+    const Entries table = entries(A.b.table + (int64_t)P.seq * A.b.table_ld);
+    Pages g;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = key + 16 * h < P.last ? key + 16 * h : P.last;
+      g.p[h] = table[(k > 0 ? k : 0) >> A.c.shift];
+    }
+    return g;
+  };
+  auto mapped = [&](const Pages& g, int h) { return (uint32_t)g.p[h] < (uint32_t)A.c.pages; };
+  // Loads are never skipped, since the wait for a tile counts those of the next
+  // one: beyond the last key, and where a page is not mapped, they read others.
+  auto load = [&](const Part& P, int key, const Pages& g, Tile<FMT, D>& T) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      load_half<FMT, D>(A.c, kv_slot(A.c, mapped(g, h) ? g.p[h] : 0, P.head, (key + 16 * h) & ((1 << A.c.shift) - 1)), T.k[h],
+                        T.ks[h], T.v[h], T.vs[h]);
+  };
+  auto issue = [&](const Part& P) {
+    const int key = P.begin + 32 * wave;
+    g0 = pages(P, key);
+    g1 = pages(P, key + kKeys);
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      const int r = r0 + kRows * i + n, tok = r / A.group;
-      const bool mine = kRows * i + n < rows;
-      R[i].start(mine ? A.q + (U.row0 + tok) * A.ldq + (int64_t)(head * A.group + r % A.group) * D : nullptr, A.scale, ek);
-      R[i].last = mine ? limit(A, U.pos0 + tok) : -1;
-      R[i].first = first_key(A, U.pos0 + tok);
+      const int r = P.r0 + kRows * i + n;
+      R[i].load(kRows * i + n < P.rows
+                    ? A.q + (P.row0 + r / A.group) * A.ldq + (int64_t)(P.head * A.group + r % A.group) * D
+                    : nullptr);
+    }
+    load(P, key, g0, T0);
+  };
+
+  Left left = {0, 0, 0, 0, 0};
+  Part P;
+  setup(P);
+  issue(P);
+  while (true) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int r = kRows * i + n;
+      const int64_t pos = P.pos0 + (P.r0 + r) / A.group;
+      R[i].start(A.scale, ek);
+      R[i].last = r < P.rows ? limit(A, pos) : -1;
+      R[i].first = first_key(A, pos);
     }
     // keys of any row of the unit, and of all
-    const int64_t p0 = U.pos0 + r0 / A.group, p1 = U.pos0 + (r0 + rows - 1) / A.group;
-    const int first = first_key(A, p0), every_first = first_key(A, p1), every_last = limit(A, p0);
-    const int64_t begin64 = (int64_t)(first_key(A, U.pos0) & ~31) + (int64_t)s0 * A.step;
-    const int begin = (int)begin64;
-    const int64_t end64 = begin64 + (int64_t)(s1 - s0) * A.step - 1;
-    const int last = end64 < limit(A, p1) ? (int)end64 : limit(A, p1);
-
-    // The table's entries are asked for two rounds ahead.
-    struct Pages {
-      int p[2];
-    };
-    const Entries table = entries(A.b.table + (int64_t)seq * A.b.table_ld);
-    auto pages = [&](int key) {
-      Pages g;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) g.p[h] = table[(key + 16 * h < last ? key + 16 * h : last) >> A.c.shift];
-      return g;
-    };
-    auto mapped = [&](const Pages& g, int h) { return (uint32_t)g.p[h] < (uint32_t)A.c.pages; };
-    // Loads are never skipped, since the wait for a tile counts those of the next
-    // one: beyond the last key, and where a page is not mapped, they read others.
-    auto load = [&](int key, const Pages& g, Tile<FMT, D>& T) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        load_half<FMT, D>(A.c, kv_slot(A.c, mapped(g, h) ? g.p[h] : 0, head, (key + 16 * h) & ((1 << A.c.shift) - 1)), T.k[h],
-                          T.ks[h], T.v[h], T.vs[h]);
-    };
+    const int64_t p0 = P.pos0 + P.r0 / A.group, p1 = P.pos0 + (P.r0 + P.rows - 1) / A.group;
+    const int first = first_key(A, p0), every_first = first_key(A, p1), every_last = limit(A, p0), last = P.last;
     auto use = [&](int key, const Pages& g, Tile<FMT, D>& T) {
       // scores: s[i][h][j] is key 16 h + 4 c + j for row n of tile i
       f4_t s[NR][2];
@@ -534,19 +599,16 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
       }
     };
 
-    int key = begin + 32 * wave;
+    int key = P.begin + 32 * wave;
     if (key <= last) {
-      Tile<FMT, D> T0, T1;
-      Pages g0 = pages(key), g1 = pages(key + kKeys);
-      load(key, g0, T0);
       while (true) {
-        load(key + kKeys, g1, T1);
-        const Pages g2 = pages(key + 2 * kKeys);
+        load(P, key + kKeys, g1, T1);
+        const Pages g2 = pages(P, key + 2 * kKeys);
         use(key, g0, T0);
         key += kKeys;
         if (key > last) break;
-        load(key + kKeys, g2, T0);
-        const Pages g3 = pages(key + 2 * kKeys);
+        load(P, key + kKeys, g2, T0);
+        const Pages g3 = pages(P, key + 2 * kKeys);
         use(key, g1, T1);
         key += kKeys;
         if (key > last) break;
@@ -554,14 +616,19 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
         g1 = g3;
       }
     }
+    const bool more = at < stop;
+    Part N = P;
+    if (more) {
+      setup(N);
+      issue(N);
+    }
 
-    // the waves' shares of the rows, joined, a tile at a time
-    const bool all = s1 - s0 == U.steps;               // the unit's: the output; else a slot, the first where a share
-    float* slot = A.part + (2 * (int64_t)blockIdx.x + (s0 == 0)) * slot_floats(D, kUnit);   // goes on with a unit
-    if (s0 == 0 && !all) left = Left{U.row0, rows, r0, head, shares.owner(at - s1 + U.steps - 1)};
+    // the waves' shares of the rows, joined, a tile at a time: the unit's output, or one of the workgroup's two slots
+    float* slot = A.part + (2 * (int64_t)blockIdx.x + !P.goes_on) * slot_floats(D, kUnit);
+    if (!P.all && !P.goes_on) left = Left{P.row0, P.rows, P.r0, P.head, P.owner};
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-      if (kRows * i >= rows) break;
+      if (kRows * i >= P.rows) break;
       const float l = row_sum(R[i].l);
       if (c == 0) {
         stats[0][wave][n] = R[i].m;
@@ -583,11 +650,11 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
         L += stats[1][k][row] * w[k];
       }
       const int ur = kRows * i + row;
-      if (ur < rows) {
-        const int rr = r0 + ur;
-        const int64_t t = U.row0 + rr / A.group;
-        const int qh = head * A.group + rr % A.group;
-        const float inv = !all ? 1.0f : L == 0.0f ? 0.0f : ldexpf(1.0f / L, ev);
+      if (ur < P.rows) {
+        const int rr = P.r0 + ur;
+        const int64_t t = P.row0 + rr / A.group;
+        const int qh = P.head * A.group + rr % A.group;
+        const float inv = !P.all ? 1.0f : L == 0.0f ? 0.0f : ldexpf(1.0f / L, ev);
 #pragma unroll
         for (int d = 0; d < D / 16; d += 4) {
           float x[4];
@@ -598,13 +665,13 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
             for (int k = 0; k < kWaves; ++k) x[e] += part[k][row * LD + d0 + d + e] * w[k];
             x[e] *= inv;
           }
-          if (all)
+          if (P.all)
             store_whole(A.out, false, t * A.ldo + (int64_t)qh * D + d0 + d, x);
           else
             store_whole(slot, true, 2 * kUnit + ur * D + d0 + d, x);
         }
         if (d0 == 0) {
-          if (!all) {
+          if (!P.all) {
             slot[ur] = M;
             slot[kUnit + ur] = L;
           } else if (A.lse) {
@@ -612,8 +679,10 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
           }
         }
       }
-      if (i + 1 < NR || at < stop) __syncthreads();
+      if (i + 1 < NR || more) __syncthreads();
     }
+    if (!more) break;
+    P = N;
   }
   if (threadIdx.x == 0) A.left[blockIdx.x] = left;
 }
@@ -714,7 +783,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 3 : 2) void kv_prompt_kernel
   for (int i = 0; i < NR; ++i) {
     const int r = w0 + kRows * i + n, tok = r / A.group;
     const bool mine = kRows * i + n < wrows;
-    R[i].start(mine ? A.q + (U.row0 + tok) * A.ldq + (int64_t)(head * A.group + r % A.group) * D : nullptr, A.scale, ek);
+    R[i].load(mine ? A.q + (U.row0 + tok) * A.ldq + (int64_t)(head * A.group + r % A.group) * D : nullptr);
+    R[i].start(A.scale, ek);
     R[i].factor = fmaxf(R[i].factor, 1.0e-37f);        // times -inf is -inf
     R[i].last = mine ? limit(A, U.pos0 + tok) : -1;
     R[i].first = first_key(A, U.pos0 + tok);
