@@ -169,7 +169,8 @@ size_t snipkv_attn_workspace(int64_t tokens, int64_t seqs, int64_t q_heads, int6
   if (tokens < 1 || tokens > kMaxTokens || seqs < 1 || seqs > kMaxSeqs || kv_heads < 1 || kv_heads > kMaxHeads ||
       q_heads < 1 || q_heads > kMaxHeads || q_heads % kv_heads || !head_dim_ok(head_dim))
     return 0;
-  if (kv_attn_tiles(tokens, seqs, q_heads / kv_heads) > kMaxTiles) return 0;
+  const int64_t tiles = kv_attn_tiles(tokens, seqs, q_heads / kv_heads);
+  if (tiles > kMaxTiles || tiles * kv_heads > (int64_t)1 << 30) return 0;      // steps are counted in 31 bits
   return align_up(kv_attn_slots((int)head_dim), kAlign);
 }
 

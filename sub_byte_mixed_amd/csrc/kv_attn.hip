@@ -50,22 +50,28 @@ struct Tile {
   uint32_t v[2][G::VL][G::VB], vs[2][G::VL];
 };
 
-template <int N>
+template <bool NT, typename T>
+__device__ __forceinline__ T fetch(const uint8_t* p) {
+  const T* q = reinterpret_cast<const T*>(p);
+  return NT ? __builtin_nontemporal_load(q) : *q;
+}
+
+template <bool NT, int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
   if constexpr (N == 4) {
-    const u32x4_t x = *reinterpret_cast<const u32x4_t*>(p);
+    const u32x4_t x = fetch<NT, u32x4_t>(p);
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = x[i];
   } else {
     static_assert(N == 2, "");
-    const u32x2_t x = *reinterpret_cast<const u32x2_t*>(p);
+    const u32x2_t x = fetch<NT, u32x2_t>(p);
     w[0] = x[0];
     w[1] = x[1];
   }
 }
 
 // 16 tokens from `slot` (wave-uniform): a lane's share.
-template <int FMT, int D>
+template <int FMT, int D, bool NT = false>
 __device__ __forceinline__ void load_half(const KvCache& C, int64_t slot, uint32_t (&k)[Geo<FMT, D>::KL][Geo<FMT, D>::KD],
                                           uint32_t (&ksc)[Geo<FMT, D>::KL], uint32_t (&v)[Geo<FMT, D>::VL][Geo<FMT, D>::VB],
                                           uint32_t (&vsc)[Geo<FMT, D>::VL]) {
@@ -77,7 +83,7 @@ __device__ __forceinline__ void load_half(const KvCache& C, int64_t slot, uint32
   const uint8_t* vs = C.vs + slot * (D / G::BLK);
 #pragma unroll
   for (int l = 0; l < G::KL; ++l) {
-    load_words<G::KD>(kc + (64 * l + lane) * G::PB, k[l]);
+    load_words<NT>(kc + (64 * l + lane) * G::PB, k[l]);
     if constexpr (G::SB == 2)
       ksc[l] = *reinterpret_cast<const uint16_t*>(ks + (64 * l + lane) * 2);
     else if constexpr (2 * G::PB < G::BLK)             // two pieces to a block
@@ -87,7 +93,7 @@ __device__ __forceinline__ void load_half(const KvCache& C, int64_t slot, uint32
   }
 #pragma unroll
   for (int l = 0; l < G::VL; ++l) {
-    load_words<G::VB>(vc + c * 2 * D + (16 * l + n) * 4 * G::VB, v[l]);
+    load_words<NT>(vc + c * 2 * D + (16 * l + n) * 4 * G::VB, v[l]);
     vsc[l] = *reinterpret_cast<const uint32_t*>(vs + c * 4 * (D / G::BLK) + (16 * l + n) * 2 * G::VB / G::BLK * 4);
   }
 }
@@ -383,7 +389,19 @@ __device__ __forceinline__ void store_lse(const KvAttn& A, int64_t t, int qh, fl
   A.lse[t * A.q_heads + qh] = L == 0.0f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(L)) * 0.693147180559945309f;
 }
 
-template <int FMT, int D, int NR>
+template <int E>
+__device__ __forceinline__ void store_few(void* p, bool f32, int64_t off, const float (&x)[E]) {
+  if constexpr (E == 2) {
+    if (f32)
+      *reinterpret_cast<float2*>(static_cast<float*>(p) + off) = make_float2(x[0], x[1]);
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p) + off) = pack_bf16(x[0], x[1]);
+  } else {
+    store_whole(p, f32, off, x);
+  }
+}
+
+template <int FMT, int D, int NR, int kWaves, bool NT>
 __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(KvAttn A) {
   using G = Geo<FMT, D>;
   constexpr int LD = D + 4;                            // a row in LDS: the lanes' rows meet different banks
@@ -403,7 +421,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
   int at = shares.first(blockIdx.x);
   const int stop = shares.first(blockIdx.x + 1);
   if (at >= stop) {
-    if (threadIdx.x == 0) A.left[blockIdx.x] = Left{0, 0, 0, 0, 0};
+    if (A.left && threadIdx.x == 0) A.left[blockIdx.x] = Left{0, 0, 0, 0, 0};
     return;
   }
 
@@ -459,7 +477,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
   auto load = [&](const Part& P, int key, const Pages& g, Tile<FMT, D>& T) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      load_half<FMT, D>(A.c, kv_slot(A.c, mapped(g, h) ? g.p[h] : 0, P.head, (key + 16 * h) & ((1 << A.c.shift) - 1)), T.k[h],
+      load_half<FMT, D, NT>(A.c, kv_slot(A.c, mapped(g, h) ? g.p[h] : 0, P.head, (key + 16 * h) & ((1 << A.c.shift) - 1)), T.k[h],
                         T.ks[h], T.v[h], T.vs[h]);
   };
   auto issue = [&](const Part& P) {
@@ -640,7 +658,9 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
         for (int j = 0; j < 4; ++j)                    // dimension of O^T's row 4 c + j in tile d
           part[wave][n * LD + (d / (2 * G::VB)) * 32 * G::VB + (4 * c + j) * 2 * G::VB + d % (2 * G::VB)] = R[i].o[d][j];
       __syncthreads();
-      const int row = threadIdx.x / 16, d0 = threadIdx.x % 16 * (D / 16);
+      constexpr int LR = 4 * kWaves;                   // lanes of a row
+      constexpr int E = D / LR < 4 ? D / LR : 4;
+      const int row = threadIdx.x / LR, d0 = threadIdx.x % LR * (D / LR);
       float M = kLowest, L = 0.0f, w[kWaves];
 #pragma unroll
       for (int k = 0; k < kWaves; ++k) M = fmaxf(M, stats[0][k][row]);
@@ -656,19 +676,19 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
         const int qh = P.head * A.group + rr % A.group;
         const float inv = !P.all ? 1.0f : L == 0.0f ? 0.0f : ldexpf(1.0f / L, ev);
 #pragma unroll
-        for (int d = 0; d < D / 16; d += 4) {
-          float x[4];
+        for (int d = 0; d < D / LR; d += E) {
+          float x[E];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < E; ++e) {
             x[e] = 0.0f;
 #pragma unroll
             for (int k = 0; k < kWaves; ++k) x[e] += part[k][row * LD + d0 + d + e] * w[k];
             x[e] *= inv;
           }
           if (P.all)
-            store_whole(A.out, false, t * A.ldo + (int64_t)qh * D + d0 + d, x);
+            store_few(A.out, false, t * A.ldo + (int64_t)qh * D + d0 + d, x);
           else
-            store_whole(slot, true, 2 * kUnit + ur * D + d0 + d, x);
+            store_few(slot, true, 2 * kUnit + ur * D + d0 + d, x);
         }
         if (d0 == 0) {
           if (!P.all) {
@@ -684,7 +704,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
     if (!more) break;
     P = N;
   }
-  if (threadIdx.x == 0) A.left[blockIdx.x] = left;
+  if (A.left && threadIdx.x == 0) A.left[blockIdx.x] = left;
 }
 
 // A unit that several workgroups had a share of, joined: blockIdx.x is the one
@@ -704,14 +724,39 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn A, bool nv) {
   const int sub = threadIdx.x / LR, d = threadIdx.x % LR * 4;
   float M = kLowest, L = 0.0f;
   f4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int w = w0 + sub; w <= w1; w += SUBS) M = fmaxf(M, slot(w)[row]);
-#pragma unroll 4
-  for (int w = w0 + sub; w <= w1; w += SUBS) {
-    const float* p = slot(w);
-    const float f = __builtin_amdgcn_exp2f(p[row] - M);
-    L += p[kUnit + row] * f;
-    x += *reinterpret_cast<const f4_t*>(p + 2 * kUnit + row * D + d) * f;
+  if (w1 - w0 < SUBS) {
+    if (w0 + sub <= w1) {
+      const float* p = slot(w0 + sub);
+      M = p[row];
+      L = p[kUnit + row];
+      x = *reinterpret_cast<const f4_t*>(p + 2 * kUnit + row * D + d);
+    }
+  } else {
+    for (int w = w0 + sub; w <= w1; w += 4 * SUBS) {   // four parts in flight
+      f4_t v[4];
+      float m[4], l[4], top = M;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool in = w + u * SUBS <= w1;
+        const float* p = slot(in ? w + u * SUBS : w);
+        m[u] = in ? p[row] : kLowest;
+        l[u] = in ? p[kUnit + row] : 0.0f;
+        v[u] = *reinterpret_cast<const f4_t*>(p + 2 * kUnit + row * D + d);
+        if (!in) v[u] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) top = fmaxf(top, m[u]);
+      const float old = __builtin_amdgcn_exp2f(M - top);
+      M = top;
+      L *= old;
+      x *= old;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float f = __builtin_amdgcn_exp2f(m[u] - M);
+        L += l[u] * f;
+        x += v[u] * f;
+      }
+    }
   }
   so[sub][threadIdx.x % LR] = x;
   if (d == 0) {
@@ -981,6 +1026,12 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 3 : 2) void kv_prompt_kernel
   }
 }
 
+// Keys up to which a workgroup takes a unit as a whole: the second launch costs
+// as much as five rounds of eight waves.
+constexpr int kShort = 1280;
+// Bytes of a cache from which it is read past the last-level cache.
+constexpr int64_t kStream = (int64_t)128 << 20;
+
 }  // namespace
 
 int64_t kv_attn_tiles(int64_t tokens, int64_t seqs, int64_t group) { return tokens * group / kRows + seqs; }
@@ -995,30 +1046,54 @@ size_t kv_attn_slots(int dim) {
 }
 
 hipError_t launch_kv_attn(int format, int dim, KvAttn a, hipStream_t s) {
-  // steps are counted in 31 bits, whatever the lengths that the tables allow
-  const double tiles = (double)kv_attn_tiles(a.tokens, a.b.seqs, a.group) * a.c.heads;
-  a.step = 32 * kWaves;
-  while (a.step < a.b.max_len && tiles * ((double)a.b.max_len / a.step + 1.0) >= 2147483647.0) a.step *= 2;
+  const bool nv = format == SNIP_NVFP4;
   const int64_t rows = a.tokens * a.group / a.b.seqs;    // of a sequence, on average
-  const bool two = dim != 256 && rows > kRows;
   const int unit = kRows * kWaves * prompt_tiles(dim);
   const int64_t places = a.b.cu ? a.tokens * a.group / unit + a.b.seqs : (int64_t)a.b.seqs * ((a.group + unit - 1) / unit);
   const bool prompt = rows >= 64 && a.tokens * a.group / unit * a.c.heads >= 256 && places * a.c.heads < (1 << 24);
   a.split = prompt && a.b.seqs > 1;
   a.few = a.split ? 64 : 0;
+  // Short tables: a workgroup a unit and no second launch.
+  const bool whole = a.b.max_len <= kShort && !prompt;
+  const double tiles = (double)kv_attn_tiles(a.tokens, a.b.seqs, a.group) * a.c.heads;
+  const bool wide = whole && tiles <= 512.0;
+  const bool two = dim != 256 && rows > kRows && !wide;
+  // steps are counted in 31 bits, whatever the lengths that the tables allow
+  a.step = 32 * kWaves;
+  while (a.step < a.b.max_len && (whole || tiles * ((double)a.b.max_len / a.step + 1.0) >= 2147483647.0)) a.step *= 2;
+  const int blk = nv ? 16 : 32;
+  const bool nt = !whole && ((int64_t)a.c.pages * a.c.heads << a.c.shift) * (dim + 2 * dim / blk) >= kStream;
+
   auto go = [&](auto f, auto d, auto t) {
-    constexpr int D = decltype(d)::value, NR = decltype(t)::value, W = workers_of(D, NR);
+    constexpr int FMT = decltype(f)::value, D = decltype(d)::value, NR = decltype(t)::value, W = workers_of(D, NR);
     if (prompt) {
-      kv_prompt_kernel<decltype(f)::value, D, prompt_tiles(D)><<<(unsigned)(places * a.c.heads), 64 * kWaves, 0, s>>>(a);
+      kv_prompt_kernel<FMT, D, prompt_tiles(D)><<<(unsigned)(places * a.c.heads), 64 * kWaves, 0, s>>>(a);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess || !a.split) return e;
     }
+    if (whole) {
+      const int64_t most = (a.b.cu ? a.tokens * a.group / (kRows * NR) + a.b.seqs
+                                   : (int64_t)a.b.seqs * ((a.group + kRows * NR - 1) / (kRows * NR))) * a.c.heads;
+      const unsigned grid = (unsigned)(most < (1 << 20) ? most : 1 << 20);
+      a.left = nullptr;
+      if constexpr (NR == 1) {
+        if (wide) {
+          kv_attn_kernel<FMT, D, 1, 8, false><<<grid, 64 * 8, 0, s>>>(a);
+          return hipGetLastError();
+        }
+      }
+      kv_attn_kernel<FMT, D, NR, kWaves, false><<<grid, 64 * kWaves, 0, s>>>(a);
+      return hipGetLastError();
+    }
     a.left = reinterpret_cast<Left*>(a.part + (size_t)W * 2 * slot_floats(D, kRows * NR));
-    kv_attn_kernel<decltype(f)::value, D, NR><<<W, 64 * kWaves, 0, s>>>(a);
+    if (nt)
+      kv_attn_kernel<FMT, D, NR, kWaves, true><<<W, 64 * kWaves, 0, s>>>(a);
+    else
+      kv_attn_kernel<FMT, D, NR, kWaves, false><<<W, 64 * kWaves, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int rows = !a.b.cu && a.group < kRows * NR ? a.group : kRows * NR;   // a unit has no more
-    kv_join_kernel<D, NR><<<dim3(W - 1, rows), 256, 0, s>>>(a, format == SNIP_NVFP4);
+    const int most = !a.b.cu && a.group < kRows * NR ? a.group : kRows * NR;   // rows of a unit
+    kv_join_kernel<D, NR><<<dim3(W - 1, most), 256, 0, s>>>(a, nv);
     return hipGetLastError();
   };
   auto of = [&](auto f, auto d) {
@@ -1031,7 +1106,7 @@ hipError_t launch_kv_attn(int format, int dim, KvAttn a, hipStream_t s) {
            : dim == 128 ? of(f, std::integral_constant<int, 128>{})
                         : of(f, std::integral_constant<int, 256>{});
   };
-  return format == SNIP_NVFP4 ? at(std::integral_constant<int, SNIP_NVFP4>{}) : at(std::integral_constant<int, SNIP_MXFP4>{});
+  return nv ? at(std::integral_constant<int, SNIP_NVFP4>{}) : at(std::integral_constant<int, SNIP_MXFP4>{});
 }
 
 }  // namespace snip
