@@ -408,7 +408,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
   constexpr int kKeys = 32 * kWaves;                   // of a round of the waves
   constexpr int kUnit = kRows * NR;
   __shared__ float stats[2][kWaves][kRows];
-  __shared__ float part[kWaves][kRows * LD];
+  __shared__ f4_t part[kWaves][kRows * LD / 4];
   __shared__ int upto[kWaves][2][64];
   const int lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -653,10 +653,13 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
         stats[1][wave][n] = l;
       }
 #pragma unroll
-      for (int d = 0; d < G::DT; ++d)
+      for (int v = 0; v < G::VL; ++v)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)                    // dimension of O^T's row 4 c + j in tile d
-          part[wave][n * LD + (d / (2 * G::VB)) * 32 * G::VB + (4 * c + j) * 2 * G::VB + d % (2 * G::VB)] = R[i].o[d][j];
+        for (int j = 0; j < 4; ++j)                    // O^T's row 4 c + j in 2 VB tiles: dimensions in a row
+#pragma unroll
+          for (int d = 0; d < 2 * G::VB; d += 4)
+            part[wave][(n * LD + v * 32 * G::VB + (4 * c + j) * 2 * G::VB + d) / 4] =
+                f4_t{R[i].o[v * 2 * G::VB + d][j], R[i].o[v * 2 * G::VB + d + 1][j], R[i].o[v * 2 * G::VB + d + 2][j], R[i].o[v * 2 * G::VB + d + 3][j]};
       __syncthreads();
       constexpr int LR = 4 * kWaves;                   // lanes of a row
       constexpr int E = D / LR < 4 ? D / LR : 4;
@@ -682,7 +685,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
           for (int e = 0; e < E; ++e) {
             x[e] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kWaves; ++k) x[e] += part[k][row * LD + d0 + d + e] * w[k];
+            for (int k = 0; k < kWaves; ++k) x[e] += reinterpret_cast<const float*>(part[k])[row * LD + d0 + d + e] * w[k];
             x[e] *= inv;
           }
           if (P.all)
