@@ -898,6 +898,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 3 : 2) void kv_prompt_kernel
   };
   auto use = [&](int key, int buf, const Pages& g) {
     f4_t s[NR][KH];
+    if constexpr (D == 128) __builtin_amdgcn_s_setprio(1);   // over the other workgroup's softmax (187 -> 183 us)
 #pragma unroll
     for (int h = 0; h < KH; ++h) {
 #pragma unroll
@@ -909,6 +910,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 3 : 2) void kv_prompt_kernel
         for (int i = 0; i < NR; ++i) s[i][h] = mfma<FMT>(k, R[i].q[w / G::KD][w % G::KD], s[i][h]);
       }
     }
+    if constexpr (D == 128) __builtin_amdgcn_s_setprio(0);
     bool whole = (key >= every_first) & (key + kKeys - 1 <= every_last);
 #pragma unroll
     for (int h = 0; h < KH; ++h) whole &= mapped(g.p[h]);
@@ -966,6 +968,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 3 : 2) void kv_prompt_kernel
           }
         }
       }
+      if constexpr (D == 128) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int d = 0; d < G::DT; ++d) {
         const u32x4_t a = *reinterpret_cast<const u32x4_t*>(vals[buf][pr][d][lane]);
@@ -975,6 +978,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 3 : 2) void kv_prompt_kernel
           if constexpr (!G::NV) R[i].o[d] = mfma<FMT>(a, pl[i], R[i].o[d]);
         }
       }
+      if constexpr (D == 128) __builtin_amdgcn_s_setprio(0);
     }
   };
 
