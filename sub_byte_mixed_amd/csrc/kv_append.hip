@@ -21,16 +21,10 @@ constexpr int kWaves = 4;
 // Waves a launch holds at most; more walk on. A grid has fewer than 2^32 threads.
 constexpr int64_t kMaxWG = 1 << 20;
 
-__device__ __forceinline__ void load8(const void* p, bool f32, int64_t off, float (&x)[8]) {
-  if (f32) {
-    Raw<true> r;
-    load_whole(p, off, r);
-    raw_to_f32(r, x);
-  } else {
-    Raw<false> r;
-    load_whole(p, off, r);
-    raw_to_f32(r, x);
-  }
+__device__ __forceinline__ void load8(const float* p, int64_t off, float (&x)[8]) {
+  Raw<true> r;
+  load_whole(p, off, r);
+  raw_to_f32(r, x);
 }
 
 // The 8 elements' share of a block: codes in *w, scale byte in *sc (the same in
@@ -64,7 +58,7 @@ __device__ __forceinline__ void encode8(float (&x)[8], int e, uint32_t* w, uint3
   *w = fp4x8_rne(x);
 }
 
-template <int FMT, int D>
+template <int FMT, int D, bool F32>
 __global__ __launch_bounds__(64 * kWaves) void kv_append_kernel(KvAppend A) {
   using At = KvAt<FMT, D>;
   constexpr int LPH = D / 16, HPW = 64 / LPH;              // lanes of a head, heads of a wave
@@ -76,7 +70,6 @@ __global__ __launch_bounds__(64 * kWaves) void kv_append_kernel(KvAppend A) {
   const bool turned = 16 * c < A.rot;                      // the part of the head that this lane has
   const int part = turned ? 0 : A.rot, half = ((turned ? A.rot : D) - part) / 2;
   const int lo = part + 8 * (c - part / 16), hi = lo + half;
-  const bool f32 = A.type == SNIPOP_F32;
   int ek = 0, ev = 0;
   if constexpr (FMT == SNIP_NVFP4) {
     if (nk) {
@@ -87,19 +80,22 @@ __global__ __launch_bounds__(64 * kWaves) void kv_append_kernel(KvAppend A) {
   for (int64_t u = (int64_t)blockIdx.x * kWaves + wave; u < all; u += (int64_t)gridDim.x * kWaves) {
     const int64_t t = u / units;
     const int h = (int)(u - t * units) * HPW + lane / LPH;
-    const KvRow row = kv_row(A.b, t);
-    if (row.seq < 0) continue;
     const int kind = h < nq ? 0 : h < nq + nk ? 1 : h < nq + 2 * nk ? 2 : 3;
     const int hh = kind == 0 ? h : kind == 1 ? h - nq : h - nq - nk;
-    float x[8] = {}, y[8] = {};
+    // the elements are asked for before the row's place is looked up
+    Raw<F32> rx = {}, ry = {};
     if (kind < 3) {
       const void* p = kind == 0 ? A.q : kind == 1 ? A.k : A.v;
       const int64_t off = t * (kind == 0 ? A.ldq : kind == 1 ? A.ldk : A.ldv) + hh * D;
-      load8(p, f32, off + lo, x);
-      load8(p, f32, off + hi, y);
+      load_whole(p, off + lo, rx);
+      load_whole(p, off + hi, ry);
     }
+    const KvRow row = kv_row(A.b, t);
+    if (row.seq < 0) continue;
+    const int page = nk ? kv_page(A.c, A.b, row.seq, row.pos) : -1;
+    float x[8], y[8];
     if (turned && kind < 2) {
-      int64_t at = A.pos ? (int64_t)A.pos[t] : row.pos;
+      int64_t at = A.pos ? (int64_t)entries(A.pos)[t] : row.pos;
       at = at < 0 ? 0 : at >= A.angles ? A.angles - 1 : at;
       const int64_t o = at * (A.rot / 2);
       if (A.interleaved) {
@@ -107,6 +103,8 @@ __global__ __launch_bounds__(64 * kWaves) void kv_append_kernel(KvAppend A) {
         float4 ch = *reinterpret_cast<const float4*>(A.cos + o + hi / 2), sh = *reinterpret_cast<const float4*>(A.sin + o + hi / 2);
         const float cc[8] = {cl.x, cl.y, cl.z, cl.w, ch.x, ch.y, ch.z, ch.w};
         const float ss[8] = {sl.x, sl.y, sl.z, sl.w, sh.x, sh.y, sh.z, sh.w};
+        raw_to_f32(rx, x);
+        raw_to_f32(ry, y);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float a = x[2 * i], b = x[2 * i + 1], p = y[2 * i], q = y[2 * i + 1];
@@ -117,8 +115,10 @@ __global__ __launch_bounds__(64 * kWaves) void kv_append_kernel(KvAppend A) {
         }
       } else {
         float cc[8], ss[8];
-        load8(A.cos, true, o + lo, cc);
-        load8(A.sin, true, o + lo, ss);
+        load8(A.cos, o + lo, cc);
+        load8(A.sin, o + lo, ss);
+        raw_to_f32(rx, x);
+        raw_to_f32(ry, y);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float a = x[i], b = y[i];
@@ -126,12 +126,14 @@ __global__ __launch_bounds__(64 * kWaves) void kv_append_kernel(KvAppend A) {
           y[i] = b * cc[i] + a * ss[i];
         }
       }
+    } else {
+      raw_to_f32(rx, x);
+      raw_to_f32(ry, y);
     }
     if (kind == 0) {
       store_whole(A.q_out, false, t * A.ldqo + hh * D + lo, x);
       store_whole(A.q_out, false, t * A.ldqo + hh * D + hi, y);
     }
-    const int page = nk ? kv_page(A.c, A.b, row.seq, row.pos) : -1;
     if (page < 0) continue;
     // every lane takes part in its block's maximum
     uint32_t wx, wy, sx, sy;
@@ -172,53 +174,58 @@ __global__ __launch_bounds__(64 * kWaves) void kv_append_kernel(KvAppend A) {
   }
 }
 
-// Reading back: a lane decodes 8 dimensions. Bound by the bf16 that it writes.
-template <int FMT, int D>
+// Reading back: a lane decodes 8 dimensions of TPW tokens in a row, whose loads
+// are in flight together. Bound by the bf16 that it writes, or by latency.
+template <int FMT, int D, int TPW>
 __global__ __launch_bounds__(64 * kWaves) void kv_gather_kernel(KvGather A) {
   using At = KvAt<FMT, D>;
   constexpr int LPH = D / 8, HPW = 64 / LPH;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nk = A.k ? A.c.heads : 0, nv = A.v ? A.c.heads : 0;
   const int units = (nk + nv + HPW - 1) / HPW;
-  const int64_t all = A.tokens * units;
+  const int64_t all = (A.tokens + TPW - 1) / TPW * units;
   const int d = 8 * (lane % LPH);
-  int ek = 0, ev = 0;
-  if constexpr (FMT == SNIP_NVFP4) {
-    ek = A.c.texp[0];
-    ev = A.c.texp[1];
-  }
+  const int ek = FMT == SNIP_NVFP4 ? entries(A.c.texp)[0] : 0, ev = FMT == SNIP_NVFP4 ? entries(A.c.texp)[1] : 0;
   for (int64_t u = (int64_t)blockIdx.x * kWaves + wave; u < all; u += (int64_t)gridDim.x * kWaves) {
-    const int64_t t = u / units;
-    const int h = (int)(u - t * units) * HPW + lane / LPH;
-    const KvRow row = kv_row(A.b, t);
-    if (row.seq < 0 || h >= nk + nv) continue;
-    const int page = kv_page(A.c, A.b, row.seq, row.pos);
-    const bool key = h < nk;
-    const int hh = key ? h : h - nk;
-    float q[8] = {};
-    if (page >= 0) {
-      const int at = (int)(row.pos & ((1 << A.c.shift) - 1));
-      const int64_t g = kv_slot(A.c, page, hh, key ? at & ~15 : at & ~3);
+    const int64_t t0 = u / units * TPW;
+    const int h = (int)(u % units) * HPW + lane / LPH;
+    const bool key = h < nk, some = h < nk + nv;
+    const int hh = some ? (key ? h : h - nk) : 0;
+    KvRow row = kv_row(A.b, t0);
+    uint32_t w[TPW], b[TPW];
+    int seq[TPW], page[TPW];
+#pragma unroll
+    for (int i = 0; i < TPW; ++i) {
+      if (i) row = t0 + i < A.tokens ? kv_next(A.b, row, t0 + i - 1) : KvRow{-1, -1, t0 + i + 1};
+      seq[i] = row.seq;
+      page[i] = kv_page(A.c, A.b, row.seq, row.pos);
+      const int at = page[i] < 0 ? 0 : (int)(row.pos & ((1 << A.c.shift) - 1));   // not mapped: any page
+      const int64_t g = kv_slot(A.c, page[i] < 0 ? 0 : page[i], hh, key ? at & ~15 : at & ~3);
       const uint8_t* pc = (key ? A.c.kc : A.c.vc) + g * (D / 2);
       const uint8_t* ps = (key ? A.c.ks : A.c.vs) + g * (D / At::BLK);
-      uint32_t w;
-      if (key || At::V == 4)
-        w = *reinterpret_cast<const uint32_t*>(pc + (key ? At::k_code(at, d) : At::v_code(at, d)));
+      if (At::V == 4)
+        w[i] = *reinterpret_cast<const uint32_t*>(pc + (key ? At::k_code(at, d) : At::v_code(at, d)));
       else
-        w = *reinterpret_cast<const uint16_t*>(pc + At::v_code(at, d)) |
-            (uint32_t)*reinterpret_cast<const uint16_t*>(pc + At::v_code(at, d + 4)) << 16;
-      const uint32_t b = ps[key ? At::k_scale(at, d) : At::v_scale(at, d)];
-      fp4x8_dec(w, q);
-      const int e = FMT == SNIP_NVFP4 ? (key ? ek : ev) : (int)b - 127;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if constexpr (FMT == SNIP_NVFP4)
-          q[i] = ldexpf(q[i] * __builtin_amdgcn_cvt_f32_fp8((int)b, 0), e);
-        else
-          q[i] = b == 255u ? __uint_as_float(0x7FC00000u) : ldexpf(q[i], e);
-      }
+        w[i] = *reinterpret_cast<const uint16_t*>(pc + (key ? At::k_code(at, d) : At::v_code(at, d))) |
+               (uint32_t)*reinterpret_cast<const uint16_t*>(pc + (key ? At::k_code(at, d) + 2 : At::v_code(at, d + 4))) << 16;
+      b[i] = ps[key ? At::k_scale(at, d) : At::v_scale(at, d)];
     }
-    store_whole(key ? A.k : A.v, false, t * (key ? A.ldk : A.ldv) + hh * D + d, q);
+#pragma unroll
+    for (int i = 0; i < TPW; ++i) {
+      if (seq[i] < 0 || !some) continue;
+      float q[8];
+      fp4x8_dec(w[i], q);
+      const int e = FMT == SNIP_NVFP4 ? (key ? ek : ev) : (int)b[i] - 127;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (FMT == SNIP_NVFP4)
+          q[j] = ldexpf(q[j] * __builtin_amdgcn_cvt_f32_fp8((int)b[i], 0), e);
+        else
+          q[j] = b[i] == 255u ? __uint_as_float(0x7FC00000u) : ldexpf(q[j], e);
+        if (page[i] < 0) q[j] = 0.0f;
+      }
+      store_whole(key ? A.k : A.v, false, (t0 + i) * (key ? A.ldk : A.ldv) + hh * D + d, q);
+    }
   }
 }
 
@@ -245,7 +252,11 @@ hipError_t launch_kv_append(int format, int dim, const KvAppend& a, hipStream_t 
   return dispatch(format, dim, [&](auto f, auto d) {
     constexpr int D = decltype(d)::value;
     const int heads = (a.q ? a.q_heads : 0) + (a.k ? 2 * a.c.heads : 0);
-    kv_append_kernel<decltype(f)::value, D><<<grid_of(a.tokens, heads, 1024 / D), 64 * kWaves, 0, s>>>(a);
+    const unsigned grid = (unsigned)grid_of(a.tokens, heads, 1024 / D);
+    if (a.type == SNIPOP_F32)
+      kv_append_kernel<decltype(f)::value, D, true><<<grid, 64 * kWaves, 0, s>>>(a);
+    else
+      kv_append_kernel<decltype(f)::value, D, false><<<grid, 64 * kWaves, 0, s>>>(a);
     return hipGetLastError();
   });
 }
@@ -254,7 +265,11 @@ hipError_t launch_kv_gather(int format, int dim, const KvGather& a, hipStream_t 
   return dispatch(format, dim, [&](auto f, auto d) {
     constexpr int D = decltype(d)::value;
     const int heads = (a.k ? a.c.heads : 0) + (a.v ? a.c.heads : 0);
-    kv_gather_kernel<decltype(f)::value, D><<<grid_of(a.tokens, heads, 512 / D), 64 * kWaves, 0, s>>>(a);
+    const int64_t wg = grid_of(a.tokens, heads, 512 / D);
+    if (a.b.cu && wg >= 8192)                              // more waves than are resident, four times over
+      kv_gather_kernel<decltype(f)::value, D, 4><<<(unsigned)grid_of((a.tokens + 3) / 4, heads, 512 / D), 64 * kWaves, 0, s>>>(a);
+    else
+      kv_gather_kernel<decltype(f)::value, D, 1><<<(unsigned)wg, 64 * kWaves, 0, s>>>(a);
     return hipGetLastError();
   });
 }

@@ -245,11 +245,6 @@ struct Rows {
   }
 };
 
-// Loads whose address is the same in the wave's lanes, of what the launch does
-// not write: scalar, and not waited for in order with the vector loads.
-typedef const __attribute__((address_space(4))) int32_t* Entries;
-__device__ __forceinline__ Entries entries(const int32_t* p) { return (Entries)(uintptr_t)p; }
-
 // Work is counted in steps of a number of keys. A unit -- 16 R rows of one kv
 // head of one sequence -- has the steps of the sequence's keys, units follow each
 // other by sequence, head and rows, and the steps of the call are shared evenly

@@ -7,6 +7,11 @@
 
 namespace snip {
 
+// Loads whose address is the same in the wave's lanes, of what the launch does
+// not write: scalar, and not waited for in order with the vector loads.
+typedef const __attribute__((address_space(4))) int32_t* Entries;
+__device__ __forceinline__ Entries entries(const int32_t* p) { return (Entries)(uintptr_t)p; }
+
 // The sequence that holds x, f ascending: the number of b in 0 .. n with
 // f(b) <= x, less one; -1 before the first, n behind the last. The wave narrows
 // 64 ways a step, so that up to 63 sequences take one load's latency.
@@ -27,22 +32,29 @@ __device__ __forceinline__ int kv_find(int n, int64_t x, F f) {
 }
 
 struct KvRow {
-  int seq;
-  int64_t pos;
+  int seq;                     // < 0: nobody's
+  int64_t pos, end;            // position; the sequence's last row and one
 };
 
-// Sequence and position of row t; seq < 0 where it is nobody's.
+// Sequence and position of row t.
 __device__ __forceinline__ KvRow kv_row(const KvBatch& b, int64_t t) {
-  if (!b.cu) return KvRow{t < b.seqs ? (int)t : -1, t < b.seqs ? (int64_t)b.lens[t] - 1 : -1};
+  if (!b.cu) return t < b.seqs ? KvRow{(int)t, (int64_t)entries(b.lens)[t] - 1, t + 1} : KvRow{-1, -1, t + 1};
   const int s = kv_find(b.seqs, t, [&](int i) { return (int64_t)b.cu[i]; });
-  if (s < 0 || s >= b.seqs) return KvRow{-1, -1};
-  return KvRow{s, (int64_t)b.lens[s] - ((int64_t)b.cu[s + 1] - t)};
+  if (s < 0 || s >= b.seqs) return KvRow{-1, -1, t + 1};
+  const int64_t end = entries(b.cu)[s + 1];
+  return KvRow{s, (int64_t)entries(b.lens)[s] - (end - t), end};
+}
+
+// Row t + 1, after row t.
+__device__ __forceinline__ KvRow kv_next(const KvBatch& b, const KvRow& r, int64_t t) {
+  if (r.seq >= 0 && t + 1 < r.end) return KvRow{r.seq, r.pos + 1, r.end};
+  return kv_row(b, t + 1);
 }
 
 // Number of a page, or -1 where the position is not mapped.
 __device__ __forceinline__ int kv_page(const KvCache& c, const KvBatch& b, int seq, int64_t pos) {
-  if (pos < 0 || pos >= b.max_len) return -1;
-  const int p = b.table[(int64_t)seq * b.table_ld + (pos >> c.shift)];
+  if (seq < 0 || pos < 0 || pos >= b.max_len) return -1;
+  const int p = entries(b.table + (int64_t)seq * b.table_ld)[pos >> c.shift];
   return p >= 0 && p < c.pages ? p : -1;
 }
 
