@@ -20,6 +20,10 @@ namespace {
 constexpr int kWaves = 4;
 // Waves a launch holds at most; more walk on. A grid has fewer than 2^32 threads.
 constexpr int64_t kMaxWG = 1 << 20;
+// Workgroups of single tokens from which a wave takes four: a fourth of the waves
+// still fill the GPU (8192 tokens of 96 heads: 169 -> 153 us with the gather; 1840
+// tokens of 80 heads gain nothing, 31 and 32).
+constexpr int64_t kLong = 8192;
 
 __device__ __forceinline__ void load8(const float* p, int64_t off, float (&x)[8]) {
   Raw<true> r;
@@ -58,117 +62,165 @@ __device__ __forceinline__ void encode8(float (&x)[8], int e, uint32_t* w, uint3
   *w = fp4x8_rne(x);
 }
 
-template <int FMT, int D, bool F32>
+// TPW tokens in a row to a wave: one, or four in long calls. Then a workgroup has
+// 16 tokens of the same heads, so that what they share -- 16 bytes of values and 4
+// of their scales, 256 bytes of keys -- is written by one wave at once, or within
+// one cache.
+template <int FMT, int D, bool F32, int TPW>
 __global__ __launch_bounds__(64 * kWaves) void kv_append_kernel(KvAppend A) {
   using At = KvAt<FMT, D>;
   constexpr int LPH = D / 16, HPW = 64 / LPH;              // lanes of a head, heads of a wave
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nq = A.q ? A.q_heads : 0, nk = A.k ? A.c.heads : 0;
   const int units = (nq + 2 * nk + HPW - 1) / HPW;         // waves of a token
-  const int64_t all = A.tokens * units;
+  const int64_t all = TPW == 1 ? A.tokens * units : (A.tokens + TPW * kWaves - 1) / (TPW * kWaves) * units * kWaves;
   const int c = lane % LPH;
   const bool turned = 16 * c < A.rot;                      // the part of the head that this lane has
   const int part = turned ? 0 : A.rot, half = ((turned ? A.rot : D) - part) / 2;
   const int lo = part + 8 * (c - part / 16), hi = lo + half;
+  const bool first = lo % At::BLK == 0;                    // of its block's lanes
   int ek = 0, ev = 0;
   if constexpr (FMT == SNIP_NVFP4) {
     if (nk) {
-      ek = A.c.texp[0];
-      ev = A.c.texp[1];
+      ek = entries(A.c.texp)[0];
+      ev = entries(A.c.texp)[1];
     }
   }
   for (int64_t u = (int64_t)blockIdx.x * kWaves + wave; u < all; u += (int64_t)gridDim.x * kWaves) {
-    const int64_t t = u / units;
-    const int h = (int)(u - t * units) * HPW + lane / LPH;
+    const int64_t t0 = TPW == 1 ? u / units : (u / kWaves / units * kWaves + wave) * TPW;
+    const int h = (int)((TPW == 1 ? u : u / kWaves) % units) * HPW + lane / LPH;
     const int kind = h < nq ? 0 : h < nq + nk ? 1 : h < nq + 2 * nk ? 2 : 3;
     const int hh = kind == 0 ? h : kind == 1 ? h - nq : h - nq - nk;
-    // the elements are asked for before the row's place is looked up
-    Raw<F32> rx = {}, ry = {};
-    if (kind < 3) {
-      const void* p = kind == 0 ? A.q : kind == 1 ? A.k : A.v;
-      const int64_t off = t * (kind == 0 ? A.ldq : kind == 1 ? A.ldk : A.ldv) + hh * D;
-      load_whole(p, off + lo, rx);
-      load_whole(p, off + hi, ry);
-    }
-    const KvRow row = kv_row(A.b, t);
-    if (row.seq < 0) continue;
-    const int page = nk ? kv_page(A.c, A.b, row.seq, row.pos) : -1;
-    float x[8], y[8];
-    if (turned && kind < 2) {
-      int64_t at = A.pos ? (int64_t)entries(A.pos)[t] : row.pos;
-      at = at < 0 ? 0 : at >= A.angles ? A.angles - 1 : at;
-      const int64_t o = at * (A.rot / 2);
-      if (A.interleaved) {
-        float4 cl = *reinterpret_cast<const float4*>(A.cos + o + lo / 2), sl = *reinterpret_cast<const float4*>(A.sin + o + lo / 2);
-        float4 ch = *reinterpret_cast<const float4*>(A.cos + o + hi / 2), sh = *reinterpret_cast<const float4*>(A.sin + o + hi / 2);
-        const float cc[8] = {cl.x, cl.y, cl.z, cl.w, ch.x, ch.y, ch.z, ch.w};
-        const float ss[8] = {sl.x, sl.y, sl.z, sl.w, sh.x, sh.y, sh.z, sh.w};
-        raw_to_f32(rx, x);
-        raw_to_f32(ry, y);
+    // the elements are asked for before the rows' places are looked up
+    Raw<F32> rx[TPW], ry[TPW];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[2 * i], b = x[2 * i + 1], p = y[2 * i], q = y[2 * i + 1];
-          x[2 * i] = a * cc[i] - b * ss[i];
-          x[2 * i + 1] = b * cc[i] + a * ss[i];
-          y[2 * i] = p * cc[4 + i] - q * ss[4 + i];
-          y[2 * i + 1] = q * cc[4 + i] + p * ss[4 + i];
-        }
-      } else {
+    for (int i = 0; i < TPW; ++i) {
+      rx[i] = {};
+      ry[i] = {};
+      if (kind < 3 && t0 + i < A.tokens) {
+        const void* p = kind == 0 ? A.q : kind == 1 ? A.k : A.v;
+        const int64_t off = (t0 + i) * (kind == 0 ? A.ldq : kind == 1 ? A.ldk : A.ldv) + hh * D;
+        load_whole(p, off + lo, rx[i]);
+        load_whole(p, off + hi, ry[i]);
+      }
+    }
+    KvRow row[TPW];
+    int page[TPW];
+#pragma unroll
+    for (int i = 0; i < TPW; ++i) {
+      row[i] = t0 + i >= A.tokens ? KvRow{-1, -1, t0 + i + 1} : i ? kv_next(A.b, row[i - 1], t0 + i - 1) : kv_row(A.b, t0);
+      page[i] = nk ? kv_page(A.c, A.b, row[i].seq, row[i].pos) : -1;
+    }
+    uint32_t wx[TPW], wy[TPW], sx[TPW], sy[TPW];
+#pragma unroll
+    for (int i = 0; i < TPW; ++i) {
+      if (row[i].seq < 0) continue;
+      const int64_t t = t0 + i;
+      float x[8], y[8];
+      raw_to_f32(rx[i], x);
+      raw_to_f32(ry[i], y);
+      if (turned && kind < 2) {
+        int64_t at = A.pos ? (int64_t)entries(A.pos)[t] : row[i].pos;
+        at = at < 0 ? 0 : at >= A.angles ? A.angles - 1 : at;
+        const int64_t o = at * (A.rot / 2);
         float cc[8], ss[8];
-        load8(A.cos, o + lo, cc);
-        load8(A.sin, o + lo, ss);
-        raw_to_f32(rx, x);
-        raw_to_f32(ry, y);
+        if (A.interleaved) {                               // 4 angles of the lower elements, 4 of the upper
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = x[i], b = y[i];
-          x[i] = a * cc[i] - b * ss[i];
-          y[i] = b * cc[i] + a * ss[i];
+          for (int k = 0; k < 2; ++k) {
+            const float4 c4 = *reinterpret_cast<const float4*>(A.cos + o + (k ? hi : lo) / 2);
+            const float4 s4 = *reinterpret_cast<const float4*>(A.sin + o + (k ? hi : lo) / 2);
+            cc[4 * k] = c4.x, cc[4 * k + 1] = c4.y, cc[4 * k + 2] = c4.z, cc[4 * k + 3] = c4.w;
+            ss[4 * k] = s4.x, ss[4 * k + 1] = s4.y, ss[4 * k + 2] = s4.z, ss[4 * k + 3] = s4.w;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float a = x[2 * k], b = x[2 * k + 1], p = y[2 * k], q = y[2 * k + 1];
+            x[2 * k] = a * cc[k] - b * ss[k];
+            x[2 * k + 1] = b * cc[k] + a * ss[k];
+            y[2 * k] = p * cc[4 + k] - q * ss[4 + k];
+            y[2 * k + 1] = q * cc[4 + k] + p * ss[4 + k];
+          }
+        } else {
+          load8(A.cos, o + lo, cc);
+          load8(A.sin, o + lo, ss);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float a = x[k], b = y[k];
+            x[k] = a * cc[k] - b * ss[k];
+            y[k] = b * cc[k] + a * ss[k];
+          }
         }
       }
-    } else {
-      raw_to_f32(rx, x);
-      raw_to_f32(ry, y);
-    }
-    if (kind == 0) {
-      store_whole(A.q_out, false, t * A.ldqo + hh * D + lo, x);
-      store_whole(A.q_out, false, t * A.ldqo + hh * D + hi, y);
-    }
-    if (page < 0) continue;
-    // every lane takes part in its block's maximum
-    uint32_t wx, wy, sx, sy;
-    const int e = kind == 2 ? ev : ek;
-    encode8<FMT>(x, e, &wx, &sx);
-    encode8<FMT>(y, e, &wy, &sy);
-    if (kind != 1 && kind != 2) continue;
-    const int at = (int)(row.pos & ((1 << A.c.shift) - 1));
-    const bool first = lo % At::BLK == 0;                  // of its block's lanes
-    if (kind == 1) {
-      const int64_t g = kv_slot(A.c, page, hh, at & ~15);
-      uint8_t* pc = A.c.kc + g * (D / 2);
-      *reinterpret_cast<uint32_t*>(pc + At::k_code(at, lo)) = wx;
-      *reinterpret_cast<uint32_t*>(pc + At::k_code(at, hi)) = wy;
-      uint8_t* ps = A.c.ks + g * (D / At::BLK);
-      if (first) {
-        ps[At::k_scale(at, lo)] = (uint8_t)sx;
-        ps[At::k_scale(at, hi)] = (uint8_t)sy;
+      if (kind == 0) {
+        store_whole(A.q_out, false, t * A.ldqo + hh * D + lo, x);
+        store_whole(A.q_out, false, t * A.ldqo + hh * D + hi, y);
       }
-    } else {
-      const int64_t g = kv_slot(A.c, page, hh, at & ~3);
+      if (page[i] < 0) continue;
+      // every lane takes part in its block's maximum
+      const int e = kind == 2 ? ev : ek;
+      encode8<FMT>(x, e, &wx[i], &sx[i]);
+      encode8<FMT>(y, e, &wy[i], &sy[i]);
+      if (kind == 1) {
+        const int at = (int)(row[i].pos & ((1 << A.c.shift) - 1));
+        const int64_t g = kv_slot(A.c, page[i], hh, at & ~15);
+        uint8_t* pc = A.c.kc + g * (D / 2);
+        *reinterpret_cast<uint32_t*>(pc + At::k_code(at, lo)) = wx[i];
+        *reinterpret_cast<uint32_t*>(pc + At::k_code(at, hi)) = wy[i];
+        uint8_t* ps = A.c.ks + g * (D / At::BLK);
+        if (first) {
+          ps[At::k_scale(at, lo)] = (uint8_t)sx[i];
+          ps[At::k_scale(at, hi)] = (uint8_t)sy[i];
+        }
+      }
+    }
+    // values: four tokens that share their 16 bytes, or each for itself
+    bool four = TPW == 4 && page[0] >= 0 && (row[0].pos & 3) == 0;
+#pragma unroll
+    for (int i = 1; i < TPW; ++i) four = four && row[i].seq == row[0].seq && page[i] == page[0];
+    if (kind != 2) continue;
+    if constexpr (TPW == 4) {
+      if (four) {
+        const int at = (int)(row[0].pos & ((1 << A.c.shift) - 1));
+        const int64_t g = kv_slot(A.c, page[0], hh, at);
+        uint8_t* pc = A.c.vc + g * (D / 2);
+        if constexpr (At::V == 4) {
+          *reinterpret_cast<u32x4_t*>(pc + At::v_code(0, lo)) = u32x4_t{wx[0], wx[1], wx[2], wx[3]};
+          *reinterpret_cast<u32x4_t*>(pc + At::v_code(0, hi)) = u32x4_t{wy[0], wy[1], wy[2], wy[3]};
+        } else {                                           // 2 bytes a token: dimensions lo .. lo + 3, then the next
+          auto low = [](uint32_t a, uint32_t b) { return (a & 0xFFFFu) | (b << 16); };
+          auto high = [](uint32_t a, uint32_t b) { return (a >> 16) | (b & 0xFFFF0000u); };
+          *reinterpret_cast<u32x4_t*>(pc + At::v_code(0, lo)) =
+              u32x4_t{low(wx[0], wx[1]), low(wx[2], wx[3]), high(wx[0], wx[1]), high(wx[2], wx[3])};
+          *reinterpret_cast<u32x4_t*>(pc + At::v_code(0, hi)) =
+              u32x4_t{low(wy[0], wy[1]), low(wy[2], wy[3]), high(wy[0], wy[1]), high(wy[2], wy[3])};
+        }
+        uint8_t* ps = A.c.vs + g * (D / At::BLK);
+        if (first) {
+          *reinterpret_cast<uint32_t*>(ps + At::v_scale(0, lo)) = sx[0] | sx[1] << 8 | sx[2] << 16 | sx[3] << 24;
+          *reinterpret_cast<uint32_t*>(ps + At::v_scale(0, hi)) = sy[0] | sy[1] << 8 | sy[2] << 16 | sy[3] << 24;
+        }
+        continue;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < TPW; ++i) {
+      if (page[i] < 0) continue;
+      const int at = (int)(row[i].pos & ((1 << A.c.shift) - 1));
+      const int64_t g = kv_slot(A.c, page[i], hh, at & ~3);
       uint8_t* pc = A.c.vc + g * (D / 2);
       if constexpr (At::V == 4) {
-        *reinterpret_cast<uint32_t*>(pc + At::v_code(at, lo)) = wx;
-        *reinterpret_cast<uint32_t*>(pc + At::v_code(at, hi)) = wy;
+        *reinterpret_cast<uint32_t*>(pc + At::v_code(at, lo)) = wx[i];
+        *reinterpret_cast<uint32_t*>(pc + At::v_code(at, hi)) = wy[i];
       } else {
-        *reinterpret_cast<uint16_t*>(pc + At::v_code(at, lo)) = (uint16_t)wx;
-        *reinterpret_cast<uint16_t*>(pc + At::v_code(at, lo + 4)) = (uint16_t)(wx >> 16);
-        *reinterpret_cast<uint16_t*>(pc + At::v_code(at, hi)) = (uint16_t)wy;
-        *reinterpret_cast<uint16_t*>(pc + At::v_code(at, hi + 4)) = (uint16_t)(wy >> 16);
+        *reinterpret_cast<uint16_t*>(pc + At::v_code(at, lo)) = (uint16_t)wx[i];
+        *reinterpret_cast<uint16_t*>(pc + At::v_code(at, lo + 4)) = (uint16_t)(wx[i] >> 16);
+        *reinterpret_cast<uint16_t*>(pc + At::v_code(at, hi)) = (uint16_t)wy[i];
+        *reinterpret_cast<uint16_t*>(pc + At::v_code(at, hi + 4)) = (uint16_t)(wy[i] >> 16);
       }
       uint8_t* ps = A.c.vs + g * (D / At::BLK);
       if (first) {
-        ps[At::v_scale(at, lo)] = (uint8_t)sx;
-        ps[At::v_scale(at, hi)] = (uint8_t)sy;
+        ps[At::v_scale(at, lo)] = (uint8_t)sx[i];
+        ps[At::v_scale(at, hi)] = (uint8_t)sy[i];
       }
     }
   }
@@ -251,12 +303,19 @@ hipError_t dispatch(int format, int dim, Fn fn) {
 hipError_t launch_kv_append(int format, int dim, const KvAppend& a, hipStream_t s) {
   return dispatch(format, dim, [&](auto f, auto d) {
     constexpr int D = decltype(d)::value;
-    const int heads = (a.q ? a.q_heads : 0) + (a.k ? 2 * a.c.heads : 0);
-    const unsigned grid = (unsigned)grid_of(a.tokens, heads, 1024 / D);
+    const int heads = (a.q ? a.q_heads : 0) + (a.k ? 2 * a.c.heads : 0), hpw = 1024 / D;
+    auto go = [&](auto f32) {
+      constexpr bool F32 = decltype(f32)::value;
+      const int64_t wg = grid_of(a.tokens, heads, hpw);
+      if (a.b.cu && wg >= kLong)
+        kv_append_kernel<decltype(f)::value, D, F32, 4><<<(unsigned)grid_of((a.tokens + 15) / 16 * 4, heads, hpw), 64 * kWaves, 0, s>>>(a);
+      else
+        kv_append_kernel<decltype(f)::value, D, F32, 1><<<(unsigned)wg, 64 * kWaves, 0, s>>>(a);
+    };
     if (a.type == SNIPOP_F32)
-      kv_append_kernel<decltype(f)::value, D, true><<<grid, 64 * kWaves, 0, s>>>(a);
+      go(std::true_type{});
     else
-      kv_append_kernel<decltype(f)::value, D, false><<<grid, 64 * kWaves, 0, s>>>(a);
+      go(std::false_type{});
     return hipGetLastError();
   });
 }
@@ -266,7 +325,7 @@ hipError_t launch_kv_gather(int format, int dim, const KvGather& a, hipStream_t 
     constexpr int D = decltype(d)::value;
     const int heads = (a.k ? a.c.heads : 0) + (a.v ? a.c.heads : 0);
     const int64_t wg = grid_of(a.tokens, heads, 512 / D);
-    if (a.b.cu && wg >= 8192)                              // more waves than are resident, four times over
+    if (a.b.cu && wg >= kLong)
       kv_gather_kernel<decltype(f)::value, D, 4><<<(unsigned)grid_of((a.tokens + 3) / 4, heads, 512 / D), 64 * kWaves, 0, s>>>(a);
     else
       kv_gather_kernel<decltype(f)::value, D, 1><<<(unsigned)wg, 64 * kWaves, 0, s>>>(a);
