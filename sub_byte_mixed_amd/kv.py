@@ -133,10 +133,13 @@ class KVBatch:
         self.ref = ctypes.byref(self._desc)
 
 
+_CPU = -1                      # get_device() of a CPU tensor
+
+
 def _place(cache: KVCache, batch: KVBatch, fn) -> int:
     """The GPU that a call's cache and sequences lie on."""
     dev = cache.device
-    if batch.device != dev:
+    if batch.device != dev or dev == _CPU:
         raise ValueError(f"the cache and the batch of {fn.__name__} must lie on one GPU, got {dev} and {batch.device}")
     return dev
 
@@ -178,7 +181,7 @@ def kv_append(k: Optional[torch.Tensor], v: Optional[torch.Tensor], cache: KVCac
     first = q if k is None else k
     if first is None or (k is None) != (v is None):
         raise ValueError("k and v are given together, or q alone")
-    dtype = first.dtype
+    dtype = getattr(first, "dtype", None)
     ty = _TYPES.get(dtype)
     if ty is None:
         raise ValueError(f"q, k and v must be bfloat16 or float32, got {dtype}")

@@ -38,16 +38,18 @@ def scale_views(cache):
 class Paged:
     """Sequences of `lens` tokens, the last new[b] of them this call's, in
     shuffled pages of a cache that is NaN wherever no token lies. unmapped: the
-    (sequence, page index) pairs whose table entry names no page."""
+    (sequence, page index) pairs whose table entry names no page. capacity:
+    tokens that the table has room for at least: above 1280 the steps of a call
+    are shared among workgroups and joined by a second launch."""
 
-    def __init__(self, fmt, dim, heads, page, lens, new, seed=0, unmapped=(), one_each=False, spare=3):
+    def __init__(self, fmt, dim, heads, page, lens, new, seed=0, unmapped=(), one_each=False, spare=3, capacity=0):
         self.fmt, self.dim, self.heads, self.page, self.lens, self.new = fmt, dim, heads, page, list(lens), list(new)
         g = torch.Generator().manual_seed(seed + 1)
         each = [max(0, -(-n // page)) for n in lens]
         pages = sum(each) + spare
         self.cache = make_cache(fmt, pages, page, heads, dim, seed)
         order = torch.randperm(pages, generator=g).tolist()
-        wide = max(each + [1])
+        wide = max(each + [1, -(-capacity // page)])
         table = np.full((len(lens), wide + 2), -1, np.int32)
         at = 0
         for b, n in enumerate(each):
@@ -83,22 +85,25 @@ class Paged:
     def positions(self, b):
         return self.lens[b] - self.new[b] + np.arange(self.new[b])
 
-    def stored(self, b):
-        """Codes and scales of sequence b's tokens, token-major: k, k scales, v, v scales [heads, tokens, ...];
-        what is not mapped reads as zeros."""
+    def views(self):
+        """The cache's bytes, token-major: k, k scales, v, v scales [pages, heads, tokens, ...]."""
         c = self.cache
+        return [tokens_view(t, keys) for t, keys in ((c.k_codes, True), (c.k_scales, True), (c.v_codes, False), (c.v_scales, False))]
+
+    def stored(self, b, views):
+        """Of sequence b's tokens [heads, tokens, ...]; what is not mapped reads as zeros."""
         n, ok = max(self.lens[b], 0), self.mapped(b)
         at = np.arange(n)
         p = np.where(ok, self.table[b][at // self.page] if n else 0, 0)
         out = []
-        for t, keys in ((c.k_codes, True), (c.k_scales, True), (c.v_codes, False), (c.v_scales, False)):
-            x = tokens_view(t, keys)[p, :, at % self.page].copy()
+        for x in views:
+            x = x[p, :, at % self.page].copy()
             x[~ok] = 0
             out.append(x.transpose(1, 0, 2))
         return out
 
-    def values(self, b):
-        k, ks, v, vs = self.stored(b)
+    def values(self, b, views=None):
+        k, ks, v, vs = self.stored(b, views or self.views())
         e = TEXP if self.fmt == S.NVFP4 else (0, 0)
         return OK.values(self.fmt, k, ks, e[0]), OK.values(self.fmt, v, vs, e[1])
 
@@ -109,9 +114,10 @@ class Paged:
         q = f64(q).reshape(q.shape[0], heads, -1, dim)
         out, lse = np.zeros(q.shape), np.full(q.shape[:3], -np.inf)
         tol_o, tol_l = np.zeros(q.shape), np.zeros(q.shape[:3])
+        views = self.views()
         for b in range(len(self.lens)):
             r = slice(self.cu[b], self.cu[b + 1])
-            k, v = self.values(b)
+            k, v = self.values(b, views)
             for h in range(heads):
                 o, z, a, size, keys = OK.attention(q[r, h], k[h], v[h], self.positions(b), self.mapped(b), scale, window)
                 out[r, h], lse[r, h] = o, z

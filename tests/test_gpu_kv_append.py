@@ -205,3 +205,53 @@ def test_many_sequences_and_tokens():
     S.kv_append(k.cuda(), v.cuda(), P.cache, P.batch)
     _, enc = expected(P, None, k, v, None, None, False)
     check_cache(P, before, enc)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim,dtype", [(64, BF), (64, F32), (128, F32), (128, BF), (256, F32)])
+def test_long_calls(fmt, dim, dtype):
+    """Calls of many waves, which take four tokens each, against the same tokens in short calls: sequences that
+    begin and end anywhere, positions that are not multiples of four, pages that are not mapped, rows of nobody."""
+    heads, hq, page = 8192 // dim, 16384 // dim, 16
+    lens, new = [700, 1203, 7, 66, 2, 0, 301, 33], [700, 1001, 5, 66, 1, 0, 298, 30]
+    say("append long", fmt, dim, dtype)
+    P = Paged(fmt, dim, heads, page, lens, new, seed=dim, unmapped=[(0, 3), (1, 20), (1, 21), (3, 0)])
+    rows = P.rows + 13
+    q, k, v = (rand((rows, h * dim), dtype, i).cuda() for i, h in enumerate((hq, heads, heads)))
+    cos, sin = (t.cuda() for t in angles(1300, 64))
+    start = snapshot(P.cache)
+    out = Guarded(rows, hq * dim, BF)
+    S.kv_append(k, v, P.cache, P.batch, q=q, cos=cos, sin=sin, interleaved=dim == 64, q_out=out.t)
+    got = snapshot(P.cache)
+    gathered = [torch.full((rows, heads * dim), 7.0, dtype=BF, device="cuda") for _ in range(2)]
+    S.kv_gather(P.cache, P.batch, k=gathered[0], v=gathered[1])
+    for t, old in zip((P.cache.k_codes, P.cache.k_scales, P.cache.v_codes, P.cache.v_scales), start):
+        t.copy_(old)
+    want, parts = torch.full_like(out.t, 7.0), [torch.full_like(gathered[0], 7.0) for _ in range(2)]
+    for b in range(len(lens)):
+        for a in range(0, new[b], 150):
+            n = min(150, new[b] - a)
+            r = slice(int(P.cu[b]) + a, int(P.cu[b]) + a + n)
+            batch = S.KVBatch(P.batch.table[b:b + 1], torch.tensor([lens[b] - new[b] + a + n], dtype=torch.int32, device="cuda"),
+                              torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+            want[r] = S.kv_append(k[r], v[r], P.cache, batch, q=q[r], cos=cos, sin=sin, interleaved=dim == 64)
+            for t, p in zip(S.kv_gather(P.cache, batch, n), parts):
+                p[r] = t
+    assert torch.equal(out.t, want) and out.intact()
+    assert all(torch.equal(a, b) for a, b in zip(got, snapshot(P.cache)))
+    assert all(torch.equal(a, b) for a, b in zip(gathered, parts))
+
+
+def test_other_stream():
+    P = Paged(S.NVFP4, 64, 2, 16, [40], [40])
+    k, v, q = (rand((40, 128), BF, i).cuda() for i in range(3))
+    want = S.kv_append(k, v, P.cache, P.batch, q=q)
+    stored = S.kv_gather(P.cache, P.batch, 40)
+    s = torch.cuda.Stream()
+    for t in (P.cache.k_codes, P.cache.v_codes):
+        t.zero_()
+    torch.cuda.synchronize()
+    got = S.kv_append(k, v, P.cache, P.batch, q=q, stream=s)
+    again = S.kv_gather(P.cache, P.batch, 40, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and all(torch.equal(a, b) for a, b in zip(again, stored))

@@ -11,6 +11,7 @@ from ops_common import BF, F32, Guarded, f64, rand, say, strided
 
 pytestmark = pytest.mark.gpu
 FORMATS = [S.NVFP4, S.MXFP4]
+CAPACITIES = [0, 5000]                                 # a workgroup a unit; steps shared among workgroups
 
 
 def run(P, group, window=0, scale=None, seed=0, qscale=0.5):
@@ -25,41 +26,47 @@ def run(P, group, window=0, scale=None, seed=0, qscale=0.5):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("group", [1, 3, 8, 17])
-def test_single_tokens(fmt, dim, group):
+@pytest.mark.parametrize("capacity", CAPACITIES)
+def test_single_tokens(fmt, dim, group, capacity):
     """Lengths around 16, 32, a page and the waves' steps; zero tokens too."""
-    say("attn", fmt, dim, group)
+    say("attn", fmt, dim, group, capacity)
     lens = [1, 2, 15, 16, 17, 31, 32, 33, 64, 65, 127, 128, 129, 200, 0, 300]
-    run(Paged(fmt, dim, 2, 16, lens, [1] * len(lens), seed=group, one_each=True), group)
+    run(Paged(fmt, dim, 2, 16, lens, [1] * len(lens), seed=group, one_each=True, capacity=capacity), group)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("page", [16, 32, 64, 256])
-def test_pages(fmt, page):
-    say("attn pages", fmt, page)
-    run(Paged(fmt, 128, 1, page, [page - 1, page, page + 1, 3 * page + 7], [1] * 4, seed=page, one_each=True), 4)
+@pytest.mark.parametrize("page", [16, 32, 64, 256, 4096])
+@pytest.mark.parametrize("capacity", CAPACITIES)
+def test_pages(fmt, page, capacity):
+    say("attn pages", fmt, page, capacity)
+    run(Paged(fmt, 128, 1, page, [page - 1, page, page + 1, 3 * page + 7], [1] * 4, seed=page, one_each=True, capacity=capacity), 4)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("group", [1, 4, 7])
-def test_prompts_and_tokens(fmt, dim, group):
+@pytest.mark.parametrize("capacity", CAPACITIES)
+def test_prompts_and_tokens(fmt, dim, group, capacity):
     """Whole prompts, chunks after others, drafted tokens, single tokens, no token, in one call."""
-    say("attn prompts", fmt, dim, group)
+    say("attn prompts", fmt, dim, group, capacity)
     lens, new = [45, 100, 67, 300, 1, 50, 161], [45, 37, 1, 4, 1, 0, 130]
-    run(Paged(fmt, dim, 2, 32, lens, new, seed=dim + group), group)
+    run(Paged(fmt, dim, 2, 32, lens, new, seed=dim + group, capacity=capacity), group)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("window", [1, 2, 16, 31, 32, 100, 2 ** 31 - 1, 2 ** 40])
-def test_windows(fmt, window):
-    say("attn window", fmt, window)
-    run(Paged(fmt, 64, 2, 16, [5, 200, 333], [5, 70, 1], seed=1), 2, window=window)
+@pytest.mark.parametrize("capacity", CAPACITIES)
+def test_windows(fmt, window, capacity):
+    say("attn window", fmt, window, capacity)
+    run(Paged(fmt, 64, 2, 16, [5, 200, 333], [5, 70, 1], seed=1, capacity=capacity), 2, window=window)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-def test_pages_that_are_not_mapped(fmt):
+@pytest.mark.parametrize("capacity", CAPACITIES)
+def test_pages_that_are_not_mapped(fmt, capacity):
     """Their keys take no part; a row that has none left is zero with lse -inf."""
-    P = Paged(fmt, 128, 2, 16, [64, 40, 16, 90], [3, 40, 1, 1], seed=2, unmapped=[(0, 0), (0, 2), (1, 0), (2, 0), (3, 5), (3, 1)])
+    P = Paged(fmt, 128, 2, 16, [64, 40, 16, 90], [3, 40, 1, 1], seed=2, unmapped=[(0, 0), (0, 2), (1, 0), (2, 0), (3, 5), (3, 1)],
+              capacity=capacity)
     q, out, lse = run(P, 4)
     r = slice(P.cu[1], P.cu[1] + 16)                   # the first page of sequence 1 is all that these see
     assert not out[r].any() and bool((lse[r] == -float("inf")).all())
@@ -67,15 +74,17 @@ def test_pages_that_are_not_mapped(fmt):
     run(P, 4, window=20)
 
 
-def test_more_new_tokens_than_the_sequence_has():
+@pytest.mark.parametrize("capacity", CAPACITIES)
+def test_more_new_tokens_than_the_sequence_has(capacity):
     """Rows at negative positions see nothing."""
-    P = Paged(S.NVFP4, 64, 1, 16, [5, -3, 0], [9, 2, 4], seed=4)
+    P = Paged(S.NVFP4, 64, 1, 16, [5, -3, 0], [9, 2, 4], seed=4, capacity=capacity)
     q, out, lse = run(P, 2)
     assert not out[:4].any() and not out[9:].any() and bool((lse[9:] == -float("inf")).all())
 
 
-def test_rows_of_nobody_and_strides():
-    P = Paged(S.NVFP4, 128, 2, 16, [33, 80], [33, 2], seed=5)
+@pytest.mark.parametrize("capacity", CAPACITIES)
+def test_rows_of_nobody_and_strides(capacity):
+    P = Paged(S.NVFP4, 128, 2, 16, [33, 80], [33, 2], seed=5, capacity=capacity)
     q = rand((P.rows + 9, 2 * 2 * 128), BF, 1)
     out = Guarded(P.rows + 9, 512, BF)
     lse = torch.full((P.rows + 9, 4), 7.0, device="cuda")
@@ -84,8 +93,9 @@ def test_rows_of_nobody_and_strides():
     assert out.intact() and bool((out.t[P.rows:] == 7.0).all()) and bool((lse[P.rows:] == 7.0).all())
 
 
-def test_in_place():
-    P = Paged(S.MXFP4, 128, 2, 16, [333, 80], [5, 40], seed=6)
+@pytest.mark.parametrize("capacity", CAPACITIES)
+def test_in_place(capacity):
+    P = Paged(S.MXFP4, 128, 2, 16, [333, 80], [5, 40], seed=6, capacity=capacity)
     q = rand((P.rows, 512), BF, 1)
     d = q.cuda()
     S.kv_attn(d, P.cache, P.batch, out=d)
@@ -101,9 +111,10 @@ def test_sizes_of_scores(fmt, qscale, scale):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-def test_rising_scores(fmt):
+@pytest.mark.parametrize("capacity", CAPACITIES)
+def test_rising_scores(fmt, capacity):
     """Keys whose scores grow along the sequence: the running maximum moves in every tile."""
-    P = Paged(fmt, 64, 1, 32, [700], [40], seed=8)
+    P = Paged(fmt, 64, 1, 32, [700], [40], seed=8, capacity=capacity)
     ramp = torch.arange(700) // 90
     base = 0x20 if fmt == S.NVFP4 else 118
     step = 8 if fmt == S.NVFP4 else 1                  # a power of two
@@ -123,10 +134,41 @@ def test_a_key_of_nan_reaches_the_rows_that_see_it():
     assert not out[:20].isnan().any() and not lse[:20].isnan().any()
 
 
-def test_a_long_sequence():
-    """One token over 40000; and many waves' partial sums."""
-    P = Paged(S.NVFP4, 64, 1, 64, [40000], [1], seed=10, one_each=True)
-    run(P, 2)
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim,heads,lens,new", [
+    (64, 1, [40000], [1]),                             # hundreds of parts to a unit
+    (128, 2, [9000, 1500, 1, 3000], [1, 1, 1, 1]),
+    (256, 1, [5000, 7000], [1, 1]),
+    (128, 1, [6000, 2000, 50], [7, 1, 3]),             # two row tiles
+    (64, 3, [3001, 1700], [5, 2]),
+])
+def test_long_sequences(fmt, dim, heads, lens, new):
+    """Many steps to a workgroup, and parts of a unit in many workgroups."""
+    say("attn long", fmt, dim, heads, lens)
+    P = Paged(fmt, dim, heads, 64, lens, new, seed=10, one_each=max(new) == 1)
+    run(P, 8)
+    run(P, 5, window=2222)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_a_cache_larger_than_the_last_level_cache(dim):
+    """Its keys are read past that cache."""
+    page, heads = 256, 2
+    P = Paged(S.NVFP4, dim, heads, page, [3000, 1400], [1, 1], seed=11, one_each=True,
+              spare=(130 << 20) // (page * heads * (dim + dim // 8)))
+    run(P, 4)
+    P = Paged(S.NVFP4, dim, heads, page, [3000, 1400], [6, 1], seed=11, spare=(130 << 20) // (page * heads * (dim + dim // 8)))
+    run(P, 4)
+
+
+@pytest.mark.parametrize("seqs", [65, 700, 5000])
+@pytest.mark.parametrize("capacity", CAPACITIES)
+def test_many_sequences(seqs, capacity):
+    """More than a wave looks up at once, some without tokens, some without new ones."""
+    say("attn sequences", seqs, capacity)
+    lens = [(37 * b) % 60 for b in range(seqs)]
+    run(Paged(S.NVFP4, 64, 1, 16, lens, [1] * seqs, seed=seqs, one_each=True, capacity=capacity), 2)
+    run(Paged(S.NVFP4, 64, 1, 16, lens, [min(n, (7 * b) % 3) for b, n in enumerate(lens)], seed=seqs, capacity=capacity), 2)
 
 
 def test_offsets_past_32_bits():
@@ -150,3 +192,29 @@ def test_offsets_past_32_bits():
     got, _ = S.kv_attn(q, cache, S.KVBatch(table, lens, cu))
     assert torch.equal(got, want) and bool(want.any())
     assert all(torch.equal(a, b) for a, b in zip(S.kv_gather(cache, S.KVBatch(table, lens, cu), n), S.kv_gather(small, low, n)))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("capacity", CAPACITIES)
+def test_what_the_workspace_holds(dim, capacity):
+    P = Paged(S.NVFP4, dim, 1, 16, [700, 40], [9, 1], seed=12, capacity=capacity)
+    q = rand((P.rows, 4 * dim), BF, 1).cuda()
+    want, _ = S.kv_attn(q, P.cache, P.batch)
+    ws = torch.empty(S.lib().snipkv_attn_workspace(P.rows, 2, 4, 1, dim) + 256, dtype=torch.uint8, device="cuda")
+    for fill in (0, 255, 127):
+        ws.fill_(fill)
+        got, _ = S.kv_attn(q, P.cache, P.batch, ws=ws[:-256])
+        assert torch.equal(got, want) and bool((ws[-256:] == fill).all())
+
+
+def test_two_calls_at_once():
+    """On two streams, each with its own workspace."""
+    P = Paged(S.NVFP4, 128, 2, 16, [5000, 3000], [1, 1], seed=13, one_each=True)
+    q = [rand((2, 8 * 128), BF, i).cuda() for i in range(2)]
+    want = [S.kv_attn(t, P.cache, P.batch)[0] for t in q]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [S.kv_attn(t, P.cache, P.batch, stream=s)[0] for t, s in zip(q, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
