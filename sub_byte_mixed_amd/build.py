@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libsnip.so")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 SOURCES = ["api.hip", "quantize.hip", "quantize_dual.hip", "quantize_fp4v.hip", "gemm.hip", "gemm_staged.hip",
            "ops_api.hip", "rmsnorm.hip", "swiglu.hip", "qgemv.hip",
-           "kv_api.hip", "kv_append.hip", "kv_attn.hip"]
+           "kv_api.hip", "kv_append.hip", "kv_attn.hip", "kv_prompt.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",

@@ -66,13 +66,28 @@ constexpr int kv_scale_piece(int dim, int block) {
   return 2 * kv_key_piece(dim) / block ? 2 * kv_key_piece(dim) / block : 1;
 }
 
-// Row tiles of an attention call, of every kv head.
-int64_t kv_attn_tiles(int64_t tokens, int64_t seqs, int64_t group);
+// The launches of an attention call: prompts, few rows, and the joining of what
+// the latter split.
+struct KvPlan {
+  bool prompt, few, join;
+  bool two, wide, past;        // few rows: two row tiles; eight waves; read past the last-level cache
+  unsigned prompt_wg, few_wg;  // workgroups
+  int join_rows;
+};
 
+// Rows of a workgroup in the launch for prompts.
+constexpr int kv_prompt_rows(int dim) { return dim == 256 ? 64 : 128; }
+
+// Tiles of 16 rows of a call, a kv head's, at most; workspace bytes.
+int64_t kv_attn_tiles(int64_t tokens, int64_t seqs, int64_t group);
 size_t kv_attn_slots(int dim);
+// Fills in what of `a` the plan decides (few, split, step, left).
+KvPlan kv_attn_plan(int format, int dim, KvAttn* a);
 
 hipError_t launch_kv_append(int format, int dim, const KvAppend& a, hipStream_t s);
 hipError_t launch_kv_gather(int format, int dim, const KvGather& a, hipStream_t s);
-hipError_t launch_kv_attn(int format, int dim, KvAttn a, hipStream_t s);
+hipError_t launch_kv_prompt(int format, int dim, const KvPlan& p, const KvAttn& a, hipStream_t s);
+hipError_t launch_kv_few(int format, int dim, const KvPlan& p, const KvAttn& a, hipStream_t s);
+hipError_t launch_kv_join(int format, int dim, const KvPlan& p, const KvAttn& a, hipStream_t s);
 
 }  // namespace snip

@@ -207,12 +207,17 @@ int snipkv_attn(const void* q, int64_t ldq, int64_t q_heads, int64_t tokens, con
   a.group = (int32_t)(q_heads / cache->kv_heads);
   a.window = window < kMaxLen ? (int32_t)window : 0;    // no position is further back
   a.scale = (float)((double)scale * 1.4426950408889634);
+  const KvPlan p = kv_attn_plan(cache->format, cache->head_dim, &a);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const double work = 4.0 * (double)tokens * (double)cols;
-  const int slot = timing_begin(LaunchTag{SNIPKV_LAUNCH_ATTN, cache->format, -1, -1, work}, s);
-  const hipError_t e = launch_kv_attn(cache->format, cache->head_dim, a, s);
-  timing_end(slot, s);
-  if ((rc = hip_check(e, "kv attention launch"))) return rc;
+  auto timed = [&](int kind, hipError_t (*launch)(int, int, const KvPlan&, const KvAttn&, hipStream_t)) {
+    const int slot = timing_begin(LaunchTag{kind, cache->format, -1, -1, 4.0 * (double)tokens * (double)cols}, s);
+    const hipError_t e = launch(cache->format, cache->head_dim, p, a, s);
+    timing_end(slot, s);
+    return hip_check(e, "kv attention launch");
+  };
+  if (p.prompt && (rc = timed(SNIPKV_LAUNCH_ATTN, launch_kv_prompt))) return rc;
+  if (p.few && (rc = timed(SNIPKV_LAUNCH_ATTN, launch_kv_few))) return rc;
+  if (p.join && (rc = timed(SNIPKV_LAUNCH_JOIN, launch_kv_join))) return rc;
   return ok();
 }
 

@@ -286,22 +286,10 @@ int64_t grid_of(int64_t tokens, int heads, int heads_per_wave) {
   return wg < kMaxWG ? wg : kMaxWG;
 }
 
-// fn(format, head_dim) of the pair at run time.
-template <typename Fn>
-hipError_t dispatch(int format, int dim, Fn fn) {
-  auto of = [&](auto f) {
-    return dim == 64    ? fn(f, std::integral_constant<int, 64>{})
-           : dim == 128 ? fn(f, std::integral_constant<int, 128>{})
-                        : fn(f, std::integral_constant<int, 256>{});
-  };
-  return format == SNIP_NVFP4 ? of(std::integral_constant<int, SNIP_NVFP4>{})
-                              : of(std::integral_constant<int, SNIP_MXFP4>{});
-}
-
 }  // namespace
 
 hipError_t launch_kv_append(int format, int dim, const KvAppend& a, hipStream_t s) {
-  return dispatch(format, dim, [&](auto f, auto d) {
+  return kv_dispatch(format, dim, [&](auto f, auto d) {
     constexpr int D = decltype(d)::value;
     const int heads = (a.q ? a.q_heads : 0) + (a.k ? 2 * a.c.heads : 0), hpw = 1024 / D;
     auto go = [&](auto f32) {
@@ -321,7 +309,7 @@ hipError_t launch_kv_append(int format, int dim, const KvAppend& a, hipStream_t 
 }
 
 hipError_t launch_kv_gather(int format, int dim, const KvGather& a, hipStream_t s) {
-  return dispatch(format, dim, [&](auto f, auto d) {
+  return kv_dispatch(format, dim, [&](auto f, auto d) {
     constexpr int D = decltype(d)::value;
     const int heads = (a.k ? a.c.heads : 0) + (a.v ? a.c.heads : 0);
     const int64_t wg = grid_of(a.tokens, heads, 512 / D);

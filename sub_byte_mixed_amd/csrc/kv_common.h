@@ -31,6 +31,17 @@ __device__ __forceinline__ int kv_find(int n, int64_t x, F f) {
   return __builtin_amdgcn_readfirstlane(lo) - 1;
 }
 
+// fn(format, head_dim) of the pair at run time.
+template <typename Fn>
+hipError_t kv_dispatch(int format, int dim, Fn fn) {
+  auto of = [&](auto f) {
+    return dim == 64    ? fn(f, std::integral_constant<int, 64>{})
+           : dim == 128 ? fn(f, std::integral_constant<int, 128>{})
+                        : fn(f, std::integral_constant<int, 256>{});
+  };
+  return format == SNIP_NVFP4 ? of(std::integral_constant<int, SNIP_NVFP4>{}) : of(std::integral_constant<int, SNIP_MXFP4>{});
+}
+
 struct KvRow {
   int seq;                     // < 0: nobody's
   int64_t pos, end;            // position; the sequence's last row and one
