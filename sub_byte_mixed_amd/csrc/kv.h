@@ -71,6 +71,7 @@ constexpr int kv_scale_piece(int dim, int block) {
 struct KvPlan {
   bool prompt, few, join;
   bool two, wide, past;        // few rows: two row tiles; eight waves; read past the last-level cache
+  int prompt_waves;            // of a workgroup for prompts
   unsigned prompt_wg, few_wg;  // workgroups
   int join_rows;
 };

@@ -543,7 +543,9 @@ KvPlan kv_attn_plan(int format, int dim, KvAttn* a) {
   // 8192, 64 heads over 8: 128 units).
   const int64_t mean = a->tokens * a->group / b.seqs;
   const int unit = kv_prompt_rows(dim);
-  p.prompt = mean >= kFew && a->tokens * a->group / unit * a->c.heads >= 256 && units(unit) < (1 << 24);
+  const int64_t full = a->tokens * a->group / unit * a->c.heads;
+  p.prompt = mean >= kFew && full >= 256 && units(unit) < (1 << 24);
+  p.prompt_waves = dim < 256 && full < 1024 ? 8 : 4;     // measured at kv_prompt_kernel
   p.prompt_wg = p.prompt ? (unsigned)units(unit) : 0;
   a->split = p.prompt && b.seqs > 1;
   a->few = a->split ? kFew : 0;

@@ -1,31 +1,41 @@
 // Attention over a 4-bit key/value cache for sequences with many new tokens,
 // gfx950 (mathematics and operand layouts: kv_tile.h).
 //
-// Many rows a sequence: a workgroup has a unit of 64 NR rows, a wave 16 NR of
-// them, and all keys of the unit. The waves decode 16 of 64 keys each into LDS, in
-// the order of the products' operands, for all of them: a quarter of the decoding
-// a wave, and one barrier for 64 keys, with two buffers.
+// Many rows a sequence: a workgroup has a unit of 128 rows (64 with heads of 256)
+// and all its keys; a wave has 16 NR of the rows. The keys and values are decoded
+// into LDS once for all waves, in the order of the products' operands: a wave
+// decodes the keys or the values of 16 tokens, so that W waves share 8 W tokens
+// and one barrier, with two buffers. Both products' operands are then read from
+// LDS, which binds: a read of 16 bytes a lane feeds NR products (MXFP4's values
+// two each). W = 4 with NR = 2 reads half as much, W = 8 with NR = 1 has twice
+// the waves for a grid that leaves CUs with few. Measured, us, W = 4 and W = 8,
+// one NVFP4 sequence:
+//     tokens = keys, 32 heads of 128    1024: 41, 32   3200: 116, 103   4096: 157, 160   8192: 540, 568
+//     the same, 32 heads of 64          1024: 25, 20   3200: 72, 68     4096: 93, 103    8192: 328, 352
+//     2048 after 4096, 32 heads of 128  210, 184
+// 4096 tokens are 1024 workgroups there, four to a CU: below that, eight waves.
+// Heads of 256 have no LDS for eight waves of 64 rows; with units of 128 rows six
+// sequences of 20 to 400 tokens took 86 us for 69.
 #include "kv_tile.h"
 
 namespace snip {
 
 namespace {
 
+// What a lane holds of 16 tokens' keys, or of their values.
 template <int FMT, int D>
-struct Half {                  // what a lane holds of 16 tokens
+struct Half {
   using G = Geo<FMT, D>;
-  uint32_t k[G::KL][G::KD], ks[G::KL];
-  uint32_t v[G::VL][G::VB], vs[G::VL];
+  static_assert(G::KL == G::VL && G::KD == G::VB && G::PB == 4 * G::VB, "");
+  uint32_t w[G::KL][G::KD], sc[G::KL];
 };
 
-constexpr int prompt_tiles(int dim) { return kv_prompt_rows(dim) / (kRows * kWaves); }   // NR
-constexpr int prompt_halves(int dim) { return dim == 256 ? 2 : 4; }
-
-template <int FMT, int D, int NR>
-__global__ __launch_bounds__(64 * kWaves, D == 64 ? 3 : 2) void kv_prompt_kernel(KvAttn A) {
+template <int FMT, int D, int W>
+__global__ __launch_bounds__(64 * W, D > 64 ? 2 : W == 4 ? 3 : 4) void kv_prompt_kernel(KvAttn A) {
   using G = Geo<FMT, D>;
-  constexpr int KH = prompt_halves(D);                 // halves of 16 keys at a time: a wave's both, or keys or values
-  constexpr int kUnit = kRows * NR * kWaves, kKeys = 16 * KH, KC = G::KL * G::KD;
+  constexpr int kUnit = kv_prompt_rows(D), NR = kUnit / (kRows * W);
+  constexpr int KH = W / 2;                            // halves of 16 keys at a time
+  constexpr int kKeys = 16 * KH, KC = G::KL * G::KD;
   __shared__ u32x4_t keys[2][KH][KC][64];              // [half of 16 keys][32 dimensions][lane]
   __shared__ alignas(16) u32x2_t vals[2][KH / 2][G::DT][64][2];    // [32 keys][tile of 16 dimensions][lane][half]
   const int lane = threadIdx.x & 63, n = lane & 15, c = lane >> 4;
@@ -73,46 +83,63 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 3 : 2) void kv_prompt_kernel
     return g;
   };
   auto mapped = [&](int p) { return (uint32_t)p < (uint32_t)A.c.pages; };
-  const int half = wave % KH;                          // what the wave decodes
-  const bool do_keys = KH == kWaves || wave < KH, do_values = KH == kWaves || wave >= KH;
+  // What the wave decodes, and where a lane's share of it lies: codes in pieces of
+  // 16 bytes (8), scales in a word, from its bit `down` on.
+  const int half = wave % KH;
+  const bool do_keys = wave < KH;
+  uint32_t code_at[G::KL], scale_at[G::KL], down[G::KL];
+#pragma unroll
+  for (int l = 0; l < G::KL; ++l) {
+    const int ks = G::SB == 2 ? (64 * l + lane) * 2 : 2 * G::PB < G::BLK ? c / 2 * 16 + n : 64 * l + lane;
+    code_at[l] = do_keys ? (64 * l + lane) * G::PB : c * 2 * D + (16 * l + n) * 4 * G::VB;
+    scale_at[l] = do_keys ? ks & ~3 : c * 4 * (D / G::BLK) + (16 * l + n) * 2 * G::VB / G::BLK * 4;
+    down[l] = do_keys ? 8 * (ks & 3) : 0;
+  }
+  const uint8_t* const codes = do_keys ? A.c.kc : A.c.vc;
+  const uint8_t* const scales = do_keys ? A.c.ks : A.c.vs;
   auto entry = [&](int key) { return table[(key + 16 * half < last ? key + 16 * half : last) >> A.c.shift]; };
   auto load = [&](int key, int p, Half<FMT, D>& T) {
-    load_half<FMT, D>(A.c, kv_slot(A.c, mapped(p) ? p : 0, head, (key + 16 * half) & ((1 << A.c.shift) - 1)), T.k, T.ks, T.v, T.vs);
+    const int64_t slot = kv_slot(A.c, mapped(p) ? p : 0, head, (key + 16 * half) & ((1 << A.c.shift) - 1));
+#pragma unroll
+    for (int l = 0; l < G::KL; ++l) {
+      load_words<false>(codes + slot * (D / 2) + code_at[l], T.w[l]);
+      T.sc[l] = *reinterpret_cast<const uint32_t*>(scales + slot * (D / G::BLK) + scale_at[l]);
+    }
   };
   auto decode = [&](int key, int buf, int p, Half<FMT, D>& T) {
+    if (do_keys) {
+#pragma unroll
+      for (int l = 0; l < G::KL; ++l) {
+        const uint32_t b = T.sc[l] >> down[l];
+        h2_t sc = {};
+        float e = 0.0f;
+        if constexpr (G::NV)
+          sc = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false);
+        else
+          e = e8m0_val(b & 0xFFu);
+#pragma unroll
+        for (int w = 0; w < G::KD; ++w) {
+          const int i = G::SB == 2 ? w / 2 : 0;        // block of the piece
+          keys[buf][half][l * G::KD + w][lane] = decode_key<FMT>(T.w[l][w], h2_t{sc[i], sc[i]}, e);
+        }
+      }
+      return;
+    }
     const int k0 = key + 16 * half, end = mapped(p) ? last : -1;
     if (k0 < first || k0 + 15 > end) {
       // values of places that no row sees may be anything: their scales are replaced
-    uint32_t keep = 0u;
+      uint32_t keep = 0u;
 #pragma unroll
       for (int j = 0; j < 4; ++j) keep |= ((k0 + 4 * c + j >= first) & (k0 + 4 * c + j <= end)) ? 0xFFu << (8 * j) : 0u;
 #pragma unroll
-      for (int l = 0; l < G::VL; ++l) T.vs[l] &= keep;
+      for (int l = 0; l < G::VL; ++l) T.sc[l] &= keep;
     }
-    if (do_keys) {
-#pragma unroll
-    for (int l = 0; l < G::KL; ++l) {
-      h2_t sc = {};
-      float e = 0.0f;
-      if constexpr (G::NV)
-        sc = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(T.ks[l], 1.0f, false);
-      else
-        e = e8m0_val(T.ks[l]);
-#pragma unroll
-      for (int w = 0; w < G::KD; ++w) {
-        const int b = G::SB == 2 ? w / 2 : 0;
-        keys[buf][half][l * G::KD + w][lane] = decode_key<FMT>(T.k[l][w], h2_t{sc[b], sc[b]}, e);
-      }
-    }
-    }
-    if (do_values) {
 #pragma unroll
     for (int l = 0; l < G::VL; ++l) {
       uint32_t v[2 * G::VB][2];
-      decode_values<FMT, D>(T.v[l], T.vs[l], v);
+      decode_values<FMT, D>(T.w[l], T.sc[l], v);
 #pragma unroll
       for (int d = 0; d < 2 * G::VB; ++d) vals[buf][half / 2][l * 2 * G::VB + d][lane][half % 2] = u32x2_t{v[d][0], v[d][1]};
-    }
     }
   };
   auto use = [&](int key, int buf, const Pages& g) {
@@ -256,8 +283,14 @@ __global__ __launch_bounds__(64 * kWaves, D == 64 ? 3 : 2) void kv_prompt_kernel
 
 hipError_t launch_kv_prompt(int format, int dim, const KvPlan& p, const KvAttn& a, hipStream_t s) {
   auto go = [&](auto f, auto d) {
-    constexpr int D = decltype(d)::value;
-    kv_prompt_kernel<decltype(f)::value, D, prompt_tiles(D)><<<p.prompt_wg, 64 * kWaves, 0, s>>>(a);
+    constexpr int F = decltype(f)::value, D = decltype(d)::value;
+    if constexpr (D < 256) {
+      if (p.prompt_waves == 8) {
+        kv_prompt_kernel<F, D, 8><<<p.prompt_wg, 64 * 8, 0, s>>>(a);
+        return hipGetLastError();
+      }
+    }
+    kv_prompt_kernel<F, D, 4><<<p.prompt_wg, 64 * 4, 0, s>>>(a);
     return hipGetLastError();
   };
   return kv_dispatch(format, dim, go);

@@ -9,12 +9,12 @@ from ops_common import BF, Guarded, rand, say, strided
 
 pytestmark = pytest.mark.gpu
 FORMATS = [S.NVFP4, S.MXFP4]
-UNIT = {64: 256, 128: 128, 256: 64}                    # rows of a workgroup
+UNIT = {64: 128, 128: 128, 256: 64}                    # rows of a workgroup
 
 
-def heads_for(dim, rows):
-    """kv heads that give the call the 256 units that the launch is for."""
-    return -(-256 // (rows // UNIT[dim]))
+def heads_for(dim, rows, units=256):
+    """kv heads that give the call the 256 units that the launch is for, or the 1024 of its four waves."""
+    return -(-units // (rows // UNIT[dim]))
 
 
 def run(P, group, window=0, seed=0):
@@ -37,11 +37,20 @@ def test_one_prompt(fmt, dim, group):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim,group,new,window", [(64, 8, 135, 0), (64, 5, 410, 100), (128, 16, 130, 0), (128, 3, 700, 33)])
+def test_four_waves(fmt, dim, group, new, window):
+    heads = heads_for(dim, new * group, 1024)
+    say("four waves", fmt, dim, group, heads)
+    run(Paged(fmt, dim, heads, 16, [new + 85], [new], seed=dim + group, unmapped=[(0, 3), (0, 8)]), group, window=window)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("units", [256, 1024])
 @pytest.mark.parametrize("window", [0, 1, 63, 64, 200])
-def test_several_sequences(fmt, window):
+def test_several_sequences(fmt, units, window):
     """Prompts, chunks after others, drafted and single tokens, none: the launch for prompts and that for few rows."""
     lens, new = [700, 40, 250, 333, 9, 1, 90, 1000], [400, 40, 250, 4, 0, 1, 65, 33]
-    heads = heads_for(64, sum(new) * 4)
+    heads = heads_for(64, sum(new) * 4, units)
     say("prompts", fmt, window, heads)
     run(Paged(fmt, 64, heads, 32, lens, new, seed=window), 4, window=window)
 
