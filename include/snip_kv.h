@@ -59,8 +59,11 @@ typedef struct snipkv_cache {
  * at page_size * i .. lie in page table[b][i]. A position below 0, one behind the
  * table, and one whose table entry is outside 0 .. pages - 1 (a page that was
  * given back, say) is not mapped: nothing is written there, and its key takes
- * no part. Rows from cu[seqs] on belong to nobody: they are neither read nor
- * written, so a captured call may hold more rows than it uses. */
+ * no part. Rows from cu[seqs] on belong to nobody: what they hold does not
+ * matter and they are not written, so a captured call may hold more rows than it
+ * uses. A call has 1 .. 2^20 tokens; attention takes SHAPE for more than 2^24
+ * tiles of 16 rows (a kv head's tokens times its query heads, and one a sequence)
+ * or 2^30 over all kv heads. */
 typedef struct snipkv_batch {
   const int32_t* table;  /* device [seqs][table_ld], max_pages entries used              */
   int64_t table_ld;
@@ -108,10 +111,12 @@ int snipkv_gather(const snipkv_cache* cache, const snipkv_batch* batch, int64_t 
  * for every row and query head; head h reads kv head h / (q_heads / kv_heads).
  * A row with no key at all: out = 0, lse = -infinity. fp32 throughout, but the
  * softmax's terms, which enter the matrix product in fp16 (MXFP4: in two parts
- * of bf16); out is rounded once. Not defined for scores past 3e38. The same
- * inputs give the same bits.
+ * of bf16); out is rounded once. Not defined for scores past 2e38, values past
+ * 1e30, and scales of NaN (which append never stores) in places that a row of the
+ * call sees: other rows of the call may become NaN. The same inputs give the same
+ * bits.
  *   q         device bf16 [tokens][q_heads * head_dim], ldq.
- *   scale     > 0, finite.
+ *   scale     > 0, up to 2e38.
  *   window    0: none; else >= 1.
  *   out       device bf16, ldo. May be q itself.
  *   lse       device fp32 [tokens][q_heads] or NULL.

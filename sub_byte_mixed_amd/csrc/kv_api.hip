@@ -188,7 +188,8 @@ int snipkv_attn(const void* q, int64_t ldq, int64_t q_heads, int64_t tokens, con
   const int64_t cols = q_heads * cache->head_dim;
   if ((rc = check_rows(who, "q", q, SNIPOP_BF16, ldq, cols))) return rc;
   if ((rc = check_rows(who, "out", out, SNIPOP_BF16, ldo, cols))) return rc;
-  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(SNIP_E_SHAPE, "%s: scale must be finite and > 0", who);
+  const float scale2 = (float)((double)scale * 1.4426950408889634);   // of powers of two
+  if (!(scale > 0.0f) || !std::isfinite(scale2)) return fail(SNIP_E_SHAPE, "%s: scale must be > 0 and up to 2e38", who);
   if (window < 0) return fail(SNIP_E_SHAPE, "%s: window=%lld must be >= 0", who, (long long)window);
   if (!aligned(lse, 4) || !aligned(ws, 16)) return fail(SNIP_E_ALIGN, "%s: misaligned pointer", who);
   const size_t need = snipkv_attn_workspace(tokens, batch->seqs, q_heads, cache->kv_heads, cache->head_dim);
@@ -206,7 +207,7 @@ int snipkv_attn(const void* q, int64_t ldq, int64_t q_heads, int64_t tokens, con
   a.q_heads = (int32_t)q_heads;
   a.group = (int32_t)(q_heads / cache->kv_heads);
   a.window = window < kMaxLen ? (int32_t)window : 0;    // no position is further back
-  a.scale = (float)((double)scale * 1.4426950408889634);
+  a.scale = scale2;
   const KvPlan p = kv_attn_plan(cache->format, cache->head_dim, &a);
   hipStream_t s = static_cast<hipStream_t>(stream);
   auto timed = [&](int kind, hipError_t (*launch)(int, int, const KvPlan&, const KvAttn&, hipStream_t)) {

@@ -277,7 +277,6 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
           for (int l = 0; l < G::VL; ++l) T.vs[h][l] &= keep;
         }
       }
-      // The maximum may lag by 2^8: terms of up to 256 are as exact, and most tiles leave the output as it is.
       float top[NR];
       bool above = false;
 #pragma unroll
@@ -287,12 +286,12 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int j = 0; j < 4; ++j) top[i] = fmaxf(top[i], s[i][h][j]);
-        above |= top[i] > R[i].m + 8.0f;
+        above |= top[i] > R[i].m + (kLag + kLift<FMT>);
       }
       if (__any(above)) {
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-          const float m = fmaxf(row_max(top[i]), R[i].m), f = __builtin_amdgcn_exp2f(R[i].m - m);
+          const float m = fmaxf(row_max(top[i]) - kLift<FMT>, R[i].m), f = __builtin_amdgcn_exp2f(R[i].m - m);
           R[i].m = m;
           R[i].l *= f;
 #pragma unroll

@@ -33,6 +33,13 @@ typedef float f4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4, kRows = 16;
 constexpr float kLowest = -3.0e38f;                    // below every score
+// A row's m may lag behind its maximum by 2^8, which leaves the output as it is
+// for most tiles. NVFP4: it lies 2^7 below the maximum besides, so that terms of
+// 2^-21 of the largest keep fp16's precision and 2^-31 still counts: a long
+// sequence has many.
+constexpr float kLag = 8.0f;
+template <int FMT>
+constexpr float kLift = FMT == SNIP_NVFP4 ? 7.0f : 0.0f;
 
 template <int FMT, int D>
 struct Geo {

@@ -132,9 +132,9 @@ class Paged:
                 half = 2.0 ** -11 if self.fmt == S.NVFP4 else 2.0 ** -17
                 sums = (keys + 64) * U
                 tol_o[r, h] = a * (2 * rel + half + 2 * sums)[..., None] + 2.0 ** -8 * np.abs(o)
-                # p below fp16's normal range is off by 2^-25 of the largest of 256, a sum of at least 2^-8
+                # p below fp16's normal range is off by 2^-25, where the largest is 2^7 at least
                 if self.fmt == S.NVFP4 and k.shape[1]:
-                    tol_o[r, h] += 2.0 ** -17 * keys[..., None] * np.abs(v[h]).max() * 2.0 ** -8
+                    tol_o[r, h] += 2.0 ** -32 * keys[..., None] * np.abs(v[h]).max()
                 # and a term below 2^-126 of the largest is lost, as is a product or an output of that size
                 if k.shape[1]:
                     tol_o[r, h] += 2.0 ** -126 * (1 + keys[..., None] * (1 + np.abs(v[h]).max()))
@@ -152,6 +152,18 @@ class Paged:
             g, z = f64(lse)[:n], z[:n]
             bad = ~((np.abs(g - np.where(np.isfinite(z), z, 0.0)) <= tl[:n]) | ((g == z) & ~np.isfinite(z)))
             assert not bad.any(), (what, "lse", np.argwhere(bad)[:4].tolist(), g[bad][:4], z[bad][:4], tl[:n][bad][:4])
+
+
+def peak(P, at):
+    """Keys of zero, but ones for token `at` of sequence 0; values of one, but zeros for that token (times 2^TEXP)."""
+    c, p, j = P.cache, int(P.table[0, at // P.page]), at % P.page
+    one = 0x38 if P.fmt == S.NVFP4 else 127
+    c.k_codes.zero_()
+    c.v_codes.fill_(0x22)
+    for t in (c.k_scales, c.v_scales):
+        t.fill_(one)
+    c.k_codes[p, :, j // 16, :, j % 16] = 0x22
+    c.v_codes[p, :, j // 4, :, j % 4] = 0
 
 
 def quantized(x, fmt, texp):

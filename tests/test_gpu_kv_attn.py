@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import sub_byte_mixed_amd as S
-from kv_common import Paged
+from kv_common import Paged, peak
 from ops_common import BF, F32, Guarded, f64, rand, say, strided
 
 pytestmark = pytest.mark.gpu
@@ -123,6 +123,56 @@ def test_rising_scores(fmt, capacity):
         n = min(16, 700 - j)
         t[int(P.table[0, j // 32]), :, j % 32 // 16, :n] = (base + step * ramp[j:j + n, None, None]).to(torch.uint8).cuda()
     run(P, 3)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("ks,vs", [((0x01, 0x10), (0x70, 0x7F)), ((0x70, 0x7F), (0x01, 0x10)), ((0x00, 0x02), (0x00, 0x02))])
+@pytest.mark.parametrize("capacity", CAPACITIES)
+def test_scales_at_the_ends(fmt, ks, vs, capacity):
+    """E4M3 scales from the subnormal to the largest; E8M0's 2^-127 on, and values to 1e30."""
+    if fmt == S.MXFP4:
+        ks, vs = [{0x01: (1, 8), 0x70: (125, 135), 0x00: (0, 2)}[a[0]] for a in (ks, vs)]
+        vs = (218, 224) if vs == (125, 135) else vs
+    P = Paged(fmt, 64, 2, 16, [300, 33], [1, 33], seed=21, capacity=capacity)
+    g = torch.Generator().manual_seed(3)
+    for t, (lo, hi) in ((P.cache.k_scales, ks), (P.cache.v_scales, vs)):
+        new = torch.randint(lo, hi, t.shape, generator=g, dtype=torch.uint8).cuda()
+        t.copy_(torch.where(t == (0x7F if fmt == S.NVFP4 else 0xFF), t, new))
+    run(P, 4)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("capacity", [0, 30000])
+def test_many_small_terms(fmt, dim, capacity):
+    """A key that takes nearly all of the softmax and whose value is zero: what is left is the others' part."""
+    n = 20000 if capacity else 1200
+    P = Paged(fmt, dim, 1, 64, [n], [1], seed=22, capacity=capacity, one_each=True)
+    peak(P, n // 3)
+    q = torch.ones((1, dim), dtype=BF)
+    scale = 26.0 * float(np.log(2.0)) / (dim * (0.125 if fmt == S.NVFP4 else 1.0))
+    out, lse = S.kv_attn(q.cuda(), P.cache, P.batch, scale=scale, with_lse=True)
+    P.check(q, out, lse, scale)
+    assert bool((out.float() > 0.9 * n * 2.0 ** -26 * (2.0 ** -5 if fmt == S.NVFP4 else 1.0)).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("capacity", CAPACITIES)
+def test_queries_that_are_not_finite(fmt, capacity):
+    """They reach their own rows alone."""
+    P = Paged(fmt, 128, 1, 16, [90, 700], [40, 1], seed=23, capacity=capacity)
+    q = rand((P.rows, 4 * 128), BF, 5, 0.5)
+    odd = q.clone()
+    bad = [(3, 0, 7), (3, 2, 100), (17, 1, 0), (39, 3, 127), (40, 0, 64)]      # token, head, dimension
+    for i, (t, h, d) in enumerate(bad):
+        odd[t, h * 128 + d] = (float("nan"), float("inf"), -float("inf"))[i % 3]
+    out, lse = S.kv_attn(odd.cuda(), P.cache, P.batch, with_lse=True)
+    want, want_lse = S.kv_attn(q.cuda(), P.cache, P.batch, with_lse=True)
+    for t, h, d in bad:
+        assert bool(out[t, h * 128:(h + 1) * 128].isnan().all())
+        out[t, h * 128:(h + 1) * 128] = want[t, h * 128:(h + 1) * 128]
+        lse[t, h] = want_lse[t, h]
+    P.check(q, out, lse)
 
 
 def test_a_key_of_nan_reaches_the_rows_that_see_it():

@@ -1,10 +1,12 @@
 """snipkv_attn with as many rows as its launch for prompts takes (64 row tiles
 or more a kv head's sequences), against float64 as in test_gpu_kv_attn.py."""
+import math
+
 import pytest
 import torch
 
 import sub_byte_mixed_amd as S
-from kv_common import Paged
+from kv_common import Paged, peak
 from ops_common import BF, Guarded, rand, say, strided
 
 pytestmark = pytest.mark.gpu
@@ -83,3 +85,20 @@ def test_many_query_heads_of_one_token():
     """More heads to a kv head than a workgroup has rows, without cu."""
     P = Paged(S.NVFP4, 64, 1, 16, [100 + b for b in range(300)], [1] * 300, one_each=True)
     run(P, 300)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("units", [256, 1024])
+def test_many_small_terms(fmt, units):
+    """As in test_gpu_kv_attn.py: the part of p keys of 2^-26 of the largest is p 2^-26, off by p 2^-32, the score's
+    error of 200 2^-24 times it, and the output's rounding."""
+    new = 2100
+    P = Paged(fmt, 64, heads_for(64, new, units), 64, [new], [new], seed=22)
+    peak(P, 0)
+    scale = 26.0 * math.log(2.0) / (64 * (0.125 if fmt == S.NVFP4 else 1.0))
+    q = torch.ones((new, P.heads * 64), dtype=BF, device="cuda")
+    out, _ = S.kv_attn(q, P.cache, P.batch, scale=scale)
+    p = torch.arange(new, dtype=torch.float64)[:, None]
+    unit = 2.0 ** -5 if fmt == S.NVFP4 else 1.0
+    want = unit * p * 2.0 ** -26 / (1.0 + p * 2.0 ** -26)
+    assert bool(((out.cpu().double() - want).abs() <= p * 2.0 ** -32 * unit + want * (2.0 ** -8 + 2.0 ** -11 + 18.1 * 200 * 2.0 ** -24)).all())

@@ -140,7 +140,7 @@ def test_attn_validation(L):
     need = L.snipkv_attn_workspace(5, 3, 8, 4, 128)
     assert need > 0
     for more, code in [(dict(q=None), NULL), (dict(out=None), NULL), (dict(heads=6), SHAPE), (dict(heads=0), SHAPE), (dict(ldq=1016), SHAPE),
-                       (dict(ldo=1028), SHAPE), (dict(scale=0.0), SHAPE), (dict(scale=-1.0), SHAPE), (dict(scale=float("inf")), SHAPE),
+                       (dict(ldo=1028), SHAPE), (dict(scale=0.0), SHAPE), (dict(scale=-1.0), SHAPE), (dict(scale=float("inf")), SHAPE), (dict(scale=3e38), SHAPE),
                        (dict(scale=float("nan")), SHAPE), (dict(window=-1), SHAPE), (dict(q=at(1) + 8), ALIGN), (dict(out=at(1) + 2), ALIGN),
                        (dict(lse=at(1) + 2), ALIGN), (dict(ws=at(1) + 8), ALIGN), (dict(ws=None), WORKSPACE), (dict(n=need - 1), WORKSPACE),
                        (dict(heads=1024, c=cache(heads=1), tokens=1 << 20, ldq=1 << 17, ldo=1 << 17), SHAPE)]:
