@@ -57,8 +57,9 @@ class CachedAttention:
 
     def prompt(self, x: torch.Tensor, res: torch.Tensor, cache: "S.KVCache", batch: "S.KVBatch", window: int = 0, ws=None):
         """x: what joins the residual stream res, both [T, hidden], T a multiple
-        of 128; rows from batch.cu[-1] on are padding, whose output is zero. res becomes the new stream, the tokens' keys and values go into
-        the cache; returns the output [T, hidden] in fp32."""
+        of 128; rows from batch.cu[-1] on are padding, whose output is zero. res
+        becomes the new stream, the tokens' keys and values go into the cache;
+        returns the output [T, hidden] in fp32."""
         y, _, _, _, _ = S.rmsnorm_fwd(x, self.gamma, self.eps, res=res, h=res, with_rstd=False)
         qy, _ = S.quantize(y, S.ROWWISE, self.fmt, with_stats=False)
         o = self._attend(S.qgemm(qy, self.q_qkv), cache, batch, window, ws)
