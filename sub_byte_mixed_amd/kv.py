@@ -73,10 +73,12 @@ def cache_shapes(fmt: int, pages: int, page_size: int, kv_heads: int, head_dim: 
             (pages, kv_heads, page_size // 4, head_dim // block, 4))
 
 
-def _buffer(t: torch.Tensor, name: str, shape: tuple, dev: int) -> None:
-    if t.dtype is not _U8 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {shape} on GPU {dev}, got {t.dtype}, "
-                         f"{tuple(t.shape)} on {t.device}")
+def _buffer(t: torch.Tensor, name: str, shape: tuple, dev: int) -> int:
+    """Its address."""
+    if t.dtype is _U8 and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {shape} on GPU {dev}, got {t.dtype}, "
+                     f"{tuple(t.shape)} on {t.device}")
 
 
 class KVCache:
@@ -92,16 +94,13 @@ class KVCache:
         pages, heads, groups, pieces, _, p = k_codes.shape
         page, dim, dev = 16 * groups, 2 * pieces * p, k_codes.get_device()
         sk, ssk, sv, ssv = cache_shapes(fmt, pages, page, heads, dim)
-        _buffer(k_codes, "k_codes", sk, dev)
-        _buffer(k_scales, "k_scales", ssk, dev)
-        _buffer(v_codes, "v_codes", sv, dev)
-        _buffer(v_scales, "v_scales", ssv, dev)
+        at = (_buffer(k_codes, "k_codes", sk, dev), _buffer(k_scales, "k_scales", ssk, dev),
+              _buffer(v_codes, "v_codes", sv, dev), _buffer(v_scales, "v_scales", ssv, dev))
         if texp is None and fmt == _S.NVFP4:
             raise ValueError("an NVFP4 cache needs texp")
         self.format, self.pages, self.kv_heads, self.page_size, self.head_dim, self.device = fmt, pages, heads, page, dim, dev
         self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.texp = k_codes, k_scales, v_codes, v_scales, texp
-        self._desc = CacheDesc(fmt, page, heads, dim, pages, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-                               v_scales.data_ptr(), _vec(texp, "texp", 2, (_I32,), dev))
+        self._desc = CacheDesc(fmt, page, heads, dim, pages, *at, _vec(texp, "texp", 2, (_I32,), dev))
         self.ref = ctypes.byref(self._desc)
 
     @classmethod
@@ -199,8 +198,10 @@ def kv_append(k: Optional[torch.Tensor], v: Optional[torch.Tensor], cache: KVCac
         elif rows != tokens:
             raise ValueError(f"q must have {tokens} rows, got {rows}")
         if q_out is None:
-            q_out = q.new_empty((tokens, heads * dim), dtype=_BF)
-        po, lo = _same(_heads(q_out, "q_out", dev, dim, _BF), "q_out", tokens, heads)
+            q_out, lo = q.new_empty((tokens, heads * dim), dtype=_BF), heads * dim
+            po = q_out.data_ptr()
+        else:
+            po, lo = _same(_heads(q_out, "q_out", dev, dim, _BF), "q_out", tokens, heads)
     elif q_out is not None:
         raise ValueError("q_out belongs to q")
     if cos is not None or sin is not None:
@@ -228,12 +229,17 @@ def kv_gather(cache: KVCache, batch: KVBatch, tokens: Optional[int] = None, k: O
     dim, hk = cache.head_dim, cache.kv_heads
     if tokens is None:
         tokens = k.shape[0] if k is not None else v.shape[0] if v is not None else batch.seqs
+    lk = lv = hk * dim
     if k is None:
-        k = cache.k_codes.new_empty((tokens, hk * dim), dtype=_BF)
+        k = cache.k_codes.new_empty((tokens, lk), dtype=_BF)
+        pk = k.data_ptr()
+    else:
+        pk, lk = _same(_heads(k, "k", dev, dim, _BF), "k", tokens, hk)
     if v is None:
-        v = cache.k_codes.new_empty((tokens, hk * dim), dtype=_BF)
-    pk, lk = _same(_heads(k, "k", dev, dim, _BF), "k", tokens, hk)
-    pv, lv = _same(_heads(v, "v", dev, dim, _BF), "v", tokens, hk)
+        v = cache.k_codes.new_empty((tokens, lv), dtype=_BF)
+        pv = v.data_ptr()
+    else:
+        pv, lv = _same(_heads(v, "v", dev, dim, _BF), "v", tokens, hk)
     _S._check(_S.lib().snipkv_gather(cache.ref, batch.ref, tokens, pk, lk, pv, lv, _ops._current_stream(dev)))
     return k, v
 
@@ -258,8 +264,10 @@ def kv_attn(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: Optional[flo
     dim, hk = cache.head_dim, cache.kv_heads
     pq, lq, tokens, heads = _heads(q, "q", dev, dim, _BF)
     if out is None:
-        out = q.new_empty((tokens, heads * dim))
-    po, lo = _same(_heads(out, "out", dev, dim, _BF), "out", tokens, heads)
+        out, lo = q.new_empty((tokens, heads * dim)), heads * dim
+        po = out.data_ptr()
+    else:
+        po, lo = _same(_heads(out, "out", dev, dim, _BF), "out", tokens, heads)
     pl = None
     if lse is None and with_lse:
         lse = q.new_empty((tokens, heads), dtype=_F32)
@@ -268,8 +276,11 @@ def kv_attn(q: torch.Tensor, cache: KVCache, batch: KVBatch, scale: Optional[flo
             raise ValueError(f"lse must be a contiguous float32 tensor of shape ({tokens}, {heads}) on GPU {dev}")
         pl = lse.data_ptr()
     if ws is None:
-        ws = q.new_empty(_workspace(tokens, batch.seqs, heads, hk, dim), dtype=_U8)
-    pw, nw = _scratch(ws, dev)
+        nw = _workspace(tokens, batch.seqs, heads, hk, dim)
+        ws = q.new_empty(nw, dtype=_U8)
+        pw = ws.data_ptr()
+    else:
+        pw, nw = _scratch(ws, dev)
     _S._check(_S.lib().snipkv_attn(pq, lq, heads, tokens, cache.ref, batch.ref, 1.0 / math.sqrt(dim) if scale is None else scale,
                                    window, po, lo, pl, pw, nw, _ops._current_stream(dev)))
     return out, lse
