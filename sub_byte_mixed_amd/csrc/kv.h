@@ -56,6 +56,7 @@ struct KvAttn {
   int32_t window;              // 0: none
   int32_t few, split;          // split: sequences of more rows than `few` have a launch of their own
   int32_t step;                // keys of a step of work, a multiple of a workgroup's
+  int32_t each;                // steps of a sequence where all have as many; 0: they follow from lens and cu
   float scale;                 // times log2 e
 };
 

@@ -136,7 +136,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
   cur.coarse = upto[wave][0];
   cur.fine = upto[wave][1];
   cur.unit_rows = kUnit;
-  const Shares shares(cur.total(A), gridDim.x);
+  const Shares shares(A.each ? A.each * A.b.seqs : cur.total(A), gridDim.x);
   int at = shares.first(blockIdx.x);
   const int stop = shares.first(blockIdx.x + 1);
   if (at >= stop) {
@@ -161,9 +161,14 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
   Pages g0, g1;
   auto setup = [&](Part& P) {
     int from;
-    P.seq = cur.seek(A, at, &from);
+    if (A.each) {
+      P.seq = at / A.each;
+      from = P.seq * A.each;
+    } else {
+      P.seq = cur.seek(A, at, &from);
+    }
     const Span U = span_of(A, P.seq, kUnit);
-    const int unit = (at - from) / U.steps, s0 = (at - from) % U.steps;
+    const int unit = A.each ? at - from : (at - from) / U.steps, s0 = A.each ? 0 : (at - from) % U.steps;
     const int s1 = stop - at < U.steps - s0 ? s0 + (stop - at) : U.steps;
     at += s1 - s0;
     P.row0 = U.row0;
@@ -508,7 +513,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn A, bool nv) {
 
 // Keys up to which a workgroup takes a unit as a whole: the second launch costs
 // as much as five rounds of eight waves (64 sequences of 1024 tokens, 8 kv heads
-// of 128: 17 us, shared and joined 28; one sequence 10.4 and 10.6).
+// of 128: 17 us, shared and joined 28; one sequence 10.0 and 10.6).
 constexpr int kShort = 1280;
 // Bytes of a cache from which it is read past the last-level cache, where it
 // cannot stay (362 MB: 82 -> 74 us; 75 MB, read again and again: 28 -> 30).
@@ -555,12 +560,18 @@ KvPlan kv_attn_plan(int format, int dim, KvAttn* a) {
   p.two = most_tiles(dim) > 1 && mean > kRows && !p.wide;
   const int tiles = p.two ? 2 : 1, block = format == SNIP_NVFP4 ? 16 : 32;
   const int64_t each = units(kRows * tiles);
-  p.few_wg = whole ? (unsigned)(each < (1 << 20) ? each : 1 << 20) : (unsigned)workers_of(dim, tiles);
+  // Whole units: more than are resident, which evens the lengths out, but not a
+  // workgroup each where there are many (256 sequences of 1200 tokens, 2048 units:
+  // 79 us, of 256 to 512: 38, and 77 and 36 with twice as many as are resident).
+  const int64_t workers = workers_of(dim, tiles);
+  p.few_wg = (unsigned)(!whole ? workers : each < 2 * workers ? each : 2 * workers);
   p.join_rows = !b.cu && a->group < kRows * tiles ? a->group : kRows * tiles;
   p.past = !whole && (((int64_t)a->c.pages * a->c.heads) << a->c.shift) * (dim + 2 * dim / block) >= kStream;
   // Steps are counted in 31 bits, whatever the lengths that the tables allow.
   a->step = 32 * kWaves;
   while (a->step < b.max_len && (whole || (double)each * ((double)b.max_len / a->step + 1.0) >= 2147483647.0)) a->step *= 2;
+  // A token each and units of one step: no search by lens (16 keys: 6.7 -> 6.2 us, 256 sequences of 256 to 512: 41 -> 38)
+  a->each = whole && !b.cu ? (a->group + kRows * tiles - 1) / (kRows * tiles) * a->c.heads : 0;
   a->left = p.join ? reinterpret_cast<Left*>(a->part + (size_t)workers_of(dim, tiles) * 2 * slot_floats(dim, kRows * tiles)) : nullptr;
   return p;
 }
