@@ -264,9 +264,11 @@ struct Span {                  // of one sequence
 __device__ __forceinline__ int limit(const KvAttn& A, int64_t p) {
   return (int)(p < 0 ? -1 : p >= A.b.max_len ? A.b.max_len - 1 : p);
 }
-// First key that a row at position p sees.
+// First key that a row at position p sees; the table's end where its window lies
+// behind that.
 __device__ __forceinline__ int first_key(const KvAttn& A, int64_t p) {
-  return A.window && p >= A.window ? limit(A, p - A.window + 1) : 0;
+  if (!A.window || p < A.window) return 0;
+  return (int)(p - A.window + 1 < A.b.max_len ? p - A.window + 1 : A.b.max_len);
 }
 
 __device__ __forceinline__ Span span_of(const KvAttn& A, int b, int unit_rows) {

@@ -82,6 +82,18 @@ def test_more_new_tokens_than_the_sequence_has(capacity):
     assert not out[:4].any() and not out[9:].any() and bool((lse[9:] == -float("inf")).all())
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("length,new,window,wide", [(50, 40, 5, 2), (50, 40, 0, 2), (45, 1, 12, 2), (1500, 300, 50, 81), (1500, 1, 200, 82), (1500, 3, 205, 81)])
+def test_positions_behind_the_table(fmt, length, new, window, wide):
+    """They see the table's keys that their window reaches, or none."""
+    P = Paged(fmt, 64, 2, 16, [length], [new], seed=24, unmapped=[(0, j) for j in range(wide, -(-length // 16))])
+    q, out, lse = run(P, 4, window)
+    got, z = S.kv_attn(q.cuda(), P.cache, S.KVBatch(P.batch.table[:, :wide], P.batch.lens, P.batch.cu), window=window, with_lse=True)
+    P.check(q, got, z, None, window)
+    if window and length - window >= 16 * wide:
+        assert not got[-1].any() and bool((z[-1] == -float("inf")).all())
+
+
 @pytest.mark.parametrize("capacity", CAPACITIES)
 def test_rows_of_nobody_and_strides(capacity):
     P = Paged(S.NVFP4, 128, 2, 16, [33, 80], [33, 2], seed=5, capacity=capacity)

@@ -102,3 +102,40 @@ def test_many_small_terms(fmt, units):
     unit = 2.0 ** -5 if fmt == S.NVFP4 else 1.0
     want = unit * p * 2.0 ** -26 / (1.0 + p * 2.0 ** -26)
     assert bool(((out.cpu().double() - want).abs() <= p * 2.0 ** -32 * unit + want * (2.0 ** -8 + 2.0 ** -11 + 18.1 * 200 * 2.0 ** -24)).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim,window", [(64, 100), (128, 17), (256, 100), (64, 0)])
+def test_positions_behind_the_table(fmt, dim, window):
+    P = Paged(fmt, dim, heads_for(dim, 600 * 2), 16, [650], [600], seed=24, unmapped=[(0, j) for j in range(31, 41)])
+    q, out, lse = run(P, 2, window)
+    got, z = S.kv_attn(q.cuda(), P.cache, S.KVBatch(P.batch.table[:, :31], P.batch.lens, P.batch.cu), window=window, with_lse=True)
+    P.check(q, got, z, None, window)
+    if window:
+        assert not got[-1].any() and bool((z[-1] == -float("inf")).all())
+
+
+def test_graph_replays_follow_the_batch():
+    """One captured call whose sequences change between prompts, few rows and none: every replay equals the eager call."""
+    P = Paged(S.NVFP4, 64, 32, 32, [1100, 900, 700], [500, 200, 100], seed=25)
+    q = rand((P.rows, 32 * 4 * 64), BF, 3, 0.5).cuda()
+    ws = torch.empty(S.lib().snipkv_attn_workspace(P.rows, 3, 128, 32, 64), dtype=torch.uint8, device="cuda")
+    S.kv_attn(q, P.cache, P.batch, ws=ws)
+    torch.cuda.synchronize()
+    graph, out = torch.cuda.CUDAGraph(), torch.zeros_like(q)
+    with torch.cuda.graph(graph):
+        S.kv_attn(q, P.cache, P.batch, ws=ws, out=out)
+    for i, (lens, new) in enumerate([((1100, 900, 700), (500, 200, 100)), ((1100, 33, 5), (790, 9, 1)), ((40, 900, 0), (40, 700, 0)),
+                                     ((1, 1, 1), (1, 1, 1)), ((1100, 900, 700), (64, 65, 300)), ((1100, 0, 0), (800, 0, 0))]):
+        say("prompt graph", i)
+        cu = [0, new[0], new[0] + new[1], sum(new)]
+        P.batch.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        P.batch.cu.copy_(torch.tensor(cu, dtype=torch.int32))
+        ws.fill_(255)
+        out.fill_(7.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        want = S.kv_attn(q, P.cache, P.batch, out=torch.full_like(q, 7.0))[0]
+        assert torch.equal(got, want) and bool((got[cu[3]:] == 7.0).all()), i
