@@ -5,7 +5,11 @@
 // head of one sequence -- has the steps of the sequence's keys, units follow each
 // other by sequence, head and rows, and the steps of the call are shared evenly
 // among the workgroups, whatever the lengths. A workgroup finds its share from
-// lens and cu alone, so a captured launch follows them.
+// lens and cu alone, so a captured launch follows them. Many sequences are bound
+// by the bytes of the keys and values (64 sequences of 1741 to 8192 keys, 64 heads
+// over 8 of 128, NVFP4: 368 MB in 66 us, 5.6 TB/s), one by the chain of loads
+// before its first keys and after its last (65536 keys: 21 us, 700: 8), rows that
+// fill a tile by decoding and the softmax (two tiles, as below: 2.2 TB/s).
 #include "kv_tile.h"
 
 namespace snip {
@@ -102,8 +106,10 @@ namespace {
 
 constexpr int slot_floats(int dim, int rows) { return rows * (dim + 2); }
 
-// Row tiles of a unit, waves of a SIMD that the registers are held to, and
-// workgroups: as many as are resident.
+// Row tiles of a unit: two decode a key once for up to 32 rows, at the price of a
+// wave of occupancy (16 sequences of 4 tokens, 64 heads over 8: 34 us, with one
+// tile 36; 8 of 32 tokens: 82 and 126). Waves of a SIMD that the registers are
+// held to, and workgroups: as many as are resident.
 constexpr int most_tiles(int dim) { return dim == 256 ? 1 : 2; }
 constexpr int waves_of(int dim, int tiles) { return dim == 256 ? 2 : (dim == 128 ? 3 : 4) - (tiles == 2); }
 constexpr int workers_of(int dim, int tiles) { return 256 * waves_of(dim, tiles); }
@@ -518,9 +524,12 @@ constexpr int kShort = 1280;
 // Bytes of a cache from which it is read past the last-level cache, where it
 // cannot stay (362 MB: 82 -> 74 us; 75 MB, read again and again: 28 -> 30).
 constexpr int64_t kStream = (int64_t)128 << 20;
-// Rows of a sequence up to which it is left to this file's launch where another
-// takes the prompts: those have 64 rows at least to a workgroup.
-constexpr int kFew = 64;
+// Mean rows of a sequence from which a call is one of prompts, and rows of a
+// sequence up to which it is left to this file's launch all the same: a token's
+// heads. More of them would follow the prompts instead of running among them (64
+// sequences of 1 to 33 new tokens, up to 2048 keys, 64 heads over 8: 16 rows 120
+// us, 64 127, 128 152; 16 of 2 to 64 after 4096: 132, 139, 142).
+constexpr int kPrompt = 64, kFew = 16;
 
 }  // namespace
 
@@ -548,7 +557,7 @@ KvPlan kv_attn_plan(int format, int dim, KvAttn* a) {
   const int64_t mean = a->tokens * a->group / b.seqs;
   const int unit = kv_prompt_rows(dim);
   const int64_t full = a->tokens * a->group / unit * a->c.heads;
-  p.prompt = mean >= kFew && full >= 256 && units(unit) < (1 << 24);
+  p.prompt = mean >= kPrompt && full >= 256 && units(unit) < (1 << 24);
   p.prompt_waves = dim < 256 && full < 1024 ? 8 : 4;     // measured at kv_prompt_kernel
   p.prompt_wg = p.prompt ? (unsigned)units(unit) : 0;
   a->split = p.prompt && b.seqs > 1;
@@ -557,7 +566,7 @@ KvPlan kv_attn_plan(int format, int dim, KvAttn* a) {
   const bool whole = b.max_len <= kShort && !p.prompt;
   p.join = p.few && !whole;
   p.wide = whole && units(kRows) <= 256;                 // no more than CUs (512: 21 us, with four waves 17)
-  p.two = most_tiles(dim) > 1 && mean > kRows && !p.wide;
+  p.two = most_tiles(dim) > 1 && mean > kRows && !p.wide && !a->split;
   const int tiles = p.two ? 2 : 1, block = format == SNIP_NVFP4 ? 16 : 32;
   const int64_t each = units(kRows * tiles);
   // Whole units: more than are resident, which evens the lengths out, but not a
