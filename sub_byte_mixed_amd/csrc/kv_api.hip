@@ -13,7 +13,7 @@ namespace {
 constexpr int64_t kMaxTokens = (int64_t)1 << 20;
 constexpr int64_t kMaxTiles = ((int64_t)1 << 24) - 1;   // of 256 threads in a grid's dimension
 constexpr int64_t kMaxSeqs = (int64_t)1 << 20;
-constexpr int64_t kMaxLen = (int64_t)1 << 30;          // positions are 32-bit
+constexpr int64_t kMaxLen = (int64_t)1 << 30;          // of a table, in tokens
 constexpr int64_t kMaxHeads = 1024;
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
 
@@ -206,7 +206,7 @@ int snipkv_attn(const void* q, int64_t ldq, int64_t q_heads, int64_t tokens, con
   a.tokens = tokens;
   a.q_heads = (int32_t)q_heads;
   a.group = (int32_t)(q_heads / cache->kv_heads);
-  a.window = window < kMaxLen ? (int32_t)window : 0;    // no position is further back
+  a.window = window <= INT32_MAX ? (int32_t)window : 0;    // positions are below that, lens being 32-bit
   a.scale = scale2;
   const KvPlan p = kv_attn_plan(cache->format, cache->head_dim, &a);
   hipStream_t s = static_cast<hipStream_t>(stream);

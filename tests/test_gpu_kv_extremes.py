@@ -1,0 +1,47 @@
+"""snipkv_attn at the ends of what its arguments may be, in the launch for few
+rows (a workgroup a unit, and steps shared among workgroups) and in the one for
+prompts (eight and four waves a workgroup), against float64 as in
+test_gpu_kv_attn.py."""
+import numpy as np
+import pytest
+import torch
+
+import sub_byte_mixed_amd as S
+from kv_common import Paged
+from ops_common import BF, rand, say
+
+pytestmark = pytest.mark.gpu
+FORMATS = [S.NVFP4, S.MXFP4]
+UNIT = {64: 128, 128: 128, 256: 64}                    # rows of a workgroup for prompts
+LAUNCHES = {"whole": 0, "shared": 0, "eight": 256, "four": 1024}     # units that a call of prompts has at least
+
+
+def paged(launch, fmt, dim, group, seed, keys=0, **more):
+    """One sequence for a launch: three new tokens of `keys` (100 where 0), or a prompt of 600, after 40 others."""
+    if LAUNCHES[launch]:
+        new = 600
+        heads = -(-LAUNCHES[launch] // (new * group // UNIT[dim]))
+        return Paged(fmt, dim, heads, 16, [keys or new + 40], [new], seed=seed, **more)
+    return Paged(fmt, dim, 2, 16, [keys or 100], [3], seed=seed, capacity=5000 if launch == "shared" else 0, **more)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("launch", LAUNCHES)
+@pytest.mark.parametrize("far,window", [
+    (2 ** 31 - 1, 2 ** 30),                            # the window lies behind the table: no key
+    (2 ** 30 + 500, 2 ** 30),                          # some rows' reaches into it
+    (2 ** 31 - 1, 2 ** 31 - 201),
+    (2 ** 31 - 1, 2 ** 31 - 1),                        # all of it
+    (2 ** 31 - 1, 2 ** 31),
+])
+def test_positions_and_windows_up_to_31_bits(fmt, launch, far, window):
+    """lens far behind a short table: rows see the table's keys that their window reaches, or none."""
+    say("far", fmt, launch, far, window)
+    P = paged(launch, fmt, 64, 2, 31, 704)             # pages are full
+    q = rand((P.rows, P.heads * 2 * 64), BF, 1, 0.5)
+    P.batch.lens.fill_(far)
+    P.positions = lambda b: far - P.new[b] + np.arange(P.new[b], dtype=np.int64)
+    out, lse = S.kv_attn(q.cuda(), P.cache, P.batch, window=window, with_lse=True)
+    P.check(q, out, lse, None, window)
+    if (far, window) == (2 ** 31 - 1, 2 ** 30):
+        assert not out.any() and bool((lse == -float("inf")).all())
