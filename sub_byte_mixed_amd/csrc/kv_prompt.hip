@@ -64,7 +64,7 @@ __global__ __launch_bounds__(64 * W, D > 64 ? 2 : W == 4 ? 3 : 4) void kv_prompt
     const bool mine = kRows * i + n < wrows;
     R[i].load(mine ? A.q + (U.row0 + tok) * A.ldq + (int64_t)(head * A.group + r % A.group) * D : nullptr);
     R[i].start(A.scale, ek);
-    R[i].factor = fmaxf(R[i].factor, 1.0e-37f);        // times -inf is -inf
+    R[i].factor = fmaxf(R[i].factor, 1.0e-45f);        // the smallest above 0: times -inf is -inf
     R[i].last = mine ? limit(A, U.pos0 + tok) : -1;
     R[i].first = first_key(A, U.pos0 + tok);
   }

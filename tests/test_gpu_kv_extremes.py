@@ -45,3 +45,18 @@ def test_positions_and_windows_up_to_31_bits(fmt, launch, far, window):
     P.check(q, out, lse, None, window)
     if (far, window) == (2 ** 31 - 1, 2 ** 30):
         assert not out.any() and bool((lse == -float("inf")).all())
+
+
+@pytest.mark.parametrize("launch", LAUNCHES)
+@pytest.mark.parametrize("scale", [1e-36, 1e-38, 1e-40])
+def test_scales_far_below_one(launch, scale):
+    """MXFP4's keys times queries up to 2^127 under a scale that brings them back."""
+    scale = float(np.float32(scale))
+    say("small scale", launch, scale)
+    P = paged(launch, S.MXFP4, 64, 2, 32)
+    t = P.cache.k_scales
+    new = torch.randint(127 + 50, 127 + 58, t.shape, generator=torch.Generator().manual_seed(1), dtype=torch.uint8).cuda()
+    t.copy_(torch.where(t == 0xFF, t, new))
+    q = rand((P.rows, P.heads * 2 * 64), torch.float32, 2).clamp(-4, 4).mul(2.0 ** 60).to(BF)
+    out, lse = S.kv_attn(q.cuda(), P.cache, P.batch, scale=scale, with_lse=True)
+    P.check(q, out, lse, scale)
