@@ -14,10 +14,11 @@
 // lanes, and the cache's order of bytes gives each lane its keys' dimensions and
 // its dimensions' values in one 16-byte load each, 1 KB in a row for the wave.
 //
-// NVFP4: E2M1 times its E4M3 scale is exact in fp16, and bf16 queries are once
-// the row's power of two is taken out (dimensions 2^-14 below the row's largest
-// lose bits of 2^-25 of it). MXFP4: exact in bf16; the softmax's terms, which
-// bf16 would round to 2^-9, enter in two parts.
+// NVFP4: E2M1 times its E4M3 scale is exact in fp16, and bf16 queries are once a
+// power of two puts the row's largest into [2^14, 2^15), as high as fp16 takes it:
+// a dimension is exact down to 2^-31 of the largest and below that off by half of
+// fp16's last step, 2^-25, which is 2^-39 of the largest at most. MXFP4: exact in
+// bf16; the softmax's terms, which bf16 would round to 2^-9, enter in two parts.
 #pragma once
 
 #include "kv_common.h"
@@ -33,6 +34,7 @@ typedef float f4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4, kRows = 16;
 constexpr float kLowest = -3.0e38f;                    // below every score
+constexpr int kTop = 15;                               // NVFP4 queries lie below 2^kTop
 // A row's m may lag behind its maximum by 2^8, which leaves the output as it is
 // for most tiles. NVFP4: it lies 2^7 below the maximum besides, so that terms of
 // 2^-21 of the largest keep fp16's precision and 2^-31 still counts: a long
@@ -238,7 +240,7 @@ struct Rows {
       big = row_max(big);
       int e;
       frexpf(big, &e);
-      e = big < __builtin_inff() ? e : 0;
+      e = big < __builtin_inff() ? e - kTop : 0;
 #pragma unroll
       for (int l_ = 0; l_ < G::KL; ++l_)
 #pragma unroll

@@ -60,3 +60,23 @@ def test_scales_far_below_one(launch, scale):
     q = rand((P.rows, P.heads * 2 * 64), torch.float32, 2).clamp(-4, 4).mul(2.0 ** 60).to(BF)
     out, lse = S.kv_attn(q.cuda(), P.cache, P.batch, scale=scale, with_lse=True)
     P.check(q, out, lse, scale)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("launch", LAUNCHES)
+def test_queries_with_dimensions_far_below_their_largest(fmt, dim, launch):
+    """A query's largest dimension meets keys of zero; the score comes from dimensions of 2^-17 of it, which are held
+    exactly. So the results and tolerances are those of queries without the largest."""
+    say("small dimensions", fmt, dim, launch)
+    P = paged(launch, fmt, dim, 2, 33)
+    P.cache.k_codes[:, :, :, 0, :, 0] &= 0xF0          # dimension 0
+    g = torch.Generator().manual_seed(3)
+    small = torch.zeros((P.rows, P.heads * 2, dim))
+    small[:, :, 1:32] = 2.0 ** -17 * (1.0 + 2.0 ** -7) * (2.0 * torch.randint(0, 2, (P.rows, P.heads * 2, 31), generator=g) - 1.0)
+    q = small.clone()
+    q[:, :, 0] = 1.0
+    q, small = (t.reshape(P.rows, -1).to(BF) for t in (q, small))
+    scale = 2.0 ** (15 if fmt == S.NVFP4 else 14)
+    out, lse = S.kv_attn(q.cuda(), P.cache, P.batch, scale=scale, with_lse=True)
+    P.check(small, out, lse, scale)
