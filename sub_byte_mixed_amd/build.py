@@ -63,14 +63,17 @@ ASAN_OPS_SRC = os.path.join(HELPERS, "abi_asan_ops_check.cpp")
 ASAN_OPS_BIN = os.path.join(HELPERS, "abi_asan_ops_check")
 ASAN_KV_SRC = os.path.join(HELPERS, "abi_asan_kv_check.cpp")
 ASAN_KV_BIN = os.path.join(HELPERS, "abi_asan_kv_check")
+ASAN_ABSENT_SRC = os.path.join(HELPERS, "abi_asan_kv_absent_check.cpp")
+ASAN_ABSENT_BIN = os.path.join(HELPERS, "abi_asan_kv_absent_check")
 
 
 def build_asan_check(verbose: bool = False) -> str:
     """The library's sources with tests/helpers/abi_asan_check.cpp, with
-    abi_asan_ops_check.cpp and with abi_asan_kv_check.cpp, as executables whose
-    host code is built with AddressSanitizer and UndefinedBehaviorSanitizer
-    (device code is not instrumented): the validation and sizing paths of every
-    entry point of snip.h, snip_ops.h and snip_kv.h, checked on the CPU."""
+    abi_asan_ops_check.cpp, with abi_asan_kv_check.cpp and with
+    abi_asan_kv_absent_check.cpp, as executables whose host code is built with
+    AddressSanitizer and UndefinedBehaviorSanitizer (device code is not
+    instrumented): the validation and sizing paths of every entry point of
+    snip.h, snip_ops.h and snip_kv.h, checked on the CPU."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     san = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
            "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-fno-sanitize-recover=undefined"]
@@ -88,10 +91,10 @@ def build_asan_check(verbose: bool = False) -> str:
         return obj
 
     from concurrent.futures import ThreadPoolExecutor
-    srcs = [os.path.join(CSRC, s) for s in SOURCES] + [ASAN_SRC, ASAN_OPS_SRC, ASAN_KV_SRC]
+    srcs = [os.path.join(CSRC, s) for s in SOURCES] + [ASAN_SRC, ASAN_OPS_SRC, ASAN_KV_SRC, ASAN_ABSENT_SRC]
     with ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 1)) as ex:
-        *objs, snip, ops, kv = ex.map(one, srcs)
-    for main, out in ((snip, ASAN_BIN), (ops, ASAN_OPS_BIN), (kv, ASAN_KV_BIN)):
+        *objs, snip, ops, kv, absent = ex.map(one, srcs)
+    for main, out in ((snip, ASAN_BIN), (ops, ASAN_OPS_BIN), (kv, ASAN_KV_BIN), (absent, ASAN_ABSENT_BIN)):
         cmd = [hipcc_path(), "--offload-arch=gfx950", *san, "-o", out + ".tmp", *objs, main]
         if verbose:
             print(" ".join(cmd), flush=True)

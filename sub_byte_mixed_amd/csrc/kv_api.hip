@@ -100,6 +100,7 @@ int snipkv_append(const void* q, int64_t ldq, int64_t q_heads, const void* k, in
   if (!q != !q_out) return fail(SNIP_E_NULL, "%s: q and q_out must be given together", who);
   if (type != SNIPOP_BF16 && type != SNIPOP_F32) return fail(SNIP_E_FORMAT, "%s: unknown element type %d", who, type);
   const int64_t D = cache->head_dim;
+  if (!q) q_heads = 0;                                   // it may be anything then
   if (q && (rc = check_heads(who, q_heads, cache->kv_heads))) return rc;
   if ((rc = check_rows(who, "q", q, type, ldq, q_heads * D))) return rc;
   if ((rc = check_rows(who, "k", k, type, ldk, cache->kv_heads * D))) return rc;
@@ -126,12 +127,12 @@ int snipkv_append(const void* q, int64_t ldq, int64_t q_heads, const void* k, in
   a.ldqo = ldqo;
   a.tokens = tokens;
   a.angles = angles;
-  a.q_heads = q ? (int32_t)q_heads : 0;
+  a.q_heads = (int32_t)q_heads;
   a.rot = (int32_t)rot_dim;
   a.interleaved = interleaved != 0;
   a.type = type;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const double work = (double)tokens * (double)((q ? q_heads : 0) + (k ? 2 * cache->kv_heads : 0)) * (double)D;
+  const double work = (double)tokens * (double)(q_heads + (k ? 2 * cache->kv_heads : 0)) * (double)D;
   const int slot = timing_begin(LaunchTag{SNIPKV_LAUNCH_APPEND, cache->format, -1, -1, work}, s);
   const hipError_t e = launch_kv_append(cache->format, cache->head_dim, a, s);
   timing_end(slot, s);
