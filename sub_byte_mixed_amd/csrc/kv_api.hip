@@ -15,7 +15,7 @@ constexpr int64_t kMaxTiles = ((int64_t)1 << 24) - 1;   // of 256 threads in a g
 constexpr int64_t kMaxSeqs = (int64_t)1 << 20;
 constexpr int64_t kMaxLen = (int64_t)1 << 30;          // of a table, in tokens
 constexpr int64_t kMaxHeads = 1024;
-constexpr int64_t kMaxLd = (int64_t)1 << 40;
+constexpr int64_t kMaxLd = (int64_t)1 << 40;            // times kMaxTokens and an element's bytes: within 63 bits
 
 bool head_dim_ok(int64_t d) { return d == 64 || d == 128 || d == 256; }
 
@@ -68,8 +68,6 @@ int check_rows(const char* who, const char* name, const void* p, int type, int64
   if (ld < cols || ld > kMaxLd || ld % step)
     return fail(SNIP_E_SHAPE, "%s: %s: leading dimension %lld must be >= %lld and a multiple of %d", who, name,
                 (long long)ld, (long long)cols, step);
-  if (ld > ((int64_t)1 << 60) / kMaxTokens)
-    return fail(SNIP_E_SHAPE, "%s: %s: leading dimension %lld is too large", who, name, (long long)ld);
   if (!aligned(p, 16)) return fail(SNIP_E_ALIGN, "%s: %s is not 16-byte aligned", who, name);
   return SNIP_OK;
 }
