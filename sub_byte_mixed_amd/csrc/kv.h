@@ -54,7 +54,8 @@ struct KvAttn {
   int64_t ldq, ldo, tokens;
   int32_t q_heads, group;      // query heads of a kv head
   int32_t window;              // 0: none
-  int32_t few, split;          // split: sequences of more rows than `few` have a launch of their own
+  int32_t split;               // the prompts among the sequences have a launch of their own: those
+  int32_t few, some, far;      // of more rows than `few`, or than `some` with more keys than `far`
   int32_t step;                // keys of a step of work, a multiple of a workgroup's
   int32_t each;                // steps of a sequence where all have as many; 0: they follow from lens and cu
   float scale;                 // times log2 e
@@ -83,7 +84,7 @@ constexpr int kv_prompt_rows(int dim) { return dim == 256 ? 64 : 128; }
 // Tiles of 16 rows of a call, a kv head's, at most; workspace bytes.
 int64_t kv_attn_tiles(int64_t tokens, int64_t seqs, int64_t group);
 size_t kv_attn_slots(int dim);
-// Fills in what of `a` the plan decides (few, split, step, left).
+// Fills in what of `a` the plan decides (split, few, some, far, step, each, left).
 KvPlan kv_attn_plan(int format, int dim, KvAttn* a);
 
 hipError_t launch_kv_append(int format, int dim, const KvAppend& a, hipStream_t s);

@@ -40,7 +40,7 @@ struct Cursor {
 
   __device__ __forceinline__ int cost(const KvAttn& A, int b) const {
     const Span x = span_of(A, b, unit_rows);
-    return A.split && x.rows > A.few ? 0 : x.tiles * x.steps * A.c.heads;
+    return A.split && prompt_rows(A, x) ? 0 : x.tiles * x.steps * A.c.heads;
   }
   // Steps of all sequences.
   __device__ __forceinline__ int total(const KvAttn& A) {
@@ -524,12 +524,16 @@ constexpr int kShort = 1280;
 // Bytes of a cache from which it is read past the last-level cache, where it
 // cannot stay (362 MB: 82 -> 74 us; 75 MB, read again and again: 28 -> 30).
 constexpr int64_t kStream = (int64_t)128 << 20;
-// Mean rows of a sequence from which a call is one of prompts, and rows of a
-// sequence up to which it is left to this file's launch all the same: a token's
-// heads. More of them would follow the prompts instead of running among them (64
-// sequences of 1 to 33 new tokens, up to 2048 keys, 64 heads over 8: 16 rows 120
-// us, 64 127, 128 152; 16 of 2 to 64 after 4096: 132, 139, 142).
-constexpr int kPrompt = 64, kFew = 16;
+// Mean rows of a sequence from which a call is one of prompts; rows of a sequence
+// up to which it is left to this file's launch all the same: a token's heads, and
+// with more than kFar keys kSome. Such rows follow the prompts in a launch of their
+// own, 5 us with few keys; among the prompts, whose units are not split over keys,
+// one unit with many keys outlasts the rest. 64 heads over 8 of 128, us, kSome rows
+// left to this launch and not:
+//     2048 tokens and 4 after   512: 115, 110   1024: 109, 116   2048: 109, 142   4096: 109, 196   65536: 143, 1936
+//     64 sequences of 1 to 33 new tokens, up to 2048 keys: 126, 120; 16 of 2 to 64, up to 4096: 138, 132
+// With kFar both of the latter are at 120 and 132.
+constexpr int kPrompt = 64, kFew = 16, kSome = 64, kFar = 1024;
 
 }  // namespace
 
@@ -562,6 +566,8 @@ KvPlan kv_attn_plan(int format, int dim, KvAttn* a) {
   p.prompt_wg = p.prompt ? (unsigned)units(unit) : 0;
   a->split = p.prompt && b.seqs > 1;
   a->few = a->split ? kFew : 0;
+  a->some = a->split ? kSome : 0;
+  a->far = kFar;
   p.few = !p.prompt || a->split;
   const bool whole = b.max_len <= kShort && !p.prompt;
   p.join = p.few && !whole;

@@ -53,7 +53,7 @@ __global__ __launch_bounds__(64 * W, D > 64 ? 2 : W == 4 ? 3 : 4) void kv_prompt
   const Span U = span_of(A, seq, kUnit);
   const int64_t base = A.b.cu ? (int64_t)entries(A.b.cu)[seq] * A.group / kUnit + seq : (int64_t)seq * U.tiles;
   const int64_t tile = U.tiles - 1 - (place - base);
-  if (tile < 0 || tile >= U.tiles || U.rows <= A.few) return;
+  if (tile < 0 || tile >= U.tiles || !prompt_rows(A, U)) return;
   const int ek = G::NV ? entries(A.c.texp)[0] : 0, ev = G::NV ? entries(A.c.texp)[1] : 0;
   const int r0 = (int)tile * kUnit, w0 = r0 + wave * kRows * NR;
   const int rows = U.rows - r0 < kUnit ? U.rows - r0 : kUnit, wrows = U.rows - w0;

@@ -261,6 +261,7 @@ struct Span {                  // of one sequence
   int64_t row0, pos0;          // first row in the call's matrices, its position
   int rows;                    // (token, query head) pairs of a kv head
   int tiles, steps;            // units a head, steps a unit
+  int keys;                    // from the first that its first row sees to the last row's
 };
 
 __device__ __forceinline__ int limit(const KvAttn& A, int64_t p) {
@@ -288,9 +289,14 @@ __device__ __forceinline__ Span span_of(const KvAttn& A, int b, int unit_rows) {
   if (a < 0 || e <= a) return x;
   x.rows = (int)(e - a) * A.group;
   x.tiles = (x.rows + unit_rows - 1) / unit_rows;
-  const int n = limit(A, len - 1) + 1 - (first_key(A, x.pos0) & ~31);
-  x.steps = n > A.step ? (n + A.step - 1) / A.step : 1;   // a unit without keys writes its zeros
+  x.keys = limit(A, len - 1) + 1 - (first_key(A, x.pos0) & ~31);
+  x.steps = x.keys > A.step ? (x.keys + A.step - 1) / A.step : 1;   // a unit without keys writes its zeros
   return x;
+}
+
+// Whether the launch for prompts has a sequence, where there are both.
+__device__ __forceinline__ bool prompt_rows(const KvAttn& A, const Span& x) {
+  return x.rows > (x.keys > A.far ? A.some : A.few);
 }
 
 __device__ __forceinline__ void store_lse(const KvAttn& A, int64_t t, int qh, float M, float L) {
