@@ -80,3 +80,69 @@ def test_queries_with_dimensions_far_below_their_largest(fmt, dim, launch):
     scale = 2.0 ** (15 if fmt == S.NVFP4 else 14)
     out, lse = S.kv_attn(q.cuda(), P.cache, P.batch, scale=scale, with_lse=True)
     P.check(small, out, lse, scale)
+
+
+def check(P, q, scale=None, window=0):
+    out, lse = S.kv_attn(q.cuda(), P.cache, P.batch, scale=scale, window=window, with_lse=True)
+    P.check(q, out, lse, scale, window)
+    again, _ = S.kv_attn(q.cuda(), P.cache, P.batch, scale=scale, window=window)
+    assert torch.equal(again, out)
+    return out, lse
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("launch", ["eight", "four"])
+@pytest.mark.parametrize("qscale,scale", [(0.0, None), (40.0, None), (1e-30, 1e29), (1e30, 1e-30), (0.5, 3.0)])
+def test_sizes_of_scores(fmt, launch, qscale, scale):
+    """Queries of zero; peaked softmaxes; queries far from 1 under a scale that brings them back."""
+    say("prompt sizes", fmt, launch, qscale, scale)
+    P = paged(launch, fmt, 64, 2, 7)
+    check(P, rand((P.rows, P.heads * 2 * 64), BF, 1, qscale), scale)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("launch", ["eight", "four"])
+def test_rising_scores(fmt, dim, launch):
+    """Keys whose scores grow along the sequence: the running maximum moves from tile to tile."""
+    say("prompt rising", fmt, dim, launch)
+    P = paged(launch, fmt, dim, 2, 8)
+    base, step = (0x20, 8) if fmt == S.NVFP4 else (118, 1)
+    t = P.cache.k_scales.transpose(3, 4)
+    for j in range(0, P.lens[0], 16):
+        up = torch.arange(j, j + min(16, P.lens[0] - j)) // 90
+        t[int(P.table[0, j // 16]), :, 0, :len(up)] = (base + step * up[:, None, None]).to(torch.uint8).cuda()
+    check(P, rand((P.rows, P.heads * 2 * dim), BF, 1, 0.5))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("launch", ["eight", "four"])
+def test_queries_that_are_not_finite(fmt, launch):
+    """They reach their own rows alone."""
+    say("prompt, not finite", fmt, launch)
+    P = paged(launch, fmt, 128, 2, 9)
+    q = rand((P.rows, P.heads * 2 * 128), BF, 5, 0.5)
+    odd = q.clone()
+    bad = [(3, 0, 7), (3, 2, 100), (300, 1, 0), (599, 3, 127), (64, 0, 64), (65, 0, 1)]      # token, head, dimension
+    for i, (t, h, d) in enumerate(bad):
+        odd[t, h * 128 + d] = (float("nan"), float("inf"), -float("inf"))[i % 3]
+    out, lse = S.kv_attn(odd.cuda(), P.cache, P.batch, with_lse=True)
+    want, want_lse = S.kv_attn(q.cuda(), P.cache, P.batch, with_lse=True)
+    for t, h, d in bad:
+        assert bool(out[t, h * 128:(h + 1) * 128].isnan().all())
+        out[t, h * 128:(h + 1) * 128] = want[t, h * 128:(h + 1) * 128]
+        lse[t, h] = want_lse[t, h]
+    P.check(q, out, lse)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("units", [256, 1024])
+@pytest.mark.parametrize("window", [0, 33])
+def test_prompts_drafts_and_tokens(fmt, dim, units, window):
+    """Prompts, chunks after others, drafted and single tokens, none, a page that is not mapped: both launches."""
+    lens, new = [333, 40, 170, 250, 9, 1, 90, 700], [333, 40, 131, 4, 0, 1, 65, 33]
+    heads = -(-units // (sum(new) * 4 // UNIT[dim]))
+    say("mixed", fmt, dim, units, window)
+    P = Paged(fmt, dim, heads, 32, lens, new, seed=dim + window, unmapped=[(0, 1), (7, 20)])
+    check(P, rand((P.rows, heads * 4 * dim), BF, 1, 0.5), None, window)
