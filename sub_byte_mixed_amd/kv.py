@@ -81,11 +81,28 @@ def _buffer(t: torch.Tensor, name: str, shape: tuple, dev: int) -> int:
                      f"{tuple(t.shape)} on {t.device}")
 
 
+def _kept(name: str) -> property:
+    """A tensor whose address the library was given: it is written into in place
+    (`t += 1` ends by assigning the same tensor), not replaced."""
+    at = "_" + name
+
+    def get(self):
+        return getattr(self, at)
+
+    def put(self, value):
+        if value is not getattr(self, at):
+            raise AttributeError(f"{name} of a {type(self).__name__} is not replaced: write into it in place, or make another "
+                                 f"{type(self).__name__}")
+    return property(get, put)
+
+
 class KVCache:
     """Caller-owned buffers of a paged cache, uint8 in the shapes of
     cache_shapes(); texp (NVFP4): int32 [2], the powers of two that keys and
     values are stored under (x = code * scale * 2^texp), chosen once by the
-    caller: the smallest e with max|x| <= 2688 * 2^e."""
+    caller: the smallest e with max|x| <= 2688 * 2^e. The
+    buffers are not replaced by others."""
+    k_codes, k_scales, v_codes, v_scales, texp = map(_kept, ("k_codes", "k_scales", "v_codes", "v_scales", "texp"))
 
     def __init__(self, fmt: int, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
                  v_scales: torch.Tensor, texp: Optional[torch.Tensor] = None):
@@ -99,7 +116,7 @@ class KVCache:
         if texp is None and fmt == _S.NVFP4:
             raise ValueError("an NVFP4 cache needs texp")
         self.format, self.pages, self.kv_heads, self.page_size, self.head_dim, self.device = fmt, pages, heads, page, dim, dev
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.texp = k_codes, k_scales, v_codes, v_scales, texp
+        self._k_codes, self._k_scales, self._v_codes, self._v_scales, self._texp = k_codes, k_scales, v_codes, v_scales, texp
         self._desc = CacheDesc(fmt, page, heads, dim, pages, *at, _vec(texp, "texp", 2, (_I32,), dev))
         self.ref = ctypes.byref(self._desc)
 
@@ -117,7 +134,9 @@ class KVBatch:
     int32 [seqs + 1] (rows cu[b] .. cu[b + 1] are sequence b's new tokens, its
     last; None: one each). A table entry outside 0 .. pages - 1 is a page that
     is not mapped. The kernels read all three when they run: a captured call
-    follows what its buffers hold."""
+    follows what its buffers hold. They are written into in place, not
+    replaced."""
+    table, lens, cu = map(_kept, ("table", "lens", "cu"))
 
     def __init__(self, table: torch.Tensor, lens: torch.Tensor, cu: Optional[torch.Tensor] = None):
         dev = table.get_device()
@@ -126,7 +145,7 @@ class KVBatch:
         (n, wide), (ld, unit) = table.shape, table.stride()
         if unit != 1 and wide > 1:
             raise ValueError("table must have unit column stride")
-        self.table, self.lens, self.cu, self.seqs, self.device = table, lens, cu, n, dev
+        self._table, self._lens, self._cu, self.seqs, self.device = table, lens, cu, n, dev
         self._desc = BatchDesc(table.data_ptr(), ld if n > 1 else wide, wide, _vec(lens, "lens", n, (_I32,), dev),
                                _vec(cu, "cu", n + 1, (_I32,), dev), n)
         self.ref = ctypes.byref(self._desc)
