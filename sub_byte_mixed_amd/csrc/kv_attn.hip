@@ -406,7 +406,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
         const int rr = P.r0 + ur;
         const int64_t t = P.row0 + rr / A.group;
         const int qh = P.head * A.group + rr % A.group;
-        const float inv = !P.all ? 1.0f : L == 0.0f ? 0.0f : ldexpf(1.0f / L, ev);
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
         for (int d = 0; d < D / LR; d += E) {
           float x[E];
@@ -415,7 +415,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
             x[e] = 0.0f;
 #pragma unroll
             for (int k = 0; k < kWaves; ++k) x[e] += reinterpret_cast<const float*>(part[k])[row * LD + d0 + d + e] * w[k];
-            x[e] *= inv;
+            if (P.all) x[e] = output<FMT>(x[e], inv, ev);
           }
           if (P.all)
             store_few(A.out, false, t * A.ldo + (int64_t)qh * D + d0 + d, x);
@@ -442,8 +442,8 @@ __global__ __launch_bounds__(64 * kWaves, waves_of(D, NR)) void kv_attn_kernel(K
 // A unit that several workgroups had a share of, joined: blockIdx.x is the one
 // that has its first step, blockIdx.y the row. The parts are taken by several
 // groups of lanes and added in a fixed order.
-template <int D, int NR>
-__global__ __launch_bounds__(256) void kv_join_kernel(KvAttn A, bool nv) {
+template <int FMT, int D, int NR>
+__global__ __launch_bounds__(256) void kv_join_kernel(KvAttn A) {
   constexpr int LR = D / 4, SUBS = 256 / LR;           // lanes of a row, parts taken at once
   constexpr int kUnit = kRows * NR;
   __shared__ float sm[SUBS], sl[SUBS];
@@ -511,8 +511,9 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn A, bool nv) {
   const int rr = U.r0 + row;
   const int64_t t = U.row0 + rr / A.group;
   const int qh = U.head * A.group + rr % A.group;
-  const float inv = L == 0.0f ? 0.0f : ldexpf(1.0f / L, nv ? A.c.texp[1] : 0);
-  const float y[4] = {x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv};
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  const int ev = FMT == SNIP_NVFP4 ? A.c.texp[1] : 0;
+  const float y[4] = {output<FMT>(x[0], inv, ev), output<FMT>(x[1], inv, ev), output<FMT>(x[2], inv, ev), output<FMT>(x[3], inv, ev)};
   store_whole(A.out, false, t * A.ldo + (int64_t)qh * D + d, y);
   if (A.lse && d == 0) store_lse(A, t, qh, M, L);
 }
@@ -613,12 +614,12 @@ hipError_t launch_kv_few(int format, int dim, const KvPlan& p, const KvAttn& a, 
 
 hipError_t launch_kv_join(int format, int dim, const KvPlan& p, const KvAttn& a, hipStream_t s) {
   return kv_dispatch(format, dim, [&](auto f, auto d) {
-    constexpr int D = decltype(d)::value;
+    constexpr int FMT = decltype(f)::value, D = decltype(d)::value;
     const dim3 grid(p.few_wg - 1, p.join_rows);
     if (p.two)
-      kv_join_kernel<D, most_tiles(D)><<<grid, 256, 0, s>>>(a, decltype(f)::value == SNIP_NVFP4);
+      kv_join_kernel<FMT, D, most_tiles(D)><<<grid, 256, 0, s>>>(a);
     else
-      kv_join_kernel<D, 1><<<grid, 256, 0, s>>>(a, decltype(f)::value == SNIP_NVFP4);
+      kv_join_kernel<FMT, D, 1><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
   });
 }

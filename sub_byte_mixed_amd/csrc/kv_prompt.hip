@@ -263,7 +263,7 @@ __global__ __launch_bounds__(64 * W, D > 64 ? 2 : W == 4 ? 3 : 4) void kv_prompt
   }
 #pragma unroll
   for (int i = 0; i < NR; ++i) {
-    const float L = row_sum(R[i].l), inv = L == 0.0f ? 0.0f : ldexpf(1.0f / L, ev);
+    const float L = row_sum(R[i].l), inv = L == 0.0f ? 0.0f : 1.0f / L;
     if (kRows * i + n >= wrows) continue;
     const int r = w0 + kRows * i + n;
     const int64_t t = U.row0 + r / A.group;
@@ -274,7 +274,7 @@ __global__ __launch_bounds__(64 * W, D > 64 ? 2 : W == 4 ? 3 : 4) void kv_prompt
       for (int j = 0; j < 4; ++j) {
         float x[2 * G::VB];
 #pragma unroll
-        for (int d = 0; d < 2 * G::VB; ++d) x[d] = R[i].o[l * 2 * G::VB + d][j] * inv;
+        for (int d = 0; d < 2 * G::VB; ++d) x[d] = output<FMT>(R[i].o[l * 2 * G::VB + d][j], inv, ev);
         store_whole(A.out, false, t * A.ldo + (int64_t)qh * D + l * 32 * G::VB + (4 * c + j) * 2 * G::VB, x);
       }
     if (A.lse && c == 0) store_lse(A, t, qh, R[i].m, L);

@@ -299,6 +299,13 @@ __device__ __forceinline__ bool prompt_rows(const KvAttn& A, const Span& x) {
   return x.rows > (x.keys > A.far ? A.some : A.few);
 }
 
+// An output: the values' power of two after the quotient, since 2^ev / L may lie
+// below fp32's normal range where the output does not.
+template <int FMT>
+__device__ __forceinline__ float output(float o, float inv, int ev) {
+  return FMT == SNIP_NVFP4 ? ldexpf(o * inv, ev) : o * inv;
+}
+
 __device__ __forceinline__ void store_lse(const KvAttn& A, int64_t t, int qh, float M, float L) {
   A.lse[t * A.q_heads + qh] = L == 0.0f ? -__builtin_inff() : (M + __builtin_amdgcn_logf(L)) * 0.693147180559945309f;
 }

@@ -146,3 +146,19 @@ def test_prompts_drafts_and_tokens(fmt, dim, units, window):
     say("mixed", fmt, dim, units, window)
     P = Paged(fmt, dim, heads, 32, lens, new, seed=dim + window, unmapped=[(0, 1), (7, 20)])
     check(P, rand((P.rows, heads * 4 * dim), BF, 1, 0.5), None, window)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("launch", LAUNCHES)
+@pytest.mark.parametrize("texp", [-112, -120, -126])
+def test_values_far_below_one(dim, launch, texp):
+    """A power of two of NVFP4's values is one of the output: bit for bit, down to the smallest normal numbers."""
+    say("small values", dim, launch, texp)
+    P = paged(launch, S.NVFP4, dim, 2, 34)
+    q = rand((P.rows, P.heads * 2 * dim), BF, 4, 0.5).cuda()
+    P.cache.texp[1] = 0
+    want = S.kv_attn(q, P.cache, P.batch)[0].float()
+    P.cache.texp[1] = texp
+    got = S.kv_attn(q, P.cache, P.batch)[0].float()
+    normal = want.abs() >= 2.0 ** (-126 - texp)
+    assert normal.float().mean() > 0.05 and torch.equal(got[normal], torch.ldexp(want, torch.tensor(float(texp), device="cuda"))[normal])
