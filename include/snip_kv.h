@@ -80,7 +80,8 @@ typedef struct snipkv_batch {
  * (2i, 2i + 1) where interleaved; then keys and values are quantized to nearest
  * as snip_quantize would a tensor with rows of head_dim, under the cache's texp.
  * A block's maximum is that of its finite elements; an infinity is stored as the
- * block's largest code, NaN as zero.
+ * block's largest code, or as zero where the maximum is zero (NVFP4: or too small
+ * for a scale above zero), NaN as zero.
  *   q         device [tokens][q_heads * head_dim], type `type`, ldq; NULL: none.
  *   k, v      device [tokens][kv_heads * head_dim], `type`, ldk, ldv. NULL (both):
  *             queries alone.
@@ -111,10 +112,11 @@ int snipkv_gather(const snipkv_cache* cache, const snipkv_batch* batch, int64_t 
  * for every row and query head; head h reads kv head h / (q_heads / kv_heads).
  * A row with no key at all: out = 0, lse = -infinity. fp32 throughout, but the
  * softmax's terms, which enter the matrix product in fp16 (MXFP4: in two parts
- * of bf16); out is rounded once. Not defined for scores past 2e38, values past
- * 1e30, and scales of NaN (which append never stores) in places that a row of the
- * call sees: other rows of the call may become NaN. The same inputs give the same
- * bits.
+ * of bf16); out is rounded once. Not defined for scores past 2e38 (NVFP4: nor for
+ * rows where scale * 2^texp[0] * max|q| is, whatever the keys; MXFP4: nor for a
+ * q . k_j that is, whatever the scale), values past 1e30, and scales of NaN (which
+ * append never stores) in places that a row of the call sees: other rows of the
+ * call may become NaN. The same inputs give the same bits.
  *   q         device bf16 [tokens][q_heads * head_dim], ldq.
  *   scale     > 0, up to 2e38.
  *   window    0: none; else >= 1.
